@@ -1,5 +1,6 @@
 /*
- * ts_attn.h - decode-step attention over a paged KV cache, for GB300 (sm_103a).
+ * ts_attn.h - attention over a paged KV cache, for GB300 (sm_103a): decode
+ * steps, and prompts in chunks.
  *
  * A C ABI: plain pointers and sizes, no framework types. Every function that
  * takes a `stream` (a cudaStream_t passed as void*, NULL = legacy default
@@ -230,6 +231,166 @@ TS_API ts_status ts_paged_decode_window_attn(const void* q, const void* k_pool, 
                                              int32_t D, int32_t page_size, int32_t num_pages, int32_t window,
                                              float scale, ts_dtype dtype, void* out, float* lse,
                                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ts_paged_decode_sink_attn - decode attention over a sliding window with a
+ * few first tokens that stay visible ("sinks").
+ *
+ * ts_paged_decode_window_attn's operation with `sinks` further tokens: the
+ * query of a sequence with L = seq_lens[b] tokens attends positions t < L
+ * with t >= L - window or t < sinks. The block table keeps real blocks for the
+ * first ceil(sinks / page_size) slots and for the window's; the slots wholly
+ * between the two, and the rows between them of the pages at their edges, are
+ * never read (they may hold placeholders). sinks == 0 gives
+ * ts_paged_decode_window_attn's result, window + sinks >= L
+ * ts_paged_decode_attn's.
+ *
+ *   window    tokens, >= 1;  sinks    tokens, >= 0 (else TS_ERR_INVALID_ARG)
+ *   workspace >= ts_paged_decode_workspace_size(B, H_q, D)
+ *   all other arguments, support (dtype f32 / bf16) and errors as in
+ *   ts_paged_decode_attn.
+ */
+TS_API ts_status ts_paged_decode_sink_attn(const void* q, const void* k_pool, const void* v_pool,
+                                           const int32_t* block_table, int32_t bt_stride,
+                                           const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv,
+                                           int32_t D, int32_t page_size, int32_t num_pages, int32_t window,
+                                           int32_t sinks, float scale, ts_dtype dtype, void* out, float* lse,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Prompt chunks. A batch of B sequences brings a chunk of new tokens each, of
+ * any lengths, as rows of one array: sequence b's are rows q_indptr[b] ..
+ * q_indptr[b + 1] - 1 of T. seq_lens[b] counts its tokens in the cache with
+ * the new ones, so that row q_indptr[b] + j of n = q_indptr[b + 1] -
+ * q_indptr[b] sits at position seq_lens[b] - n + j. The same q_indptr and
+ * seq_lens serve ts_kv_append_chunk (or ts_kv_append_chunk_fp8) and then
+ * ts_paged_prefill_attn. q_indptr is device int32 [B + 1], not decreasing,
+ * within [0, T]; rows outside [q_indptr[0], q_indptr[B]) (padding of a captured
+ * graph) are neither read nor written. Entries out of order never cause an
+ * access out of range; which rows are then taken is not defined. n == 0 is a
+ * sequence without new tokens. Two sequences of one call that write the same
+ * page row leave either's values there.
+ */
+
+/*
+ * ts_kv_append_chunk - write the K and V rows of prompt chunks into the pools.
+ *
+ * SwiftLLM page, section 3.1 (ts_kv_append for any number of new tokens per
+ * sequence): the row at position pos goes to page block_table[b][pos /
+ * page_size], row pos % page_size. The block table must already hold it.
+ *
+ *   k_new, v_new  device [T, H_kv, D] of dtype, rows new_stride elements
+ *                 apart (>= H_kv * D; a part of a fused projection's output)
+ *   k_pool,v_pool device [num_pages, page_size, H_kv, D] of dtype (written)
+ *   seq_lens      device int32 [B], q_indptr device int32 [B + 1]: see above
+ * The copy is bit-exact. Rows whose position is negative or whose block-table
+ * slot or page id is out of range are skipped. T == 0 or B == 0 returns TS_OK
+ * with nothing enqueued. H_kv * D and new_stride are multiples of 16 bytes
+ * (else TS_ERR_UNSUPPORTED), the pointers 16-byte aligned.
+ */
+TS_API ts_status ts_kv_append_chunk(const void* k_new, const void* v_new, void* k_pool, void* v_pool,
+                                    const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                    const int32_t* q_indptr, int64_t new_stride, int32_t T, int32_t B,
+                                    int32_t H_kv, int32_t D, int32_t page_size, int32_t num_pages,
+                                    ts_dtype dtype, void* stream);
+
+/*
+ * ts_kv_append_chunk_fp8 - quantize the K and V rows of prompt chunks into an
+ * fp8 (e4m3fn) cache.
+ *
+ * Placement as ts_kv_append_chunk; codes and scales as ts_kv_append_fp8, bit
+ * for bit (one float32 scale per token and kv head).
+ *
+ *   k_new, v_new    device [T, H_kv, D] of dtype (bf16 or f32), rows
+ *                   new_stride elements apart
+ *   k_pool, v_pool  device uint8 [num_pages, page_size, H_kv, D] e4m3fn codes (written)
+ *   k_scale,v_scale device float32 [num_pages, page_size, H_kv] (written)
+ *   other arguments as ts_kv_append_chunk. D in {64, 128}.
+ */
+TS_API ts_status ts_kv_append_chunk_fp8(const void* k_new, const void* v_new, void* k_pool, void* v_pool,
+                                        float* k_scale, float* v_scale, const int32_t* block_table,
+                                        int32_t bt_stride, const int32_t* seq_lens, const int32_t* q_indptr,
+                                        int64_t new_stride, int32_t T, int32_t B, int32_t H_kv, int32_t D,
+                                        int32_t page_size, int32_t num_pages, ts_dtype dtype, void* stream);
+
+/*
+ * ts_kv_read_fp8 - read an fp8 (e4m3fn) cache back into rows.
+ *
+ * Row kv_indptr[b] + t of the result is token t of sequence b, for t <
+ * seq_lens[b]: code * scale of its token group (tokenspeed 딥다이브,
+ * fiv.co.kr, section 6-4), the product in float32, rounded once more to the
+ * result's type. Rows of kv_indptr's ranges past a sequence's end, rows outside
+ * all ranges, and rows of a token whose block-table slot or page id is out of
+ * range are left as they were. Where every kv_indptr[b] is a multiple of
+ * page_size, k_out and v_out can be taken as pools [rows / page_size,
+ * page_size, H_kv, D] with consecutive pages, for ts_paged_prefill_attn for
+ * example.
+ *
+ *   k_pool, v_pool  device uint8 [num_pages, page_size, H_kv, D] e4m3fn codes
+ *   k_scale,v_scale device float32 [num_pages, page_size, H_kv]
+ *   seq_lens        device int32 [B] tokens to read (from the first on)
+ *   kv_indptr       device int32 [B + 1], not decreasing, within [0, rows]
+ *   k_out, v_out    device [rows, H_kv, D] of dtype (bf16 or f32) (written)
+ * Supported: D in {64, 128}. rows == 0 or B == 0 returns TS_OK with nothing
+ * enqueued. Pools and results are 16-byte aligned.
+ */
+TS_API ts_status ts_kv_read_fp8(const void* k_pool, const void* v_pool, const float* k_scale,
+                                const float* v_scale, const int32_t* block_table, int32_t bt_stride,
+                                const int32_t* seq_lens, const int32_t* kv_indptr, int32_t rows, int32_t B,
+                                int32_t H_kv, int32_t D, int32_t page_size, int32_t num_pages, ts_dtype dtype,
+                                void* k_out, void* v_out, void* stream);
+
+/*
+ * ts_paged_prefill_workspace_size - workspace bytes for ts_paged_prefill_attn
+ * with T rows. Depends on the device's SM count. Returns 0 on invalid or
+ * unsupported arguments.
+ */
+TS_API size_t ts_paged_prefill_workspace_size(int32_t T, int32_t B, int32_t H_q, int32_t H_kv, int32_t D);
+
+/*
+ * ts_paged_prefill_attn - attention of prompt chunks over a paged cache that
+ * already holds their K/V rows.
+ *
+ * SwiftLLM page, section 5.1 (the query, block tables and context lengths),
+ * for a chunk of new tokens per sequence. The token at position p attends t <=
+ * p; with window > 0 only those with t > p - window or t < sinks (TokenSpeed
+ * deep dive, section 4.1: sliding-window KV groups, with first tokens that stay
+ * visible as in ts_paged_decode_sink_attn). For every query head, as in
+ * ts_paged_decode_attn: O = softmax(scale q K^T) V, LSE = log sum exp. A token
+ * that sees no key (its position is negative) gets O = 0, LSE = -inf.
+ *
+ * bf16 runs on tcgen05 with float32 accumulation and softmax statistics; the
+ * softmax weights are rounded to bf16 for the product with V, and O is divided
+ * by the sum of the rounded weights. float32 runs on the CUDA cores. Long
+ * key ranges are cut over the SMs and joined by LSE; the cut depends only on
+ * lengths and the device, so equal calls give equal bits.
+ *
+ *   q             device [T, H_q, D] of dtype, rows q_stride elements apart
+ *                 (>= H_q * D; a part of a fused projection's output)
+ *   out           device [T, H_q, D] of dtype (written; rows of no sequence
+ *                 are left as they were)
+ *   lse           device float32 [T, H_q] (written) or NULL
+ *   seq_lens      device int32 [B], q_indptr device int32 [B + 1]: see above.
+ *                 Both are read before the wait for the previous kernel
+ *                 (programmatic dependent launch, as above).
+ *   window        tokens, 0: no window;  sinks  tokens, >= 0
+ *   workspace     >= ts_paged_prefill_workspace_size(T, B, H_q, H_kv, D)
+ *                 bytes, 256-byte aligned, the error word in front
+ *   other arguments and errors as in ts_paged_decode_attn.
+ * Pages that no row of a call sees are never read, nor are rows of a seen
+ * page that lie past the sequence's end or outside every row's window. The
+ * tokens of a page whose id is out of range, or past the block table's row,
+ * count as absent and set TS_DEVERR_PAGE_RANGE. A V row that some rows of a
+ * 128-key tile see and others do not must be finite (the others weigh it by 0).
+ * Supported: D in {64, 128}, H_q / H_kv up to 64, page_size in {8, 16, 32},
+ * T up to 2^30, q_stride a multiple of 16 bytes.
+ */
+TS_API ts_status ts_paged_prefill_attn(const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
+                                       const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                       const int32_t* q_indptr, int32_t T, int32_t B, int32_t H_q, int32_t H_kv,
+                                       int32_t D, int32_t page_size, int32_t num_pages, int32_t window,
+                                       int32_t sinks, float scale, ts_dtype dtype, void* out, float* lse,
+                                       void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * ts_paged_decode_multi_workspace_size - workspace bytes for

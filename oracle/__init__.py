@@ -52,6 +52,13 @@ from .fp8 import (
     decode_attention_fp8,
     mla_decode_attention_fp8,
 )
+from .chunks import (
+    decode_attention_sinks,
+    prefill_attention,
+    kv_append_chunk,
+    kv_append_chunk_fp8,
+    kv_read_fp8,
+)
 
 __all__ = [
     "gather_sequence",
@@ -75,5 +82,10 @@ __all__ = [
     "kv_append_fp8",
     "decode_attention_fp8",
     "mla_decode_attention_fp8",
+    "decode_attention_sinks",
+    "prefill_attention",
+    "kv_append_chunk",
+    "kv_append_chunk_fp8",
+    "kv_read_fp8",
     "PrefixGroups",
 ]

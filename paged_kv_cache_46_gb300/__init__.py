@@ -91,6 +91,17 @@ _SIGNATURES = {
                                                     _I32, _I32, _F32, ctypes.c_int, _VP, _VP, _VP]),
     "ts_paged_decode_window_attn": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I32, _VP, _I32, _I32, _I32, _I32, _I32,
                                                    _I32, _I32, _F32, ctypes.c_int, _VP, _VP, _VP, _SZ, _VP]),
+    "ts_paged_decode_sink_attn": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I32, _VP, _I32, _I32, _I32, _I32, _I32,
+                                                 _I32, _I32, _I32, _F32, ctypes.c_int, _VP, _VP, _VP, _SZ, _VP]),
+    "ts_kv_append_chunk": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _I64, _I32, _I32, _I32, _I32,
+                                          _I32, _I32, ctypes.c_int, _VP]),
+    "ts_kv_append_chunk_fp8": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _I64, _I32, _I32,
+                                              _I32, _I32, _I32, _I32, ctypes.c_int, _VP]),
+    "ts_kv_read_fp8": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _I32,
+                                      ctypes.c_int, _VP, _VP, _VP]),
+    "ts_paged_prefill_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
+    "ts_paged_prefill_attn": (ctypes.c_int, [_VP, _I64, _VP, _VP, _VP, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I32,
+                                             _I32, _I32, _I32, _I32, _F32, ctypes.c_int, _VP, _VP, _VP, _SZ, _VP]),
     "ts_paged_decode_multi_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
     "ts_paged_decode_multi_attn": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I32, _VP, _I32, _I32, _I32, _I32, _I32,
                                                   _I32, _I32, _F32, ctypes.c_int, _VP, _VP, _VP, _SZ, _VP]),
@@ -179,6 +190,15 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
+def _rows(t: torch.Tensor):
+    """Pointer and row step (elements) of a [rows, heads, D] tensor whose rows are contiguous."""
+    rows, heads, D = t.shape
+    step, head_step, unit = t.stride()
+    if (D > 1 and unit != 1) or (heads > 1 and head_step != D):
+        raise ValueError("the heads of a row must be contiguous")
+    return t.data_ptr(), step if rows > 1 else heads * D
+
+
 def _require_i32(*ts):
     for t in ts:
         if t.dtype != torch.int32:
@@ -246,6 +266,152 @@ def ts_paged_decode_window_attn(q, k_pool, v_pool, block_table, seq_lens, scale:
                                              int(window), float(scale), _dt(q), _ptr(out), _ptr(lse),
                                              _ptr(workspace), workspace.numel() * workspace.element_size(),
                                              _stream(stream)))
+    return (out, lse) if return_lse else out
+
+
+def ts_paged_decode_sink_attn(q, k_pool, v_pool, block_table, seq_lens, scale: float, window: int, sinks: int,
+                              out=None, lse=None, workspace=None, stream=None, return_lse: bool = False):
+    """Decode attention over a sliding window whose sequence's first ``sinks`` tokens stay
+    visible; returns ``out`` (and ``lse``)."""
+    _require_i32(block_table, seq_lens)
+    B, H_q, D = q.shape
+    P, ps, H_kv, _ = k_pool.shape
+    _require_cache(q, k_pool, v_pool)
+    if out is None:
+        out = torch.empty(B, H_q, D, dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty(B, H_q, dtype=torch.float32, device=q.device)
+    _require_result(out, lse, q)
+    _require_current_device(q, k_pool, v_pool, block_table, seq_lens, out, lse, workspace)
+    if workspace is None:
+        workspace = new_workspace(ts_paged_decode_workspace_size(B, H_q, D), q.device)
+    _check(lib().ts_paged_decode_sink_attn(_ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
+                                           block_table.shape[1], _ptr(seq_lens), B, H_q, H_kv, D, ps, P,
+                                           int(window), int(sinks), float(scale), _dt(q), _ptr(out), _ptr(lse),
+                                           _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                           _stream(stream)))
+    return (out, lse) if return_lse else out
+
+
+def _require_current_device(*tensors):
+    """The library launches on the current device: every tensor must live there."""
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != torch.cuda.current_device()):
+            raise ValueError(f"tensors must be on the current CUDA device (got {t.device})")
+
+
+def _require_cache(q, k_pool, v_pool):
+    """Queries and pools of one type; pools [num_pages, page_size, H_kv, D] alike."""
+    if k_pool.dtype != q.dtype or v_pool.dtype != q.dtype:
+        raise TypeError("queries and pools must have one dtype")
+    if k_pool.shape != v_pool.shape or k_pool.shape[3] != q.shape[2]:
+        raise ValueError("pools must be [num_pages, page_size, H_kv, D] with the queries' D")
+
+
+def _require_result(out, lse, q):
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have the queries' shape and dtype")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2]):
+        raise ValueError("lse must be float32 of the queries' rows and heads")
+
+
+def _require_chunks(seq_lens, indptr, block_table):
+    """Ragged batches: indptr has one entry more than there are sequences."""
+    _require_i32(seq_lens, indptr, block_table)
+    B = seq_lens.shape[0]
+    if indptr.shape != (B + 1,) or block_table.shape[0] != B:
+        raise ValueError("a batch of B sequences has B lengths, B block-table rows and B + 1 row offsets")
+    return B
+
+
+def _chunk_rows(k_new, v_new, k_pool, v_pool):
+    """Pointers and common row step of new K and V rows [T, H_kv, D] for pools [P, ps, H_kv, D]."""
+    if k_new.shape != v_new.shape or k_new.dtype != v_new.dtype:
+        raise ValueError("k_new and v_new must be alike")
+    if k_pool.shape != v_pool.shape or k_pool.shape[2:] != k_new.shape[1:]:
+        raise ValueError("pools must be [num_pages, page_size, H_kv, D] with the new rows' H_kv and D")
+    (k, step), (v, v_step) = _rows(k_new), _rows(v_new)
+    if step != v_step:
+        raise ValueError("k_new and v_new rows must be equally far apart")
+    return k, v, step
+
+
+def ts_kv_append_chunk(k_new, v_new, k_pool, v_pool, block_table, seq_lens, q_indptr, stream=None) -> None:
+    """Write the K/V rows [T, H_kv, D] of a ragged batch of prompt chunks into the pools:
+    rows ``q_indptr[b]`` .. ``q_indptr[b + 1] - 1`` are sequence b's newest tokens, which
+    ``seq_lens[b]`` counts already (see ts_attn.h). Rows may be a part of wider rows."""
+    B = _require_chunks(seq_lens, q_indptr, block_table)
+    if k_pool.dtype != k_new.dtype or v_pool.dtype != k_new.dtype:
+        raise TypeError("new rows and pools must have one dtype")
+    k, v, step = _chunk_rows(k_new, v_new, k_pool, v_pool)
+    _require_current_device(k_new, v_new, k_pool, v_pool, block_table, seq_lens, q_indptr)
+    T, H_kv, D = k_new.shape
+    _check(lib().ts_kv_append_chunk(k, v, _ptr(k_pool), _ptr(v_pool), _ptr(block_table), block_table.shape[1],
+                                    _ptr(seq_lens), _ptr(q_indptr), step, T, B, H_kv, D, k_pool.shape[1],
+                                    k_pool.shape[0], _dt(k_new), _stream(stream)))
+
+
+def ts_kv_append_chunk_fp8(k_new, v_new, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, q_indptr,
+                           stream=None) -> None:
+    """Quantize the K/V rows of a ragged batch of prompt chunks into fp8 pools and their
+    scales: placement as ``ts_kv_append_chunk``, values as ``ts_kv_append_fp8``."""
+    B = _require_chunks(seq_lens, q_indptr, block_table)
+    _require_fp8_cache(k_pool, v_pool, k_scale, v_scale)
+    k, v, step = _chunk_rows(k_new, v_new, k_pool, v_pool)
+    _require_current_device(k_new, v_new, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, q_indptr)
+    T, H_kv, D = k_new.shape
+    _check(lib().ts_kv_append_chunk_fp8(k, v, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
+                                        _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(q_indptr),
+                                        step, T, B, H_kv, D, k_pool.shape[1], k_pool.shape[0], _dt(k_new),
+                                        _stream(stream)))
+
+
+def ts_kv_read_fp8(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, kv_indptr, k_out, v_out,
+                   stream=None) -> None:
+    """Read an fp8 cache back: row ``kv_indptr[b] + t`` of k_out / v_out [rows, H_kv, D] (bf16
+    or f32) becomes token t of sequence b; other rows stay as they were (see ts_attn.h)."""
+    B = _require_chunks(seq_lens, kv_indptr, block_table)
+    _require_fp8_cache(k_pool, v_pool, k_scale, v_scale)
+    if k_pool.shape != v_pool.shape or k_out.shape != v_out.shape or k_out.dtype != v_out.dtype or \
+            k_out.shape[1:] != k_pool.shape[2:]:
+        raise ValueError("k_out and v_out must be [rows, H_kv, D] with the pools' H_kv and D")
+    _require_current_device(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, kv_indptr, k_out, v_out)
+    rows, H_kv, D = k_out.shape
+    _check(lib().ts_kv_read_fp8(_ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+                                block_table.shape[1], _ptr(seq_lens), _ptr(kv_indptr), rows, B, H_kv, D,
+                                k_pool.shape[1], k_pool.shape[0], _dt(k_out), _ptr(k_out), _ptr(v_out),
+                                _stream(stream)))
+
+
+def ts_paged_prefill_workspace_size(T: int, B: int, H_q: int, H_kv: int, D: int) -> int:
+    return int(lib().ts_paged_prefill_workspace_size(T, B, H_q, H_kv, D))
+
+
+def ts_paged_prefill_attn(q, k_pool, v_pool, block_table, seq_lens, q_indptr, scale: float, window: int = 0,
+                          sinks: int = 0, out=None, lse=None, workspace=None, stream=None, return_lse: bool = False):
+    """Attention of a ragged batch of prompt chunks, q [T, H_q, D] with rows ``q_indptr[b]`` ..
+    ``q_indptr[b + 1] - 1`` of sequence b, over a paged cache that holds their K/V rows
+    (``ts_kv_append_chunk``); ``seq_lens`` count them. Causal; ``window`` > 0 keeps the last
+    ``window`` tokens of each query and the sequence's first ``sinks``. Returns ``out``
+    [T, H_q, D] (and ``lse``); rows of no sequence are left as they were."""
+    B = _require_chunks(seq_lens, q_indptr, block_table)
+    T, H_q, D = q.shape
+    P, ps, H_kv, _ = k_pool.shape
+    _require_cache(q, k_pool, v_pool)
+    qp, step = _rows(q)
+    if out is None:
+        out = torch.empty(T, H_q, D, dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty(T, H_q, dtype=torch.float32, device=q.device)
+    _require_result(out, lse, q)
+    _require_current_device(q, k_pool, v_pool, block_table, seq_lens, q_indptr, out, lse, workspace)
+    if workspace is None:
+        workspace = new_workspace(ts_paged_prefill_workspace_size(T, B, H_q, H_kv, D), q.device)
+    _check(lib().ts_paged_prefill_attn(qp, step, _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
+                                       block_table.shape[1], _ptr(seq_lens), _ptr(q_indptr), T, B, H_q, H_kv, D, ps,
+                                       P, int(window), int(sinks), float(scale), _dt(q), _ptr(out), _ptr(lse),
+                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       _stream(stream)))
     return (out, lse) if return_lse else out
 
 

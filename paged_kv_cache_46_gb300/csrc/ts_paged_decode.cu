@@ -215,7 +215,7 @@ ts_status paged_decode_core(const void* q, const void* k_pool, const void* v_poo
                             void* out, float* lse, void* workspace, size_t workspace_bytes,
                             cudaStream_t stream, const char* who, const PrefixInputs* pre,
                             const Fp8Scales* f8 = nullptr, int32_t window = 0,
-                            bool check_only = false) {
+                            bool check_only = false, int32_t sinks = 0) {
   if (B < 0 || H_q <= 0 || H_kv <= 0 || D <= 0 || page_size <= 0 || num_pages <= 0 ||
       bt_stride <= 0 || static_cast<long long>(num_pages) * page_size > INT32_MAX)
     return fail(TS_ERR_INVALID_ARG, "%s: bad sizes (B=%d H_q=%d H_kv=%d D=%d ps=%d P=%d bt=%d)",
@@ -254,6 +254,7 @@ ts_status paged_decode_core(const void* q, const void* k_pool, const void* v_poo
       return fail(TS_ERR_INVALID_ARG, "%s: scale arrays must be 16-byte aligned", who);
   }
   KernelFn fn = f8 != nullptr ? pick_paged_fp8_kernel(D, g)
+                : sinks > 0   ? pick_paged_sink_kernel(dtype, D, g)
                 : window > 0  ? pick_paged_window_kernel(dtype, D, g)
                 : q_len == 1  ? pick_kernel(dtype, D, g, pre != nullptr)
                               : pick_paged_multi_kernel(dtype, D, g * fold);
@@ -302,6 +303,7 @@ ts_status paged_decode_core(const void* q, const void* k_pool, const void* v_poo
   prm.prefix_o = pre ? pre->prefix_o : nullptr;
   prm.prefix_lse = pre ? pre->prefix_lse : nullptr;
   prm.window = window;
+  prm.sinks = sinks;
   if (workspace != nullptr) {
     unsigned char* wsb = static_cast<unsigned char*>(workspace);
     prm.err_word = reinterpret_cast<uint32_t*>(wsb);
@@ -531,6 +533,21 @@ extern "C" ts_status ts_paged_decode_window_attn(const void* q, const void* k_po
   return ts::paged_decode_core(q, k_pool, v_pool, block_table, bt_stride, seq_lens, B, 1, H_q, H_kv, D,
                                page_size, num_pages, scale, dtype, out, lse, workspace, workspace_bytes,
                                static_cast<cudaStream_t>(stream), who, nullptr, nullptr, window);
+}
+
+extern "C" ts_status ts_paged_decode_sink_attn(const void* q, const void* k_pool, const void* v_pool,
+                                               const int32_t* block_table, int32_t bt_stride,
+                                               const int32_t* seq_lens, int32_t B, int32_t H_q, int32_t H_kv,
+                                               int32_t D, int32_t page_size, int32_t num_pages, int32_t window,
+                                               int32_t sinks, float scale, ts_dtype dtype, void* out, float* lse,
+                                               void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "ts_paged_decode_sink_attn";
+  if (window < 1 || sinks < 0)
+    return ts::fail(TS_ERR_INVALID_ARG, "%s: window=%d (>= 1 token), sinks=%d (>= 0 tokens)", who, window, sinks);
+  // no first tokens: the plain sliding window
+  return ts::paged_decode_core(q, k_pool, v_pool, block_table, bt_stride, seq_lens, B, 1, H_q, H_kv, D,
+                               page_size, num_pages, scale, dtype, out, lse, workspace, workspace_bytes,
+                               static_cast<cudaStream_t>(stream), who, nullptr, nullptr, window, false, sinks);
 }
 
 extern "C" size_t ts_paged_decode_multi_workspace_size(int32_t B, int32_t q_len, int32_t H_q, int32_t D) {

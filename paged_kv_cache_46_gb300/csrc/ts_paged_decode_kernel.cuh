@@ -68,6 +68,8 @@ struct PagedParams {
   // Sliding-window KV group (plain decode only): a sequence attends its last
   // `window` tokens; 0 = the whole context.
   int32_t window = 0;
+  // With a window: the first `sinks` tokens of the sequence stay visible too.
+  int32_t sinks = 0;
   // Byte offset in dynamic shared memory where the prologue keeps an int2 [B]
   // array of each virtual sequence's (own length, tokens in front of its own
   // pages) while it cuts the batch: the stage area, free until the producer's
@@ -89,6 +91,9 @@ PagedKernelFn pick_paged_fp8_kernel(int D, int G);
 // Kernel for a sliding-window KV group with G rows per kv head (defined in
 // ts_paged_decode_window.cu); nullptr if not compiled.
 PagedKernelFn pick_paged_window_kernel(ts_dtype dt, int D, int G);
+// Kernel for a sliding window with first tokens that stay visible, G rows per
+// kv head (defined in ts_paged_decode_sink.cu); nullptr if not compiled.
+PagedKernelFn pick_paged_sink_kernel(ts_dtype dt, int D, int G);
 
 namespace {
 
@@ -207,43 +212,63 @@ __device__ __forceinline__ int real_seq(const PagedParams& p, int v) {
   return v;
 }
 
+// Pages that hold the first tokens kept beside a sliding window, for a
+// sequence of L tokens; -1 where the window and those tokens together cover
+// the sequence, so that all of it is visible. (window >= 1: L - window does
+// not overflow.)
+__device__ __forceinline__ int sink_pages(const PagedParams& p, int L) {
+  return L > 0 && L - p.window > p.sinks ? (p.sinks + p.page_size - 1) / p.page_size : -1;
+}
+
 // Tokens in the whole pages in front of a sliding window (TokenSpeed deep
 // dive, section 4.1: a sliding_window KV group; tokenspeed 딥다이브, section
 // 6-3: the slots in front of the window hold a placeholder block). Their
-// block-table slots are skipped, never read.
-template <bool kWin>
-__device__ __forceinline__ int window_skip(const PagedParams& p, int v) {
+// block-table slots are skipped, never read. With first tokens kept (kSink)
+// the sequence's own pages are those of the first tokens followed by the
+// window's, and the skip is the tokens of the pages between the two; it is
+// -page_size when both meet in one page, which is then taken twice, each time
+// with its own rows.
+template <bool kWin, bool kSink>
+__device__ __forceinline__ int window_skip_len(const PagedParams& p, int L) {
   if constexpr (!kWin) {
     return 0;
+  } else if constexpr (kSink) {
+    const int ns = sink_pages(p, L);
+    return ns < 0 ? 0 : ((L - p.window) & -p.page_size) - ns * p.page_size;
   } else {
-    const int L = p.seq_lens[v];
     return L > p.window ? (L - p.window) & -p.page_size : 0;  // page_size: a power of two
   }
+}
+
+template <bool kWin, bool kSink>
+__device__ __forceinline__ int window_skip(const PagedParams& p, int v) {
+  if constexpr (!kWin) return 0;
+  else return window_skip_len<kWin, kSink>(p, p.seq_lens[v]);
 }
 
 // Own tokens of virtual sequence v: those its last row attends (after the
 // shared prefix in prefix mode, where every sequence has one query token).
 // With a sliding window: the tokens from the window's first page on (its
 // rows in front of the window are not copied).
-template <bool kPfx, bool kMulti, bool kWin>
+template <bool kPfx, bool kMulti, bool kWin, bool kSink>
 __device__ __forceinline__ int vseq_len(const PagedParams& p, int v) {
   if constexpr (kMulti) {
     const int b = real_seq<kMulti>(p, v);
     return p.seq_lens[b] - p.q_len + (v - b * p.steps + 1) * p.fold;
   } else {
-    return p.seq_lens[v] - prefix_tokens<kPfx>(p, v) - window_skip<kWin>(p, v);
+    return p.seq_lens[v] - prefix_tokens<kPfx>(p, v) - window_skip<kWin, kSink>(p, v);
   }
 }
 
 // vseq_len, also returning the tokens in front of the sequence's own pages
 // (its shared prefix, or the whole pages in front of its window).
-template <bool kPfx, bool kMulti, bool kWin>
+template <bool kPfx, bool kMulti, bool kWin, bool kSink>
 __device__ __forceinline__ int vseq_len_pre(const PagedParams& p, int v, int& pre) {
   if constexpr (kMulti) {
     pre = 0;
-    return vseq_len<kPfx, kMulti, kWin>(p, v);
+    return vseq_len<kPfx, kMulti, kWin, kSink>(p, v);
   } else {
-    pre = prefix_tokens<kPfx>(p, v) + window_skip<kWin>(p, v);
+    pre = prefix_tokens<kPfx>(p, v) + window_skip<kWin, kSink>(p, v);
     return p.seq_lens[v] - pre;
   }
 }
@@ -264,10 +289,11 @@ __device__ void write_empty_sequence(const PagedParams& p, int D, int b, int k, 
   if (lane == 0) p.split_info[b] = make_int2(k, 0);
 }
 
-template <typename T, int D, int G, bool kPfx, bool kMulti, bool kFp8, bool kWin = false>
+template <typename T, int D, int G, bool kPfx, bool kMulti, bool kFp8, bool kWin = false, bool kSink = false>
 __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const PagedParams p) {
   static_assert(!(kPfx && kMulti), "shared prefixes take one query token per sequence");
   static_assert(!kWin || (!kPfx && !kMulti && !kFp8), "sliding windows: plain decode");
+  static_assert(!kSink || kWin, "first tokens are kept beside a window");
   static_assert(!kFp8 || (G <= 4 && sizeof(T) == 2 && !kPfx), "fp8 cache: bf16 queries, up to 4 rows");
   // K/V element type (the lane split follows it); T is the query / output type
   using KV = std::conditional_t<kFp8, uint8_t, T>;
@@ -360,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const PagedPa
             const int g = grp[u];
             pre = g < 0 ? 0 : (s_plen != nullptr ? (g < p.num_groups ? s_plen[g] : 0) : p.prefix_len[g]);
           }
-          if constexpr (kWin) pre += raw[u] > p.window ? (raw[u] - p.window) & -p.page_size : 0;
+          if constexpr (kWin) pre += window_skip_len<kWin, kSink>(p, raw[u]);
           L = raw[u] - pre;
         }
         s_pro[b] = make_int2(L, pre);
@@ -374,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const PagedPa
       L = s_pro[b].x;
     } else {
       int pre;
-      L = vseq_len_pre<kPfx, kMulti, kWin>(p, b, pre);
+      L = vseq_len_pre<kPfx, kMulti, kWin, kSink>(p, b, pre);
       if (s_pro != nullptr) s_pro[b] = make_int2(L, pre);
     }
     if (L > 0)
@@ -393,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const PagedPa
       todo &= todo - 1u;
       const int slo = __shfl_sync(0xffffffffu, lo, src), shi = __shfl_sync(0xffffffffu, hi, src);
       for (int b = slo; b < shi; ++b)
-        if (vseq_len<kPfx, kMulti, kWin>(p, b) <= 0 && b % G_ctas == k)
+        if (vseq_len<kPfx, kMulti, kWin, kSink>(p, b) <= 0 && b % G_ctas == k)
           write_empty_sequence<T, kPfx>(p, D, b, k, lane);
     }
   }
@@ -421,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const PagedPa
   if (start < end && excl <= start && start < excl + mine) {
     long long off = excl;
     for (int b = lo; b < hi; ++b) {  // entries this thread wrote, or gathered before a barrier
-      const int L = s_pro != nullptr ? s_pro[b].x : vseq_len<kPfx, kMulti, kWin>(p, b);
+      const int L = s_pro != nullptr ? s_pro[b].x : vseq_len<kPfx, kMulti, kWin, kSink>(p, b);
       const long long np = L > 0 ? (L + ps - 1) / ps + A : 0;
       if (start < off + np) {
         s_start[0] = b;
@@ -461,8 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const PagedPa
         const int bb = base + lane;
         pre_out = 0;
         if (bb >= B) return -1;
-        pre_out = prefix_tokens<kPfx>(p, bb) + window_skip<kWin>(p, bb);
-        return max(vseq_len<kPfx, kMulti, kWin>(p, bb), 0);
+        pre_out = prefix_tokens<kPfx>(p, bb) + window_skip<kWin, kSink>(p, bb);
+        return max(vseq_len<kPfx, kMulti, kWin, kSink>(p, bb), 0);
       };
       int win_pre, nxt_pre;
       int win_len = load_len(wb, win_pre);
@@ -472,10 +498,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const PagedPa
       constexpr int kSegFirst = 1, kSegLast = 2;
       struct Chunk {
         int b, pg0, cnt, L, slot, flags, split;
+        int ns = -1;  // kSink: pages of first tokens kept in front of the window's (-1: whole context)
       };
       // entries past the row (length inconsistent with bt_stride) count as bad pages
       auto load_pid = [&](const Chunk& c, int pre) {
-        const int idx = pre / ps + c.pg0 + lane;  // prefix pages come first in the row
+        int idx = pre / ps + c.pg0 + lane;  // prefix pages come first in the row
+        if constexpr (kSink) {
+          if (c.pg0 + lane < c.ns) idx = c.pg0 + lane;  // a page of the first tokens
+        }
         if (lane < c.cnt && idx < p.bt_stride)
           return p.block_table[static_cast<int64_t>(real_seq<kMulti>(p, c.b)) * p.bt_stride + idx];
         return -1;
@@ -536,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const PagedPa
         c.cnt = min(32, seg_left);
         c.L = seg_L;
         c.slot = seg_slot;
+        if constexpr (kSink) c.ns = sink_pages(p, seg_L + seg_pre);
         seg_left -= c.cnt;
         if (seg_left == 0) c.flags |= kSegLast;
         pg += c.cnt;
@@ -563,9 +594,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const PagedPa
           const int pidx = cur.pg0 + i;
           const bool ok = page >= 0 && page < p.num_pages;
           // rows [lo, rows_end) of the page: a sliding window's first page
-          // starts at the window's first token
-          const int lo = (kWin && pidx == 0) ? max(0, cur.L - p.window) : 0;
-          const int rows_end = ok ? ((pidx == np_cur - 1) ? (cur.L - pidx * ps) : ps) : 0;
+          // starts at the window's first token, the last page of first tokens
+          // ends at the last of them
+          int lo = (kWin && pidx == 0) ? max(0, cur.L - p.window) : 0;
+          int rows_end = ok ? ((pidx == np_cur - 1) ? (cur.L - pidx * ps) : ps) : 0;
+          if constexpr (kSink) {
+            lo = pidx == cur.ns ? max(0, cur.L - p.window - pidx * ps) : 0;
+            if (pidx < cur.ns) rows_end = min(rows_end, p.sinks - pidx * ps);
+          }
           const int rows = kWin ? max(0, rows_end - lo) : rows_end;
           const int nchunks = rows > 0 ? (rows + p.chunk_rows - 1) / p.chunk_rows : 1;
           for (int c = 0; c < nchunks; ++c) {

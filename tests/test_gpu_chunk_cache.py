@@ -1,0 +1,283 @@
+"""GPU parity of the chunk appends (plain and quantizing, bit-exact), of the
+read-back of a quantized cache, and a run of all of them as a server makes it."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import paged_kv_cache_46_gb300 as ts
+from chunk_cases import DEV, ChunkCase, check_attention
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from paged_kv_cache_46_gb300 import build
+    build.build()
+    assert torch.cuda.is_available()
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+def _batch(seed, n, ctx, H_kv, D, ps, dtype, pad=0, fused=False):
+    """(k_new, v_new, block table, seq_lens, indptr, pages)."""
+    rng = np.random.default_rng(seed)
+    g = torch.Generator().manual_seed(seed)
+    n, L = np.asarray(n), np.asarray(n) + np.asarray(ctx)
+    need = (L + ps - 1) // ps
+    P = int(need.sum()) + 2
+    order = rng.permutation(P)
+    bt = np.full((len(n), max(1, int(need.max()))), order[-1], dtype=np.int32)
+    at = 0
+    for b in range(len(n)):
+        bt[b, :need[b]] = order[at:at + need[b]]
+        at += int(need[b])
+    T = int(n.sum()) + pad
+    x = torch.randn(T, 2 * H_kv + (3 if fused else 0), D, generator=g)
+    x[:, :, ::9] *= 30
+    x = x.to(dtype)
+    k, v = x[:, :H_kv], x[:, H_kv:2 * H_kv]
+    if not fused:
+        k, v = k.contiguous(), v.contiguous()
+    return k, v, bt, L, np.concatenate([[0], np.cumsum(n)]), P
+
+
+SHAPES = [
+    ([1], [0], 1, 64, 16), ([33], [99], 8, 128, 16), ([5, 0, 17], [3, 9, 0], 2, 64, 8),
+    ([130, 1, 64], [0, 31, 100], 4, 128, 32), ([7, 8, 9], [1, 2, 3], 3, 64, 16), ([0, 0, 3, 0], [5, 0, 1, 2], 1, 128, 8),
+]
+
+
+def _bits(t):
+    return t.contiguous().view(torch.int16 if t.element_size() == 2 else torch.int32)
+
+
+@pytest.mark.parametrize("n,ctx,H_kv,D,ps", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fused", [False, True])
+def test_append_is_exact_and_touches_nothing_else(n, ctx, H_kv, D, ps, dtype, fused):
+    k, v, bt, L, ptr, P = _batch(sum(n) + D, n, ctx, H_kv, D, ps, dtype, pad=5, fused=fused)
+    pools = [torch.full((P, ps, H_kv, D), float("nan"), dtype=dtype, device=DEV) for _ in range(2)]
+    before = [_bits(p).cpu().numpy() for p in pools]
+    ts.ts_kv_append_chunk(k.to(DEV), v.to(DEV), *pools, _i32(bt), _i32(L), _i32(ptr))
+    torch.cuda.synchronize()
+    ref = oracle.kv_append_chunk(*before, _bits(k).numpy(), _bits(v).numpy(), bt, L, ptr)
+    for got, want in zip(pools, ref):
+        assert np.array_equal(_bits(got).cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("n,ctx,H_kv,D,ps", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fused", [False, True])
+def test_fp8_append_is_exact_and_touches_nothing_else(n, ctx, H_kv, D, ps, dtype, fused):
+    k, v, bt, L, ptr, P = _batch(sum(n) + D, n, ctx, H_kv, D, ps, dtype, pad=5, fused=fused)
+    if len(k):
+        k[0, 0] = 0.0  # a group of zeros takes the scale's floor
+        v[-1, 0] = 1e-30
+    pools = [torch.randint(0, 255, (P, ps, H_kv, D), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    scales = [torch.rand(P, ps, H_kv, device=DEV) for _ in range(2)]
+    before = [t.cpu().numpy() for t in pools + scales]
+    ts.ts_kv_append_chunk_fp8(k.to(DEV), v.to(DEV), *pools, *scales, _i32(bt), _i32(L), _i32(ptr))
+    torch.cuda.synchronize()
+    ref = oracle.kv_append_chunk_fp8(*before, k.float().numpy(), v.float().numpy(), bt, L, ptr)
+    for got, want in zip(pools + scales, ref):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_fp8_append_of_every_bf16_magnitude(dtype):
+    """Quotients near every rounding border: all positive bf16 values within 2^-18 .. 1 of the
+    group's maximum, and random float32 ones, against the single-token append bit for bit."""
+    H_kv, D, ps = 2, 128, 16
+    vals = torch.arange(0x3600, 0x3f80, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).float()
+    rows = []
+    for top in (1.0, 1.5, 1.0078125, 1.9921875, 7.0, 448.0, 0.33):
+        x = vals * top
+        x = x[: len(x) // 127 * 127].view(-1, 127)
+        rows.append(torch.cat([x, torch.full((len(x), 1), top)], 1))
+    x = torch.cat(rows)
+    x = torch.cat([x, torch.randn(301, D, generator=torch.Generator().manual_seed(1)).exp()])
+    x = x[: len(x) // 2 * 2].view(-1, 2, D).to(dtype).to(DEV)
+    T = len(x)
+    P = (T + ps - 1) // ps
+    bt = torch.arange(P, dtype=torch.int32, device=DEV)[None].contiguous()
+    new = [torch.zeros(P, ps, H_kv, D, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    new += [torch.zeros(P, ps, H_kv, device=DEV) for _ in range(2)]
+    old = [torch.zeros_like(t) for t in new]
+    ts.ts_kv_append_chunk_fp8(x, -x, *new, bt, _i32([T]), _i32([0, T]))
+    ts.ts_kv_append_fp8(x, -x, *old, bt.expand(T, -1).contiguous(), torch.arange(T, dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    for a, b in zip(new, old):
+        assert torch.equal(a, b)
+    ref = oracle.kv_append_chunk_fp8(*[t.cpu().numpy() * 0 for t in new], x.float().cpu().numpy(),
+                                     -x.float().cpu().numpy(), bt.cpu().numpy(), [T], [0, T])
+    for a, b in zip(new, ref):
+        assert np.array_equal(a.cpu().numpy(), b)
+
+
+def test_appends_skip_rows_without_a_place():
+    """Negative positions, slots past the table, page ids out of range, rows outside the
+    offsets, offsets out of order: skipped, nothing else written."""
+    k, v, bt, L, ptr, P = _batch(4, [20, 20], [30, 30], 2, 64, 16, torch.bfloat16)
+    k, v = k.to(DEV), v.to(DEV)
+    bt = bt.copy()
+    bt[0, 2], bt[1, 3] = -5, P
+    for lens, offsets in (([50, 50], [0, 20, 40]), ([10, 0], [0, 20, 40]), ([500, 50], [3, 20, 35]),
+                          ([50, 50], [0, 60, 40]), ([50, 50], [40, 20, 0]), ([50, 50], [-8, 20, 4000])):
+        room = [torch.zeros(P + 4, 16, 2, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        room8 = [torch.zeros(P + 4, 16, 2, 64, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        scales = [torch.zeros(P + 4, 16, 2, device=DEV) for _ in range(2)]
+        inner = lambda ts_: [t[2:-2] for t in ts_]  # noqa: E731
+        ts.ts_kv_append_chunk(k, v, *inner(room), _i32(bt), _i32(lens), _i32(offsets))
+        ts.ts_kv_append_chunk_fp8(k, v, *inner(room8), *inner(scales), _i32(bt), _i32(lens), _i32(offsets))
+        torch.cuda.synchronize()
+        for t in room + room8 + scales:
+            assert not t[:2].any() and not t[-2:].any()
+        if offsets == [0, 20, 40] and lens == [50, 50]:
+            good = [(b, j) for b in range(2) for j in range(20) if 0 <= bt[b, (30 + j) // 16] < P]
+            want = torch.zeros(P, 16, 2, 64, dtype=torch.bfloat16)
+            for b, j in good:
+                want[bt[b, (30 + j) // 16], (30 + j) % 16] = k[20 * b + j].cpu()
+            assert torch.equal(room[0][2:-2].cpu(), want)
+
+
+@pytest.mark.parametrize("n,ctx,H_kv,D,ps", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_read_back_is_exact_and_touches_nothing_else(n, ctx, H_kv, D, ps, dtype):
+    """Every code value, ranges longer than the sequences, rows in front and behind."""
+    _, _, bt, L, _, P = _batch(sum(n), n, ctx, H_kv, D, ps, torch.bfloat16)
+    g = torch.Generator().manual_seed(1)
+    pools = [torch.randint(0, 256, (P, ps, H_kv, D), dtype=torch.uint8, generator=g) for _ in range(2)]
+    for p in pools:
+        p[(p & 0x7f) == 0x7f] = 0x7e  # no NaN codes: they compare unequal
+    scales = [torch.rand(P, ps, H_kv, generator=g) for _ in range(2)]
+    ptr = np.concatenate([[3], 3 + np.cumsum(L + np.arange(len(L)) % 3)])
+    rows = int(ptr[-1]) + 4
+    outs = [torch.full((rows, H_kv, D), 7.0, dtype=dtype, device=DEV) for _ in range(2)]
+    ts.ts_kv_read_fp8(*[t.to(DEV) for t in pools + scales], _i32(bt), _i32(L), _i32(ptr), *outs)
+    torch.cuda.synchronize()
+    for p, s, got in zip(pools, scales, outs):
+        ref = oracle.kv_read_fp8(p.numpy(), s.numpy(), bt, L, ptr, np.full((rows, H_kv, D), 7.0))
+        assert torch.equal(got.cpu(), torch.from_numpy(ref).to(dtype))
+
+
+def test_read_back_keeps_rows_without_a_token():
+    _, _, bt, L, _, P = _batch(5, [20, 20], [30, 30], 2, 64, 16, torch.bfloat16)
+    bt = bt.copy()
+    bt[0, 1], bt[1, 0] = -1, P
+    pool = torch.full((P, 16, 2, 64), 0x38, dtype=torch.uint8, device=DEV)  # 1.0
+    scale = torch.full((P, 16, 2), 2.0, device=DEV)
+    for lens, ptr in (([50, 50], [0, 50, 100]), ([-4, 900], [0, 50, 100]), ([50, 50], [0, 70, 20]),
+                      ([50, 50], [-9, 50, 5000])):
+        outs = [torch.full((100 + 8, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        ts.ts_kv_read_fp8(pool, pool, scale, scale, _i32(bt), _i32(lens), _i32(ptr), *[o[4:-4] for o in outs])
+        torch.cuda.synchronize()
+        for o in outs:
+            assert torch.all(o[:4] == 7.0) and torch.all(o[-4:] == 7.0)
+            assert torch.all((o == 7.0) | (o == 2.0))
+        if ptr == [0, 50, 100] and lens == [50, 50]:
+            there = torch.ones(100, dtype=torch.bool)
+            there[16:32] = False
+            there[50:66] = False
+            assert torch.equal((outs[0][4:-4, 0, 0] == 2.0).cpu(), there)
+
+
+def test_empty_calls_do_nothing():
+    k = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    pool = torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16, device=DEV)
+    ts.ts_kv_append_chunk(k, k, pool, pool.clone(), _i32([[0]]), _i32([0]), _i32([0, 0]))
+    q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=DEV)
+    assert ts.ts_paged_prefill_attn(q, pool, pool, _i32([[0]]), _i32([0]), _i32([0, 0]), 0.1).shape == (0, 4, 64)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("ps", [8, 16])
+def test_a_server_run_over_a_quantized_cache(ps):
+    """Three steps of two prompts: chunks quantized into the cache, the cache read back as
+    consecutive pages, the chunks' attention over those; the same over a bf16 cache; then a
+    decode step over each. Held to the oracle over the very values each cache holds."""
+    H_q, H_kv, D, B = 8, 2, 64, 2
+    g = torch.Generator().manual_seed(3)
+    P, slots = 40, 16
+    bt = torch.randperm(P, generator=g)[:B * slots].view(B, slots).to(torch.int32)
+    chunks = [[60, 7], [33, 0], [1, 90]]
+    pools = [torch.full((P, ps, H_kv, D), float("nan"), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    codes = [torch.full((P, ps, H_kv, D), 0x7f, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    scales = [torch.full((P, ps, H_kv), float("nan"), device=DEV) for _ in range(2)]
+    scale = D ** -0.5
+    L = np.zeros(B, dtype=np.int64)
+    for n in chunks:
+        L = L + n
+        T = sum(n)
+        ptr = np.concatenate([[0], np.cumsum(n)])
+        qkv = torch.randn(T, H_q + 2 * H_kv, D, generator=g).to(torch.bfloat16).to(DEV)
+        q, k, v = qkv[:, :H_q], qkv[:, H_q:H_q + H_kv], qkv[:, H_q + H_kv:]
+        dev = (bt.to(DEV), _i32(L), _i32(ptr))
+        ts.ts_kv_append_chunk(k, v, *pools, *dev)
+        ts.ts_kv_append_chunk_fp8(k, v, *codes, *scales, *dev)
+        starts = np.concatenate([[0], np.cumsum((L + ps - 1) // ps * ps)])
+        flat = [torch.zeros(int(starts[-1]), H_kv, D, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        ts.ts_kv_read_fp8(*codes, *scales, dev[0], dev[1], _i32(starts), *flat)
+        read = [f.view(-1, ps, H_kv, D) for f in flat]
+        at = np.arange(slots)[None] + starts[:-1, None] // ps
+        at = np.where(at < starts[1:, None] // ps, at, 0).astype(np.int32)
+        for pk, pv, table in ((*pools, bt.numpy()), (*read, at)):
+            out, lse = ts.ts_paged_prefill_attn(q, pk, pv, _i32(table), dev[1], dev[2], scale, return_lse=True)
+            dq = torch.randn(B, H_q, D, generator=g).to(torch.bfloat16)
+            d_out, d_lse = ts.ts_paged_decode_sink_attn(dq.to(DEV), pk, pv, _i32(table), dev[1], scale, 20, 3,
+                                                        return_lse=True)
+            torch.cuda.synchronize()
+            kk, vv = pk.double().cpu().numpy(), pv.double().cpu().numpy()
+            args = (table, L, ptr, scale)
+            qd = q.double().cpu().numpy()
+            ref = (*oracle.prefill_attention(qd, kk, vv, *args), oracle.prefill_attention(qd, kk, np.abs(vv), *args)[0],
+                   scale * np.nanmax(np.abs(kk).sum(-1)) * np.abs(qd).max())
+            check_attention(out, lse, ref, D, int(L.max()), "bf16")
+            dd = dq.double().numpy()
+            ref = (*oracle.decode_attention_sinks(dd, kk, vv, table, L, scale, 20, 3),
+                   oracle.decode_attention_sinks(dd, kk, np.abs(vv), table, L, scale, 20, 3)[0],
+                   scale * np.nanmax(np.abs(kk).sum(-1)) * np.abs(dd).max())
+            check_attention(d_out, d_lse, ref, D, int(L.max()), "bf16")
+
+
+def test_appends_and_attention_captured_together():
+    """The step of a server as one graph, replayed with new rows and lengths."""
+    case = ChunkCase(20, [30, 50], [40, 0], 8, 2, 64)
+    a = case.device()
+    T = case.T
+    kn, vn = (torch.zeros(T, 2, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    ws = ts.new_workspace(ts.ts_paged_prefill_workspace_size(T, 2, 8, 2, 64))
+    out = torch.zeros(T, 8, 64, dtype=torch.bfloat16, device=DEV)
+    lse = torch.zeros(T, 8, device=DEV)
+
+    def step():
+        ts.ts_kv_append_chunk(kn, vn, a["k_pool"], a["v_pool"], a["block_table"], a["seq_lens"], a["q_indptr"])
+        ts.ts_paged_prefill_attn(**a, workspace=ws, out=out, lse=lse)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    g = torch.Generator().manual_seed(1)
+    for n in ([30, 50], [45, 35]):
+        case.n = np.array(n)
+        case.L = np.array([70, 50]) if n[0] == 30 else np.array([60, 45])
+        case.indptr = np.array([0, n[0], 80], dtype=np.int32)
+        a["seq_lens"].copy_(torch.from_numpy(case.L.astype(np.int32)))
+        a["q_indptr"].copy_(torch.from_numpy(case.indptr))
+        kn.copy_(torch.randn(T, 2, 64, generator=g).to(torch.bfloat16))
+        vn.copy_(torch.randn(T, 2, 64, generator=g).to(torch.bfloat16))
+        want = oracle.kv_append_chunk(a["k_pool"].double().cpu().numpy(), a["v_pool"].double().cpu().numpy(),
+                                      kn.double().cpu().numpy(), vn.double().cpu().numpy(), case.bt, case.L,
+                                      case.indptr)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip((a["k_pool"], a["v_pool"]), want):
+            assert np.array_equal(got.double().cpu().numpy(), ref, equal_nan=True)
+        assert ts.ts_read_device_error(ws) == 0
+        check_attention(out, lse, case.oracle(torch.from_numpy(want[0]), torch.from_numpy(want[1])), 64, 80, "bf16")

@@ -22,6 +22,7 @@
 //   warp 8          TMA of K and V: one box per page and 64-column atom
 //   warp 9          issues the products
 //   warp 10         TMA of the queries
+//   warp 11         walks the range and hands its pieces to the others
 // S = Q K^T goes to TMEM (128 columns a tile); the softmax takes its row into
 // registers and writes P, as bf16, over the front half of the same columns,
 // where it is the A operand of O += P V. Products of one thread complete in
@@ -60,8 +61,9 @@ struct Lay {
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = 2 * kTileBytes;
   static constexpr int kOffBar = kOffKV + kRing * kTileBytes;
-  static constexpr int kOffBad = kOffBar + 256;
-  static constexpr int kOffMisc = kOffBad + kBadRing * 4;
+  static constexpr int kOffBad = kOffBar + 320;
+  static constexpr int kOffPieces = kOffBad + kBadRing * 4;
+  static constexpr int kOffMisc = kOffPieces + 4 * 48;
   static constexpr int kSmem = kOffMisc + 128 + 12 * 8;
   static constexpr uint32_t kTmemO = 256;  // S of tile t at 128 t, O of tile t at 256 + D t
 };
@@ -105,6 +107,9 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
+// The lowest n bits (none below 0, all from 32 on).
+__device__ __forceinline__ uint32_t ones(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // A sequence of the batch, and an item of it.
 struct Seq {
   int row0, n, L, blocks;  // first row, new tokens, tokens in the cache, token blocks
@@ -143,18 +148,25 @@ __device__ __forceinline__ Item load_item(const PrefillParams& p, const Seq& s, 
   return it;
 }
 
-__device__ __forceinline__ int key_tile(const Item& it, int i) { return i < it.ns ? i : it.w0 + i - it.ns; }
+// A piece of the CTA's range: key tiles [t0, t0 + nk) of one item. Warp 11
+// writes them to a ring in shared memory, ahead of the roles that read them.
+struct alignas(16) Piece {
+  int nk, t0;            // key tiles; nk = 0: an item without keys, nk < 0: the range's end
+  int ns, w0;            // key tile i of the item is tile i < ns ? i : w0 + i - ns of the sequence
+  int klo, khi;          // keys some row of the item sees: [klo, khi) and [0, sinks)
+  int p0, tokens;        // position of its first token, its tokens
+  int head, row0, slot;  // kv head; first token's row in the batch; slot of the state, -1: the whole item
+  int seq;               // sequence
+};
+constexpr int kPieces = 4;        // pieces in the ring
+constexpr int kPieceReaders = 11;  // warps that read each piece
 
-// The CTA's range of units, walked piece by piece. Every role walks it itself:
-// a step within a sequence is arithmetic only.
+// The CTA's range of units, walked piece by piece.
 struct Walk {
   int left;              // units of the range still to walk
   int b, h, block, rem;  // the next unit: item, and unit within it
   Seq s;
   bool first;  // no piece returned yet
-  // the current piece: key tiles [t0, t1) of item `it` of sequence pb, kv head ph
-  Item it;
-  int pb, ph, prow0, t0, t1, slot;
 
   __device__ __forceinline__ void init(const PrefillParams& p, const int* start) {
     left = start[4];
@@ -165,17 +177,26 @@ struct Walk {
     first = true;
     if (left > 0) s = load_seq(p, b);
   }
-  __device__ __forceinline__ bool next(const PrefillParams& p, int k) {
+  // The next piece; also whether the item goes on in later CTAs from its first
+  // key tile here (then `rest` is the number of its key tiles there).
+  __device__ __forceinline__ bool next(const PrefillParams& p, int k, Piece& q, int& rest) {
     while (left > 0) {
-      it = load_item(p, s, block);
+      const Item it = load_item(p, s, block);
       const int cost = it.nt + kItemUnits;
       const int here = min(cost - rem, left);
       const bool owner = rem == 0;
-      t0 = max(0, rem - kItemUnits);
-      t1 = max(t0, rem + here - kItemUnits);
-      pb = b;
-      ph = h;
-      prow0 = s.row0 + it.j0;
+      const int t0 = max(0, rem - kItemUnits), t1 = max(t0, rem + here - kItemUnits);
+      q.nk = t1 - t0;
+      q.t0 = t0;
+      q.ns = it.ns;
+      q.w0 = it.w0;
+      q.klo = it.klo;
+      q.khi = it.khi;
+      q.p0 = it.p0;
+      q.tokens = it.tokens;
+      q.head = h;
+      q.row0 = s.row0 + it.j0;
+      q.seq = b;
       left -= here;
       rem += here;
       if (rem == cost) {
@@ -198,7 +219,8 @@ struct Walk {
       }
       if (t1 > t0 || (it.nt == 0 && owner)) {
         const bool whole = t0 == 0 && t1 == it.nt;
-        slot = whole ? -1 : 2 * k + (first ? 0 : 1);
+        q.slot = whole ? -1 : 2 * k + (first ? 0 : 1);
+        rest = t0 == 0 ? it.nt - t1 : 0;
         first = false;
         return true;
       }
@@ -230,7 +252,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
   auto b_pvdone = [&](int t) { return smem_u32(&bars[2 * kRing + 4 + t]); };
   auto b_ofree = [&](int t) { return smem_u32(&bars[2 * kRing + 6 + t]); };
   const uint32_t b_qfull = smem_u32(&bars[2 * kRing + 8]), b_qempty = smem_u32(&bars[2 * kRing + 9]);
-  static_assert((2 * kRing + 10) * 8 <= 256, "mbarriers fit their slot");
+  auto b_piece = [&](int s) { return smem_u32(&bars[2 * kRing + 10 + s]); };
+  auto b_taken = [&](int s) { return smem_u32(&bars[2 * kRing + 10 + kPieces + s]); };
+  static_assert((2 * kRing + 10 + 2 * kPieces) * 8 <= 320, "mbarriers fit their slot");
+  static_assert(kPieces * sizeof(Piece) == L::kOffMisc - L::kOffPieces, "piece ring");
+  Piece* ring = reinterpret_cast<Piece*>(smem + L::kOffPieces);
   volatile uint32_t* bad_ring = reinterpret_cast<volatile uint32_t*>(smem + L::kOffBad);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   int* start = reinterpret_cast<int*>(smem + L::kOffMisc + 16);
@@ -250,6 +276,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     }
     mbar_init(b_qfull, 1);
     mbar_init(b_qempty, 1);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(b_piece(i), 1);
+      mbar_init(b_taken(i), kPieceReaders);
+    }
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(smem_u32(tmem_slot), 512);
@@ -322,22 +352,62 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
 
   const int tt = p.tile_tokens;
   bool ok = true;
+  // A reader waits for piece n (all its threads that use it), copies what it
+  // needs, and hands the entry back once per warp.
+  auto piece_ready = [&](uint32_t n) { return mbar_wait(b_piece(n % kPieces), (n / kPieces) & 1); };
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    Walk w;
-    w.init(p, start);
-    if (warp == 8) {
+    if (warp == 11) {
+      // ---------------- pieces ------------------------------------------------
+      if (lane == 0) {
+        Walk w;
+        w.init(p, start);
+        p.split[k].row0 = -1;
+        bool more = true;
+        for (uint32_t n = 0; more; ++n) {
+          Piece q;
+          int rest = 0;
+          more = w.next(p, k, q, rest);
+          if (!more) q.nk = -1;
+          if (n >= kPieces && !mbar_wait(b_taken(n % kPieces), (n / kPieces - 1) & 1)) {
+            set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
+            break;
+          }
+          ring[n % kPieces] = q;
+          mbar_arrive(b_piece(n % kPieces));
+          if (more && rest > 0) {  // its last key tile lies `rest` units behind this CTA's range
+            const long long qu = cut[1], r = cut[2], big = r * (qu + 1), last = cut[0] + rest - 1;
+            SplitItem si;
+            si.tokens = q.tokens;
+            si.head = q.head;
+            si.parts = static_cast<int>(last < big ? last / (qu + 1) : r + (last - big) / max(qu, 1ll)) - k + 1;
+            si.slot = q.slot;
+            si.row0 = q.row0;
+            p.split[k] = si;
+          }
+        }
+      }
+    } else if (warp == 8) {
       // ---------------- K and V: lane i holds page i of the key tile --------
       const int npg = kBN / p.page_size;
       const int oob = p.num_pages * p.page_size;  // a row past the pool: zero fill
       uint32_t seq = 0, tiles = 0;                // K and V tiles issued; key tiles
-      while (ok && w.next(p, k)) {
-        const int64_t bt = static_cast<int64_t>(w.pb) * p.bt_stride;
-        auto page_row = [&](int i, uint32_t& bad) {  // this lane's page of tile i
-          const int pi = key_tile(w.it, i) * npg + lane, t = pi * p.page_size;
+      uint32_t s = 0, phase = 1;                  // ring slot of the next one, and its last use's phase
+      for (uint32_t n = 0;; ++n) {
+        ok = __all_sync(0xffffffffu, piece_ready(n));
+        if (!ok) break;
+        const Piece q = ring[n % kPieces];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_taken(n % kPieces));
+        if (q.nk < 0) break;
+        // tokens past the block table's row: absent, as those of a bad page
+        if (lane == 0 && q.p0 + q.tokens > max(q.khi, 0)) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
+        const int64_t bt = static_cast<int64_t>(q.seq) * p.bt_stride;
+        auto page_row = [&](int i, uint32_t& bad) {  // this lane's page of tile i of the item
+          const int pi = (i < q.ns ? i : q.w0 + i - q.ns) * npg + lane, t = pi * p.page_size;
           int row = oob;
           bool wrong = false;
-          if (lane < npg && t < w.it.khi && (t + p.page_size > w.it.klo || t < p.sinks)) {
+          if (lane < npg && t < q.khi && (t + p.page_size > q.klo || t < p.sinks)) {
             const int page = p.block_table[bt + pi];
             wrong = page < 0 || page >= p.num_pages;
             if (!wrong) row = page * p.page_size;
@@ -346,9 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           return row;
         };
         auto load_tile = [&](const CUtensorMap* map, int row) {
-          const int s = seq % kRing;
           bool good = true;
-          if (lane == 0 && seq >= kRing) good = mbar_wait(b_empty(s), (seq / kRing - 1) & 1);
+          if (lane == 0 && seq >= kRing) good = mbar_wait(b_empty(s), phase);
           good = __shfl_sync(0xffffffffu, good, 0);
           if (!good) return false;
           if (lane == 0) mbar_arrive_expect_tx(b_full(s), kTile);
@@ -357,15 +426,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           const int pg = lane / kAtoms, a = lane % kAtoms;
           const int r = __shfl_sync(0xffffffffu, row, pg);
           if (lane < boxes)
-            tma_load_3d(sKV + s * kTile + a * kAtom + pg * p.page_size * 128, map, a * 64, r, w.ph, b_full(s));
+            tma_load_3d(sKV + s * kTile + a * kAtom + pg * p.page_size * 128, map, a * 64, r, q.head, b_full(s));
           ++seq;
+          if (++s == kRing) {
+            s = 0;
+            phase ^= 1;
+          }
           return true;
         };
-        uint32_t bad;
-        int row = page_row(w.t0, bad);
-        for (int i = w.t0; i < w.t1 && ok; ++i) {
+        const int t1 = q.t0 + q.nk;
+        uint32_t bad = 0;
+        int row = q.nk > 0 ? page_row(q.t0, bad) : oob;
+        for (int i = q.t0; i < t1 && ok; ++i) {
           uint32_t bad_next = 0;
-          const int row_next = i + 1 < w.t1 ? page_row(i + 1, bad_next) : oob;
+          const int row_next = i + 1 < t1 ? page_row(i + 1, bad_next) : oob;
           if (lane == 0) {
             bad_ring[tiles % kBadRing] = bad;
             if (bad) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
@@ -375,31 +449,37 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           row = row_next;
           bad = bad_next;
         }
-        // tokens past the block table's row: absent, as those of a bad page
-        if (lane == 0 && w.it.p0 + w.it.tokens > w.it.khi && w.it.p0 + w.it.tokens > 0)
-          set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
+        if (!ok) break;
       }
       if (!ok && lane == 0) {
         set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
         // let the copies in flight land before the CTA's shared memory goes
-        for (uint32_t s = seq > kRing ? seq - kRing : 0; s < seq; ++s) mbar_wait(b_full(s % kRing), (s / kRing) & 1);
+        for (uint32_t i = seq > kRing ? seq - kRing : 0; i < seq; ++i) mbar_wait(b_full(i % kRing), (i / kRing) & 1);
       }
     } else if (warp == 10) {
       // ---------------- queries ---------------------------------------------
       if (lane == 0) {
         uint32_t pieces = 0;
-        while (w.next(p, k)) {
-          if (w.t1 == w.t0) continue;
-          if (pieces > 0 && !mbar_wait(b_qempty, (pieces - 1) & 1)) {
-            set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
-            break;
-          }
-          const int nq = w.it.tokens > tt ? 2 : 1;
+        for (uint32_t n = 0;; ++n) {
+          ok = piece_ready(n);
+          if (!ok) break;
+          const Piece& q = ring[n % kPieces];
+          const int nk = q.nk, tokens = q.tokens, row0 = q.row0, head = q.head;
+          mbar_arrive(b_taken(n % kPieces));
+          if (nk < 0) break;
+          if (nk == 0) continue;
+          ok = pieces == 0 || mbar_wait(b_qempty, (pieces - 1) & 1);
+          if (!ok) break;
+          const int nq = tokens > tt ? 2 : 1;
           mbar_arrive_expect_tx(b_qfull, nq * kAtoms * tt * p.g * 128);
           for (int t = 0; t < nq; ++t)
             for (int a = 0; a < kAtoms; ++a)
-              tma_load_3d(sQ + t * kTile + a * kAtom, &qmap, a * 64, w.ph * p.g, w.prow0 + t * tt, b_qfull);
+              tma_load_3d(sQ + t * kTile + a * kAtom, &qmap, a * 64, head * p.g, row0 + t * tt, b_qfull);
           ++pieces;
+        }
+        if (!ok) {
+          set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
+          if (pieces > 0) mbar_wait(b_qfull, (pieces - 1) & 1);  // a copy in flight lands first
         }
       }
     } else if (warp == 9) {
@@ -407,58 +487,94 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       if (lane == 0) {
         constexpr uint32_t iS = idesc_bf16(kBM, kBN, 0);
         constexpr uint32_t iO = idesc_bf16(kBM, D, 1);
-        uint32_t seq = 0, pieces = 0;
-        uint32_t steps[2] = {0, 0}, used[2] = {0, 0};  // P V products and pieces of each tile
-        auto issue_s = [&](int t, uint32_t kseq, bool last) {
-          const uint32_t q = sQ + t * kTile, kb = sKV + (kseq % kRing) * kTile;
+        // descriptors of the first Q and ring tile; others differ by an address
+        // difference in 16-byte units, which stays within the address field
+        const uint64_t dQ = desc_sw128(sQ), dK = desc_sw128(sKV), dV = desc_sw128(sKV, kAtom, 1024);
+        constexpr uint64_t kTileStep = kTile >> 4;
+        uint32_t slot = 0, phase = 0;  // of the next K or V tile to wait for
+        uint32_t pieces = 0, steps0 = 0, steps1 = 0, used0 = 0, used1 = 0;
+        auto wait_next = [&]() {  // the next K or V tile has landed
+          const bool good = mbar_wait(b_full(slot), phase);
+          tc_fence_after();
+          return good;
+        };
+        auto advance = [&]() {
+          const uint32_t s = slot;
+          if (++slot == kRing) {
+            slot = 0;
+            phase ^= 1;
+          }
+          return s;
+        };
+        auto issue_s = [&](int t, uint32_t ks_slot) {
+          const uint64_t q = dQ + t * kTileStep, kb = dK + ks_slot * kTileStep;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks >> 2) * kAtom + (ks & 3) * 32;
-            mma_bf16(tmem + t * 128, desc_sw128(q + off), desc_sw128(kb + off), iS, ks > 0);
+            constexpr uint64_t kAtomStep = kAtom >> 4;
+            const uint64_t off = (ks >> 2) * kAtomStep + (ks & 3) * 2;
+            mma_bf16(tmem + t * 128, q + off, kb + off, iS, ks > 0);
           }
           mma_commit(b_sfull(t));
           // the arrival carries what the key tile's barrier carried here: the
           // softmax reads the tile's bad-page mask after it
           mbar_arrive(b_sfull(t));
-          if (last) mma_commit(b_empty(kseq % kRing));
         };
-        auto wait_full = [&](uint32_t s) {
-          const bool good = mbar_wait(b_full(s % kRing), (s / kRing) & 1);
+        auto issue_pv = [&](int t, uint32_t v_slot, bool first) {
           tc_fence_after();
-          return good;
-        };
-        while (ok && w.next(p, k)) {
-          if (w.t1 == w.t0) continue;
-          const int nq = w.it.tokens > tt ? 2 : 1;
-          ok = mbar_wait(b_qfull, pieces & 1) && wait_full(seq);
-          if (!ok) break;
-          for (int t = 0; t < nq; ++t) issue_s(t, seq, t == nq - 1);
-          if (w.t1 - w.t0 == 1) mma_commit(b_qempty);
-          for (int i = w.t0; i < w.t1 && ok; ++i) {
-            for (int t = 0; t < nq; ++t) {
-              ok = mbar_wait(b_pfull(t), steps[t] & 1);
-              if (ok && t == 0) ok = wait_full(seq + 1);
-              if (ok && i == w.t0 && used[t] > 0) ok = mbar_wait(b_ofree(t), (used[t] - 1) & 1);
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t vb = sKV + ((seq + 1) % kRing) * kTile;
+          const uint64_t vb = dV + v_slot * kTileStep;
 #pragma unroll
-              for (int ks = 0; ks < kBN / 16; ++ks)
-                mma_bf16_tmem_a(tmem + L::kTmemO + t * D, tmem + t * 128 + ks * 8,
-                                desc_sw128(vb + ks * 2048, kAtom, 1024), iO, (i > w.t0 || ks > 0) ? 1u : 0u);
-              mma_commit(b_pvdone(t));
-              if (t == nq - 1) mma_commit(b_empty((seq + 1) % kRing));
-              ++steps[t];
-              if (i + 1 < w.t1) {
-                if (t == 0) ok = wait_full(seq + 2);
-                if (!ok) break;
-                issue_s(t, seq + 2, t == nq - 1);
-                if (t == nq - 1 && i + 2 == w.t1) mma_commit(b_qempty);
-              }
+          for (int ks = 0; ks < kBN / 16; ++ks)
+            mma_bf16_tmem_a(tmem + L::kTmemO + t * D, tmem + t * 128 + ks * 8, vb + ks * 128, iO,
+                            (!first || ks > 0) ? 1u : 0u);
+          mma_commit(b_pvdone(t));
+        };
+        for (uint32_t n = 0;; ++n) {
+          ok = piece_ready(n);
+          if (!ok) break;
+          const int nk = ring[n % kPieces].nk;
+          const bool two = ring[n % kPieces].tokens > tt;
+          mbar_arrive(b_taken(n % kPieces));
+          if (nk < 0) break;
+          if (nk == 0) continue;
+          ok = mbar_wait(b_qfull, pieces & 1) && wait_next();
+          if (!ok) break;
+          uint32_t ks_slot = advance();
+          issue_s(0, ks_slot);
+          if (two) issue_s(1, ks_slot);
+          mma_commit(b_empty(ks_slot));
+          if (nk == 1) mma_commit(b_qempty);
+          for (int i = 0; i < nk; ++i) {
+            const bool more = i + 1 < nk;
+            ok = mbar_wait(b_pfull(0), steps0 & 1) && wait_next();
+            if (ok && i == 0 && used0 > 0) ok = mbar_wait(b_ofree(0), (used0 - 1) & 1);
+            if (!ok) break;
+            const uint32_t v_slot = advance();
+            ++steps0;
+            issue_pv(0, v_slot, i == 0);
+            if (!two) mma_commit(b_empty(v_slot));
+            if (more) {
+              ok = wait_next();
+              if (!ok) break;
+              ks_slot = advance();
+              issue_s(0, ks_slot);
             }
-            seq += 2;
+            if (two) {
+              ok = mbar_wait(b_pfull(1), steps1 & 1);
+              if (ok && i == 0 && used1 > 0) ok = mbar_wait(b_ofree(1), (used1 - 1) & 1);
+              if (!ok) break;
+              ++steps1;
+              issue_pv(1, v_slot, i == 0);
+              mma_commit(b_empty(v_slot));
+              if (more) issue_s(1, ks_slot);
+            }
+            if (more) {
+              mma_commit(b_empty(ks_slot));
+              if (i + 2 == nk) mma_commit(b_qempty);
+            }
           }
-          for (int t = 0; t < nq; ++t) ++used[t];
+          if (!ok) break;
+          ++used0;
+          if (two) ++used1;
           ++pieces;
         }
         if (!ok) set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
@@ -468,70 +584,69 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---------------- softmax: one query row per thread -----------------------
     const int t = warp >> 2, r = tid & 127;
-    const int rt = r / p.g, rh = r % p.g;  // token of the tile, head of the group
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + L::kTmemO + t * D;
-    const float sl = p.scale_log2;
-    Walk w;
-    w.init(p, start);
-    uint32_t steps = 0, tiles = 0;  // of this tile; key tiles of the CTA
-    if (tid == 0) p.split[k].row0 = -1;
-    while (ok && w.next(p, k)) {
-      const Item it = w.it;
-      const int nk = w.t1 - w.t0;
-      if (tid == 0 && w.t0 == 0 && w.t1 < it.nt) {
-        SplitItem si;
-        si.tokens = it.tokens;
-        si.head = w.ph;
-        // the item goes on in the next CTAs: those up to its last key tile's
-        const long long q = cut[1], rr = cut[2], big = rr * (q + 1);
-        const long long last = cut[0] - w.left + (it.nt - w.t1) - 1;
-        si.parts = static_cast<int>(last < big ? last / (q + 1) : rr + (last - big) / max(q, 1ll)) - k + 1;
-        si.slot = w.slot;
-        si.row0 = w.prow0;
-        p.split[k] = si;
-      }
-      if (it.tokens <= t * tt) {  // no row in this tile
+    uint32_t steps = 0, tiles = 0;  // P V products of this tile; key tiles of the CTA
+    for (uint32_t n = 0;; ++n) {
+      ok = __all_sync(0xffffffffu, piece_ready(n));
+      if (!ok) break;
+      const Piece& q = ring[n % kPieces];  // read until this warp hands it back
+      const int nk = q.nk;
+      if (nk < 0) break;
+      if (q.tokens <= t * tt) {  // no row in this tile
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_taken(n % kPieces));
         tiles += nk;
         continue;
       }
-      const int j = t * tt + rt;  // token of the item
-      const bool real = rt < tt && j < it.tokens;
-      const int pos = it.p0 + j;
-      const int pfirst = it.p0 + t * tt, plast = pfirst + tt - 1;
+      const int pos = q.p0 + t * tt + r / p.g;  // this row's token
       float m = -INFINITY, l = 0.f, lr = 0.f;
-      for (int i = w.t0; i < w.t1; ++i) {
-        const int k0 = key_tile(it, i) * kBN;
+      for (int i = 0; i < nk; ++i) {
+        const int ti = q.t0 + i;
+        const int k0 = (ti < q.ns ? ti : q.w0 + ti - q.ns) * kBN;
         ok = __all_sync(0xffffffffu, mbar_wait(b_sfull(t), steps & 1));
         if (!ok) break;
         tc_fence_after();
         float s[kBN];
 #pragma unroll
         for (int c = 0; c < kBN; c += 32) tmem_ld32(tS + c, reinterpret_cast<uint32_t*>(s) + c);
-        tmem_wait_ld();
         const uint32_t bad = bad_ring[tiles % kBadRing];
         // every row of the tile sees every key: no masks
-        const bool full = k0 + kBN - 1 <= pfirst && k0 + kBN <= it.khi && bad == 0u && sl > 0.f &&
+        const int pfirst = q.p0 + t * tt, plast = pfirst + tt - 1;
+        const bool full = k0 + kBN - 1 <= pfirst && k0 + kBN <= q.khi && bad == 0u && p.scale_log2 > 0.f &&
                           (p.window == 0 || k0 > plast - p.window || k0 + kBN <= p.sinks);
-        float f = sl;  // what the scores are still to be multiplied by
+        float f = p.scale_log2;  // what the scores are still to be multiplied by
+        tmem_wait_ld();
         float mx = -INFINITY;
         if (full) {
+          float mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < kBN; c += 2) mx = fmax3(mx, s[c], s[c + 1]);
-          mx *= sl;
-        } else {
-          f = 1.f;
-          const int first = (p.window > 0 && pos >= p.window) ? pos - p.window + 1 - k0 : 0;
-          const int end = min(pos + 1, it.khi) - k0, keep = p.sinks - k0;
-          const int shift = 31 - __clz(p.page_size);
-#pragma unroll
-          for (int c = 0; c < kBN; ++c) {
-            const bool vis = c < end && (c >= first || c < keep) && ((bad >> (c >> shift)) & 1u) == 0u;
-            s[c] = vis ? s[c] * sl : -INFINITY;
-            mx = fmaxf(mx, s[c]);
+          for (int c = 0; c < kBN; c += 8) {
+            mx = fmax3(mx, s[c], s[c + 1]);
+            mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
+            mx2 = fmax3(mx2, s[c + 4], s[c + 5]);
+            mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
           }
+          mx = fmaxf(fmaxf(mx, mx1), fmaxf(mx2, mx3)) * f;
+        } else {
+          const int first = (p.window > 0 && pos >= p.window) ? pos - p.window + 1 - k0 : 0;
+          const int end = min(pos + 1, q.khi) - k0, keep = p.sinks - k0;
+#pragma unroll
+          for (int c0 = 0; c0 < kBN; c0 += 32) {
+            uint32_t vis = ones(end - c0) & (~ones(first - c0) | ones(keep - c0));
+            if (bad != 0u) {
+              for (int c = 0; c < 32; c += p.page_size)
+                if ((bad >> ((c0 + c) / p.page_size)) & 1u) vis &= ~(ones(c + p.page_size) & ~ones(c));
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              s[c0 + c] = (vis >> c) & 1u ? s[c0 + c] * f : -INFINITY;
+              mx = fmaxf(mx, s[c0 + c]);
+            }
+          }
+          f = 1.f;
         }
-        if (i == w.t0) {
+        if (i == 0) {
           m = mx;
         } else if (__any_sync(0xffffffffu, mx > m + kSlack)) {
           ok = __all_sync(0xffffffffu, mbar_wait(b_pvdone(t), (steps - 1) & 1));
@@ -574,14 +689,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         // front of the window, behind the first tokens) may hold anything, and
         // 0 * NaN is NaN in the product: zero them once landed. Both tiles'
         // warps do, each before its own product.
-        const int mask = p.page_size - 1;
-        auto cuts_page = [&](int x) { return x > k0 && x < k0 + kBN && (x & mask) != 0; };
-        if (cuts_page(it.khi) || cuts_page(it.klo) || (it.klo > 0 && cuts_page(p.sinks))) {
+        auto cuts_page = [&](int x) { return x > k0 && x < k0 + kBN && (x & (p.page_size - 1)) != 0; };
+        if (cuts_page(q.khi) || cuts_page(q.klo) || (q.klo > 0 && cuts_page(p.sinks))) {
           const uint32_t vseq = 2 * tiles + 1;
           ok = __all_sync(0xffffffffu, mbar_wait(b_full(vseq % kRing), (vseq / kRing) & 1));
           if (!ok) break;
           const int key = k0 + r;
-          if (!(key < it.khi && (key >= it.klo || key < p.sinks))) {
+          if (!(key < q.khi && (key >= q.klo || key < p.sinks))) {
             unsigned char* v = smem + L::kOffKV + (vseq % kRing) * kTile + r * 128;
 #pragma unroll
             for (int a = 0; a < kAtoms; ++a)
@@ -607,8 +721,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       }
       const float inv = lr > 0.f ? 1.0f / lr : 0.f;
       const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
-      const int64_t row = static_cast<int64_t>(w.prow0 + j) * p.H_q + w.ph * p.g + rh;
-      const int64_t prow = static_cast<int64_t>(w.slot) * p.slot_rows + t * kBM + r;
+      const int rt = r / p.g, j = t * tt + rt;  // token of the tile, of the item
+      const bool real = rt < tt && j < q.tokens;
+      const int slot = q.slot;
+      const int64_t row = static_cast<int64_t>(q.row0 + j) * p.H_q + q.head * p.g + r % p.g;
+      const int64_t prow = static_cast<int64_t>(slot) * p.slot_rows + t * kBM + r;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_taken(n % kPieces));
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
         float o[32];
@@ -621,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         }
 #pragma unroll
         for (int x = 0; x < 32; ++x) o[x] *= inv;
-        if (real && w.slot < 0) {
+        if (real && slot < 0) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + c0);
 #pragma unroll
           for (int x = 0; x < 32; x += 8)
@@ -633,8 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           for (int x = 0; x < 32; x += 4) dst[x / 4] = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
         }
       }
-      if (real && w.slot >= 0) p.part_lse[prow] = lse2 * kLn2C;
-      if (real && w.slot < 0 && p.lse) p.lse[row] = lse2 * kLn2C;
+      if (real && slot >= 0) p.part_lse[prow] = lse2 * kLn2C;
+      if (real && slot < 0 && p.lse) p.lse[row] = lse2 * kLn2C;
       if (nk > 0) {
         tc_fence_before();
         __syncwarp();

@@ -19,10 +19,9 @@
 //
 // Inside a CTA (384 threads):
 //   warps 0-3, 4-7  softmax of tile 0 and tile 1, one query row per thread
-//   warp 8          TMA of K and V: one box per page and 64-column atom
+//   warps 8, 10     TMA of K and of V: one box per page and 64-column atom
 //   warp 9          issues the products
-//   warp 10         TMA of the queries
-//   warp 11         walks the range and hands its pieces to the others
+//   warp 11         walks the range, hands its pieces to the others, loads queries
 // S = Q K^T goes to TMEM (128 columns a tile); the softmax takes its row into
 // registers and writes P, as bf16, over the front half of the same columns,
 // where it is the A operand of O += P V. Products of one thread complete in
@@ -105,6 +104,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+
+// True for one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 
 // The lowest n bits (none below 0, all from 32 on).
@@ -364,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         w.init(p, start);
         p.split[k].row0 = -1;
         bool more = true;
+        uint32_t pieces = 0;  // with queries
         for (uint32_t n = 0; more; ++n) {
           Piece q;
           int rest = 0;
@@ -375,6 +386,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           }
           ring[n % kPieces] = q;
           mbar_arrive(b_piece(n % kPieces));
+          if (q.nk > 0) {  // its queries, once the products have read the last piece's
+            if (pieces > 0 && !mbar_wait(b_qempty, (pieces - 1) & 1)) {
+              set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
+              mbar_wait(b_qfull, (pieces - 1) & 1);  // a copy in flight lands first
+              break;
+            }
+            const int nq = q.tokens > tt ? 2 : 1;
+            mbar_arrive_expect_tx(b_qfull, nq * kAtoms * tt * p.g * 128);
+            for (int t2 = 0; t2 < nq; ++t2)
+              for (int a = 0; a < kAtoms; ++a)
+                tma_load_3d(sQ + t2 * kTile + a * kAtom, &qmap, a * 64, q.head * p.g, q.row0 + t2 * tt, b_qfull);
+            ++pieces;
+          }
           if (more && rest > 0) {  // its last key tile lies `rest` units behind this CTA's range
             const long long qu = cut[1], r = cut[2], big = r * (qu + 1), last = cut[0] + rest - 1;
             SplitItem si;
@@ -387,12 +411,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           }
         }
       }
-    } else if (warp == 8) {
-      // ---------------- K and V: lane i holds page i of the key tile --------
+    } else if (warp != 9) {
+      // ---------------- K (warp 8) and V (warp 10): lane i holds page i of the key tile
+      const bool is_v = warp == 10;
+      const CUtensorMap* map = is_v ? &vmap : &kmap;
       const int npg = kBN / p.page_size;
       const int oob = p.num_pages * p.page_size;  // a row past the pool: zero fill
-      uint32_t seq = 0, tiles = 0;                // K and V tiles issued; key tiles
-      uint32_t s = 0, phase = 1;                  // ring slot of the next one, and its last use's phase
+      uint32_t tiles = 0;                         // key tiles loaded; K of tile j is tile 2 j of the ring, V 2 j + 1
       for (uint32_t n = 0;; ++n) {
         ok = __all_sync(0xffffffffu, piece_ready(n));
         if (!ok) break;
@@ -415,37 +440,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           bad = __ballot_sync(0xffffffffu, wrong);
           return row;
         };
-        auto load_tile = [&](const CUtensorMap* map, int row) {
-          bool good = true;
-          if (lane == 0 && seq >= kRing) good = mbar_wait(b_empty(s), phase);
-          good = __shfl_sync(0xffffffffu, good, 0);
-          if (!good) return false;
-          if (lane == 0) mbar_arrive_expect_tx(b_full(s), kTile);
-          __syncwarp();
-          const int boxes = npg * kAtoms;
-          const int pg = lane / kAtoms, a = lane % kAtoms;
-          const int r = __shfl_sync(0xffffffffu, row, pg);
-          if (lane < boxes)
-            tma_load_3d(sKV + s * kTile + a * kAtom + pg * p.page_size * 128, map, a * 64, r, q.head, b_full(s));
-          ++seq;
-          if (++s == kRing) {
-            s = 0;
-            phase ^= 1;
-          }
-          return true;
-        };
         const int t1 = q.t0 + q.nk;
         uint32_t bad = 0;
         int row = q.nk > 0 ? page_row(q.t0, bad) : oob;
-        for (int i = q.t0; i < t1 && ok; ++i) {
+        for (int i = q.t0; i < t1; ++i) {
           uint32_t bad_next = 0;
           const int row_next = i + 1 < t1 ? page_row(i + 1, bad_next) : oob;
-          if (lane == 0) {
+          if (lane == 0 && !is_v) {
             bad_ring[tiles % kBadRing] = bad;
             if (bad) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
           }
+          const uint32_t seq = 2 * tiles + (is_v ? 1 : 0), s = seq % kRing;
+          if (seq >= kRing) {
+            ok = __all_sync(0xffffffffu, mbar_wait(b_empty(s), (seq / kRing - 1) & 1));
+            if (!ok) break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(b_full(s), kTile);
+          __syncwarp();
+          const int pg = lane / kAtoms, a = lane % kAtoms;
+          const int r = __shfl_sync(0xffffffffu, row, pg);
+          if (lane < npg * kAtoms)
+            tma_load_3d(sKV + s * kTile + a * kAtom + pg * p.page_size * 128, map, a * 64, r, q.head, b_full(s));
           ++tiles;
-          ok = load_tile(&kmap, row) && load_tile(&vmap, row);
           row = row_next;
           bad = bad_next;
         }
@@ -454,131 +470,124 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       if (!ok && lane == 0) {
         set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
         // let the copies in flight land before the CTA's shared memory goes
-        for (uint32_t i = seq > kRing ? seq - kRing : 0; i < seq; ++i) mbar_wait(b_full(i % kRing), (i / kRing) & 1);
-      }
-    } else if (warp == 10) {
-      // ---------------- queries ---------------------------------------------
-      if (lane == 0) {
-        uint32_t pieces = 0;
-        for (uint32_t n = 0;; ++n) {
-          ok = piece_ready(n);
-          if (!ok) break;
-          const Piece& q = ring[n % kPieces];
-          const int nk = q.nk, tokens = q.tokens, row0 = q.row0, head = q.head;
-          mbar_arrive(b_taken(n % kPieces));
-          if (nk < 0) break;
-          if (nk == 0) continue;
-          ok = pieces == 0 || mbar_wait(b_qempty, (pieces - 1) & 1);
-          if (!ok) break;
-          const int nq = tokens > tt ? 2 : 1;
-          mbar_arrive_expect_tx(b_qfull, nq * kAtoms * tt * p.g * 128);
-          for (int t = 0; t < nq; ++t)
-            for (int a = 0; a < kAtoms; ++a)
-              tma_load_3d(sQ + t * kTile + a * kAtom, &qmap, a * 64, head * p.g, row0 + t * tt, b_qfull);
-          ++pieces;
-        }
-        if (!ok) {
-          set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
-          if (pieces > 0) mbar_wait(b_qfull, (pieces - 1) & 1);  // a copy in flight lands first
+        for (uint32_t i = tiles > kRing ? tiles - kRing : 0; i < tiles; ++i) {
+          const uint32_t seq = 2 * i + (is_v ? 1 : 0);
+          mbar_wait(b_full(seq % kRing), (seq / kRing) & 1);
         }
       }
     } else if (warp == 9) {
       // ---------------- products --------------------------------------------
-      if (lane == 0) {
-        constexpr uint32_t iS = idesc_bf16(kBM, kBN, 0);
-        constexpr uint32_t iO = idesc_bf16(kBM, D, 1);
-        // descriptors of the first Q and ring tile; others differ by an address
-        // difference in 16-byte units, which stays within the address field
-        const uint64_t dQ = desc_sw128(sQ), dK = desc_sw128(sKV), dV = desc_sw128(sKV, kAtom, 1024);
-        constexpr uint64_t kTileStep = kTile >> 4;
-        uint32_t slot = 0, phase = 0;  // of the next K or V tile to wait for
-        uint32_t pieces = 0, steps0 = 0, steps1 = 0, used0 = 0, used1 = 0;
-        auto wait_next = [&]() {  // the next K or V tile has landed
-          const bool good = mbar_wait(b_full(slot), phase);
-          tc_fence_after();
-          return good;
-        };
-        auto advance = [&]() {
-          const uint32_t s = slot;
-          if (++slot == kRing) {
-            slot = 0;
-            phase ^= 1;
-          }
-          return s;
-        };
-        auto issue_s = [&](int t, uint32_t ks_slot) {
-          const uint64_t q = dQ + t * kTileStep, kb = dK + ks_slot * kTileStep;
+      // The whole warp runs this code and one elected lane issues: descriptors
+      // and loop counts stay in uniform registers, as the instruction wants
+      // them. (Run by one lane in a branch of its own, every product moved its
+      // operands there first and took 119 cycles instead of 64.)
+      constexpr uint32_t iS = idesc_bf16(kBM, kBN, 0);
+      constexpr uint32_t iO = idesc_bf16(kBM, D, 1);
+      // descriptors of the first Q and ring tile; others differ by an address
+      // difference in 16-byte units, which stays within the address field
+      const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t dQ = desc_sw128(sQ), dK = desc_sw128(sKV), dV = desc_sw128(sKV, kAtom, 1024);
+      constexpr uint64_t kTileStep = kTile >> 4;
+      uint32_t slot = 0, phase = 0;  // of the next K or V tile to wait for
+      uint32_t pieces = 0, steps0 = 0, steps1 = 0, used0 = 0, used1 = 0;
+      auto wait_next = [&]() {  // the next K or V tile has landed
+        const bool good = mbar_wait(b_full(slot), phase);
+        tc_fence_after();
+        return good;
+      };
+      auto advance = [&]() {
+        const uint32_t s = slot;
+        if (++slot == kRing) {
+          slot = 0;
+          phase ^= 1;
+        }
+        return s;
+      };
+      auto issue_s = [&](int t, uint32_t ks_slot) {
+        const uint64_t q = dQ + t * kTileStep, kb = dK + ks_slot * kTileStep;
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             constexpr uint64_t kAtomStep = kAtom >> 4;
             const uint64_t off = (ks >> 2) * kAtomStep + (ks & 3) * 2;
-            mma_bf16(tmem + t * 128, q + off, kb + off, iS, ks > 0);
+            mma_bf16(utmem + t * 128, q + off, kb + off, iS, ks > 0);
           }
           mma_commit(b_sfull(t));
           // the arrival carries what the key tile's barrier carried here: the
           // softmax reads the tile's bad-page mask after it
           mbar_arrive(b_sfull(t));
-        };
-        auto issue_pv = [&](int t, uint32_t v_slot, bool first) {
-          tc_fence_after();
-          const uint64_t vb = dV + v_slot * kTileStep;
+        }
+        __syncwarp();
+      };
+      auto issue_pv = [&](int t, uint32_t v_slot, uint32_t add) {
+        tc_fence_after();
+        const uint64_t vb = dV + v_slot * kTileStep;
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < kBN / 16; ++ks)
-            mma_bf16_tmem_a(tmem + L::kTmemO + t * D, tmem + t * 128 + ks * 8, vb + ks * 128, iO,
-                            (!first || ks > 0) ? 1u : 0u);
+            mma_bf16_tmem_a(utmem + L::kTmemO + t * D, utmem + t * 128 + ks * 8, vb + ks * 128, iO,
+                            ks > 0 ? 1u : add);
           mma_commit(b_pvdone(t));
-        };
-        for (uint32_t n = 0;; ++n) {
-          ok = piece_ready(n);
-          if (!ok) break;
-          const int nk = ring[n % kPieces].nk;
-          const bool two = ring[n % kPieces].tokens > tt;
-          mbar_arrive(b_taken(n % kPieces));
-          if (nk < 0) break;
-          if (nk == 0) continue;
-          ok = mbar_wait(b_qfull, pieces & 1) && wait_next();
-          if (!ok) break;
-          uint32_t ks_slot = advance();
-          issue_s(0, ks_slot);
-          if (two) issue_s(1, ks_slot);
-          mma_commit(b_empty(ks_slot));
-          if (nk == 1) mma_commit(b_qempty);
-          for (int i = 0; i < nk; ++i) {
-            const bool more = i + 1 < nk;
-            ok = mbar_wait(b_pfull(0), steps0 & 1) && wait_next();
-            if (ok && i == 0 && used0 > 0) ok = mbar_wait(b_ofree(0), (used0 - 1) & 1);
-            if (!ok) break;
-            const uint32_t v_slot = advance();
-            ++steps0;
-            issue_pv(0, v_slot, i == 0);
-            if (!two) mma_commit(b_empty(v_slot));
-            if (more) {
-              ok = wait_next();
-              if (!ok) break;
-              ks_slot = advance();
-              issue_s(0, ks_slot);
-            }
-            if (two) {
-              ok = mbar_wait(b_pfull(1), steps1 & 1);
-              if (ok && i == 0 && used1 > 0) ok = mbar_wait(b_ofree(1), (used1 - 1) & 1);
-              if (!ok) break;
-              ++steps1;
-              issue_pv(1, v_slot, i == 0);
-              mma_commit(b_empty(v_slot));
-              if (more) issue_s(1, ks_slot);
-            }
-            if (more) {
-              mma_commit(b_empty(ks_slot));
-              if (i + 2 == nk) mma_commit(b_qempty);
-            }
-          }
-          if (!ok) break;
-          ++used0;
-          if (two) ++used1;
-          ++pieces;
         }
-        if (!ok) set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
+        __syncwarp();
+      };
+      auto commit = [&](uint32_t bar) {
+        if (elect_one()) mma_commit(bar);
+        __syncwarp();
+      };
+      for (uint32_t n = 0;; ++n) {
+        ok = __all_sync(0xffffffffu, piece_ready(n));
+        if (!ok) break;
+        const int nk = __shfl_sync(0xffffffffu, ring[n % kPieces].nk, 0);
+        const bool two = __all_sync(0xffffffffu, ring[n % kPieces].tokens > tt);
+        if (lane == 0) mbar_arrive(b_taken(n % kPieces));
+        __syncwarp();
+        if (nk < 0) break;
+        if (nk == 0) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(b_qfull, pieces & 1) && wait_next());
+        if (!ok) break;
+        uint32_t ks_slot = advance();
+        issue_s(0, ks_slot);
+        if (two) issue_s(1, ks_slot);
+        commit(b_empty(ks_slot));
+        if (nk == 1) commit(b_qempty);
+        for (int i = 0; i < nk; ++i) {
+          const bool more = i + 1 < nk;
+          bool good = mbar_wait(b_pfull(0), steps0 & 1) && wait_next();
+          if (good && i == 0 && used0 > 0) good = mbar_wait(b_ofree(0), (used0 - 1) & 1);
+          ok = __all_sync(0xffffffffu, good);
+          if (!ok) break;
+          const uint32_t v_slot = advance();
+          ++steps0;
+          issue_pv(0, v_slot, i > 0 ? 1u : 0u);
+          if (!two) commit(b_empty(v_slot));
+          if (more) {
+            ok = __all_sync(0xffffffffu, wait_next());
+            if (!ok) break;
+            ks_slot = advance();
+            issue_s(0, ks_slot);
+          }
+          if (two) {
+            good = mbar_wait(b_pfull(1), steps1 & 1);
+            if (good && i == 0 && used1 > 0) good = mbar_wait(b_ofree(1), (used1 - 1) & 1);
+            ok = __all_sync(0xffffffffu, good);
+            if (!ok) break;
+            ++steps1;
+            issue_pv(1, v_slot, i > 0 ? 1u : 0u);
+            commit(b_empty(v_slot));
+            if (more) issue_s(1, ks_slot);
+          }
+          if (more) {
+            commit(b_empty(ks_slot));
+            if (i + 2 == nk) commit(b_qempty);
+          }
+        }
+        if (!ok) break;
+        ++used0;
+        if (two) ++used1;
+        ++pieces;
       }
+      if (!ok && lane == 0) set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));

@@ -64,7 +64,12 @@ struct Lay {
   static constexpr int kOffPieces = kOffBad + kBadRing * 4;
   static constexpr int kOffMisc = kOffPieces + 4 * 48;
   static constexpr int kSmem = kOffMisc + 128 + 12 * 8;
-  static constexpr uint32_t kTmemO = 256;  // S of tile t at 128 t, O of tile t at 256 + D t
+  // TMEM columns of tile t: S at 128 t, O at 256 + D t. P (64 columns) goes over
+  // the front of S at D = 128, where all 512 columns are taken, and has its own
+  // place at D = 64: the next S product then need not wait for P V.
+  static constexpr uint32_t kTmemO = 256;
+  static constexpr bool kOwnP = D == 64;
+  static constexpr uint32_t kTmemP = kOwnP ? 256 + 2 * D : 0, kTmemPStep = kOwnP ? 64 : 128;
 };
 static_assert(Lay<128>::kSmem <= 227 * 1024, "shared memory");
 
@@ -258,13 +263,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
   auto b_full = [&](int s) { return smem_u32(&bars[s]); };
   auto b_empty = [&](int s) { return smem_u32(&bars[kRing + s]); };
   auto b_sfull = [&](int t) { return smem_u32(&bars[2 * kRing + t]); };
-  auto b_pfull = [&](int t) { return smem_u32(&bars[2 * kRing + 2 + t]); };
+  auto b_pfull = [&](int t, int half) { return smem_u32(&bars[2 * kRing + 18 + 2 * t + half]); };
+  auto b_sfree = [&](int t) { return smem_u32(&bars[2 * kRing + 2 + t]); };
   auto b_pvdone = [&](int t) { return smem_u32(&bars[2 * kRing + 4 + t]); };
   auto b_ofree = [&](int t) { return smem_u32(&bars[2 * kRing + 6 + t]); };
   const uint32_t b_qfull = smem_u32(&bars[2 * kRing + 8]), b_qempty = smem_u32(&bars[2 * kRing + 9]);
   auto b_piece = [&](int s) { return smem_u32(&bars[2 * kRing + 10 + s]); };
   auto b_taken = [&](int s) { return smem_u32(&bars[2 * kRing + 10 + kPieces + s]); };
-  static_assert((2 * kRing + 10 + 2 * kPieces) * 8 <= 320, "mbarriers fit their slot");
+  static_assert(kPieces == 4 && (2 * kRing + 22) * 8 <= 320, "mbarriers fit their slot");
   static_assert(kPieces * sizeof(Piece) == L::kOffMisc - L::kOffPieces, "piece ring");
   Piece* ring = reinterpret_cast<Piece*>(smem + L::kOffPieces);
   volatile uint32_t* bad_ring = reinterpret_cast<volatile uint32_t*>(smem + L::kOffBad);
@@ -280,7 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(b_sfull(t), 2);  // the products' commit and the issuer's own arrival
-      mbar_init(b_pfull(t), 4);
+      mbar_init(b_pfull(t, 0), 4);
+      mbar_init(b_pfull(t, 1), 4);
+      mbar_init(b_sfree(t), 4);
       mbar_init(b_pvdone(t), 1);
       mbar_init(b_ofree(t), 4);
     }
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     }
   }
   __syncthreads();
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0;  // all 512 columns: there is no other place for them
   const uint32_t sQ = smem_u32(smem + L::kOffQ), sKV = smem_u32(smem + L::kOffKV);
   pdl_wait_primary();
 
@@ -485,102 +493,111 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       constexpr uint32_t iO = idesc_bf16(kBM, D, 1);
       // descriptors of the first Q and ring tile; others differ by an address
       // difference in 16-byte units, which stays within the address field
-      const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
       const uint64_t dQ = desc_sw128(sQ), dK = desc_sw128(sKV), dV = desc_sw128(sKV, kAtom, 1024);
       constexpr uint64_t kTileStep = kTile >> 4;
-      uint32_t slot = 0, phase = 0;  // of the next K or V tile to wait for
-      uint32_t pieces = 0, steps0 = 0, steps1 = 0, used0 = 0, used1 = 0;
-      auto wait_next = [&]() {  // the next K or V tile has landed
-        const bool good = mbar_wait(b_full(slot), phase);
+      uint32_t seq = 0;     // K tile of the current step in the ring (V: the one after it)
+      uint32_t pieces = 0;  // with products
+      uint32_t sn0 = 0, sn1 = 0, pn0 = 0, pn1 = 0, used0 = 0, used1 = 0;  // S, P V products, pieces of each tile
+      auto landed = [&](uint32_t x) { return mbar_wait(b_full(x % kRing), (x / kRing) & 1); };
+      // S of tile t from ring tile x; `last`: no other product reads it, `q_last`: nor the queries
+      auto issue_s = [&](int t, uint32_t x, bool last, bool q_last) {
+        const uint64_t q = dQ + t * kTileStep, kb = dK + (x % kRing) * kTileStep;
         tc_fence_after();
-        return good;
-      };
-      auto advance = [&]() {
-        const uint32_t s = slot;
-        if (++slot == kRing) {
-          slot = 0;
-          phase ^= 1;
-        }
-        return s;
-      };
-      auto issue_s = [&](int t, uint32_t ks_slot) {
-        const uint64_t q = dQ + t * kTileStep, kb = dK + ks_slot * kTileStep;
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             constexpr uint64_t kAtomStep = kAtom >> 4;
             const uint64_t off = (ks >> 2) * kAtomStep + (ks & 3) * 2;
-            mma_bf16(utmem + t * 128, q + off, kb + off, iS, ks > 0);
+            mma_bf16(t * 128, q + off, kb + off, iS, ks > 0);
           }
           mma_commit(b_sfull(t));
           // the arrival carries what the key tile's barrier carried here: the
           // softmax reads the tile's bad-page mask after it
           mbar_arrive(b_sfull(t));
+          if (last) mma_commit(b_empty(x % kRing));
+          if (q_last) mma_commit(b_qempty);
         }
         __syncwarp();
       };
-      auto issue_pv = [&](int t, uint32_t v_slot, uint32_t add) {
+      // half of P V of tile t (64 keys), V in ring tile x; `last` as above
+      auto issue_pv = [&](int t, int half, uint32_t x, uint32_t add, bool last) {
+        const uint64_t vb = dV + (x % kRing) * kTileStep + half * 512;
         tc_fence_after();
-        const uint64_t vb = dV + v_slot * kTileStep;
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < kBN / 16; ++ks)
-            mma_bf16_tmem_a(utmem + L::kTmemO + t * D, utmem + t * 128 + ks * 8, vb + ks * 128, iO,
+          for (int ks = 0; ks < kBN / 32; ++ks)
+            mma_bf16_tmem_a(L::kTmemO + t * D, L::kTmemP + t * L::kTmemPStep + half * 32 + ks * 8, vb + ks * 128, iO,
                             ks > 0 ? 1u : add);
-          mma_commit(b_pvdone(t));
+          if (half == 1) mma_commit(b_pvdone(t));
+          if (last) mma_commit(b_empty(x % kRing));
         }
         __syncwarp();
       };
-      auto commit = [&](uint32_t bar) {
-        if (elect_one()) mma_commit(bar);
-        __syncwarp();
-      };
+      // S may be overwritten once the softmax has read it (with P over it: once
+      // P V is issued, which it is by then)
+      auto s_free = [&](int t, uint32_t sn) { return !L::kOwnP || sn == 0 || mbar_wait(b_sfree(t), (sn - 1) & 1); };
       for (uint32_t n = 0;; ++n) {
         ok = __all_sync(0xffffffffu, piece_ready(n));
         if (!ok) break;
-        const int nk = __shfl_sync(0xffffffffu, ring[n % kPieces].nk, 0);
-        const bool two = __all_sync(0xffffffffu, ring[n % kPieces].tokens > tt);
+        // a reduction's result is known to be the same in all lanes
+        const int nk = __reduce_max_sync(0xffffffffu, ring[n % kPieces].nk);
+        const bool two = __reduce_max_sync(0xffffffffu, ring[n % kPieces].tokens) > tt;
         if (lane == 0) mbar_arrive(b_taken(n % kPieces));
         __syncwarp();
         if (nk < 0) break;
         if (nk == 0) continue;
-        ok = __all_sync(0xffffffffu, mbar_wait(b_qfull, pieces & 1) && wait_next());
+        ok = __all_sync(0xffffffffu, mbar_wait(b_qfull, pieces & 1) && landed(seq) && s_free(0, sn0));
         if (!ok) break;
-        uint32_t ks_slot = advance();
-        issue_s(0, ks_slot);
-        if (two) issue_s(1, ks_slot);
-        commit(b_empty(ks_slot));
-        if (nk == 1) commit(b_qempty);
-        for (int i = 0; i < nk; ++i) {
-          const bool more = i + 1 < nk;
-          bool good = mbar_wait(b_pfull(0), steps0 & 1) && wait_next();
-          if (good && i == 0 && used0 > 0) good = mbar_wait(b_ofree(0), (used0 - 1) & 1);
-          ok = __all_sync(0xffffffffu, good);
+        issue_s(0, seq, !two, !two && nk == 1);
+        ++sn0;
+        if (two) {
+          ok = __all_sync(0xffffffffu, s_free(1, sn1));
           if (!ok) break;
-          const uint32_t v_slot = advance();
-          ++steps0;
-          issue_pv(0, v_slot, i > 0 ? 1u : 0u);
-          if (!two) commit(b_empty(v_slot));
-          if (more) {
-            ok = __all_sync(0xffffffffu, wait_next());
-            if (!ok) break;
-            ks_slot = advance();
-            issue_s(0, ks_slot);
+          issue_s(1, seq, true, nk == 1);
+          ++sn1;
+        }
+        for (int i = 0; i < nk; ++i) {
+          const bool more = i + 1 < nk, q_last = i + 2 == nk;
+          const uint32_t add = i > 0 ? 1u : 0u;
+          bool good = landed(seq + 1) && (!more || landed(seq + 2));
+          if (i == 0) {  // O of the last piece has been read
+            if (used0 > 0) good = good && mbar_wait(b_ofree(0), (used0 - 1) & 1);
+            if (two && used1 > 0) good = good && mbar_wait(b_ofree(1), (used1 - 1) & 1);
           }
+          if constexpr (L::kOwnP) {
+            if (more) {
+              ok = __all_sync(0xffffffffu, good && s_free(0, sn0));
+              if (!ok) break;
+              issue_s(0, seq + 2, !two, !two && q_last);
+              ++sn0;
+              if (two) {
+                good = s_free(1, sn1);
+                ok = __all_sync(0xffffffffu, good);
+                if (!ok) break;
+                issue_s(1, seq + 2, true, q_last);
+                ++sn1;
+              }
+            }
+          }
+          ok = __all_sync(0xffffffffu, good && mbar_wait(b_pfull(0, 0), pn0 & 1));
+          if (!ok) break;
+          issue_pv(0, 0, seq + 1, add, false);
+          ok = __all_sync(0xffffffffu, mbar_wait(b_pfull(0, 1), pn0 & 1));
+          if (!ok) break;
+          issue_pv(0, 1, seq + 1, 1u, !two);
+          ++pn0;
+          if (!L::kOwnP && more) issue_s(0, seq + 2, !two, !two && q_last);
           if (two) {
-            good = mbar_wait(b_pfull(1), steps1 & 1);
-            if (good && i == 0 && used1 > 0) good = mbar_wait(b_ofree(1), (used1 - 1) & 1);
-            ok = __all_sync(0xffffffffu, good);
+            ok = __all_sync(0xffffffffu, mbar_wait(b_pfull(1, 0), pn1 & 1));
             if (!ok) break;
-            ++steps1;
-            issue_pv(1, v_slot, i > 0 ? 1u : 0u);
-            commit(b_empty(v_slot));
-            if (more) issue_s(1, ks_slot);
+            issue_pv(1, 0, seq + 1, add, false);
+            ok = __all_sync(0xffffffffu, mbar_wait(b_pfull(1, 1), pn1 & 1));
+            if (!ok) break;
+            issue_pv(1, 1, seq + 1, 1u, true);
+            ++pn1;
+            if (!L::kOwnP && more) issue_s(1, seq + 2, true, q_last);
           }
-          if (more) {
-            commit(b_empty(ks_slot));
-            if (i + 2 == nk) commit(b_qempty);
-          }
+          seq += 2;
         }
         if (!ok) break;
         ++used0;
@@ -595,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + L::kTmemO + t * D;
+    const uint32_t tP = tmem + lanes + L::kTmemP + t * L::kTmemPStep;
     uint32_t steps = 0, tiles = 0;  // P V products of this tile; key tiles of the CTA
     for (uint32_t n = 0;; ++n) {
       ok = __all_sync(0xffffffffu, piece_ready(n));
@@ -609,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         continue;
       }
       const int pos = q.p0 + t * tt + r / p.g;  // this row's token
-      float m = -INFINITY, l = 0.f, lr = 0.f;
+      float m = -INFINITY, l = 0.f;
       for (int i = 0; i < nk; ++i) {
         const int ti = q.t0 + i;
         const int k0 = (ti < q.ns ? ti : q.w0 + ti - q.ns) * kBN;
@@ -626,6 +644,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
                           (p.window == 0 || k0 > plast - p.window || k0 + kBN <= p.sinks);
         float f = p.scale_log2;  // what the scores are still to be multiplied by
         tmem_wait_ld();
+        if constexpr (L::kOwnP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_sfree(t));
+        }
         float mx = -INFINITY;
         if (full) {
           float mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
@@ -665,7 +688,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           const float alpha = m == -INFINITY ? 0.f : fast_exp2(m - mnew);
           m = mnew;
           l *= alpha;
-          lr *= alpha;
 #pragma unroll
           for (int c0 = 0; c0 < D; c0 += 16) {
             uint32_t u[16];
@@ -676,24 +698,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
             tmem_st16(tO + c0, u);
           }
         }
-        const float ms = m == -INFINITY ? 0.f : m;
-        const float2 f2 = make_float2(f, f), nm = make_float2(-ms, -ms);
-        float2 l2 = make_float2(0.f, 0.f), lr2 = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c0 = 0; c0 < kBN; c0 += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 x = __ffma2_rn(make_float2(s[c0 + c], s[c0 + c + 1]), f2, nm);
-            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            pk[c / 2] = float2_to_bf16x2(e.x, e.y);
-            l2 = __fadd2_rn(l2, e);
-            lr2 = __fadd2_rn(lr2, bf16x2_to_float2(pk[c / 2]));
-          }
-          tmem_st16(tS + c0 / 2, pk);
-        }
-        l += l2.x + l2.y;
-        lr += lr2.x + lr2.y;
         // Rows of a loaded page that no row sees (past the sequence's end, in
         // front of the window, behind the first tokens) may hold anything, and
         // 0 * NaN is NaN in the product: zero them once landed. Both tiles'
@@ -714,10 +718,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           }
           fence_async_smem();
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b_pfull(t));
+        if (L::kOwnP && steps > 0) {  // P V has read the last P
+          ok = __all_sync(0xffffffffu, mbar_wait(b_pvdone(t), (steps - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const float ms = m == -INFINITY ? 0.f : m;
+        const float2 f2 = make_float2(f, f), nm = make_float2(-ms, -ms);
+        float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c0 = 0; c0 < kBN; c0 += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 x = __ffma2_rn(make_float2(s[c0 + c], s[c0 + c + 1]), f2, nm);
+            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            pk[c / 2] = float2_to_bf16x2(e.x, e.y);
+            l2 = __fadd2_rn(l2, e);
+          }
+          tmem_st16(tP + c0 / 2, pk);
+          if (c0 == 32 || c0 == 96) {  // half of P is there: its product may start
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_pfull(t, c0 / 64));
+          }
+        }
+        l += l2.x + l2.y;
         ++steps;
         ++tiles;
       }
@@ -728,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         if (!ok) break;
         tc_fence_after();
       }
-      const float inv = lr > 0.f ? 1.0f / lr : 0.f;
+      const float inv = l > 0.f ? 1.0f / l : 0.f;
       const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
       const int rt = r / p.g, j = t * tt + rt;  // token of the tile, of the item
       const bool real = rt < tt && j < q.tokens;

@@ -60,16 +60,17 @@ struct Lay {
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = 2 * kTileBytes;
   static constexpr int kOffBar = kOffKV + kRing * kTileBytes;
-  static constexpr int kOffBad = kOffBar + 320;
+  static constexpr int kOffBad = kOffBar + 384;
   static constexpr int kOffPieces = kOffBad + kBadRing * 4;
   static constexpr int kOffMisc = kOffPieces + 4 * 48;
-  static constexpr int kSmem = kOffMisc + 128 + 12 * 8;
-  // TMEM columns of tile t: S at 128 t, O at 256 + D t. P (64 columns) goes over
-  // the front of S at D = 128, where all 512 columns are taken, and has its own
-  // place at D = 64: the next S product then need not wait for P V.
-  static constexpr uint32_t kTmemO = 256;
-  static constexpr bool kOwnP = D == 64;
-  static constexpr uint32_t kTmemP = kOwnP ? 256 + 2 * D : 0, kTmemPStep = kOwnP ? 64 : 128;
+  static constexpr int kSmem = kOffMisc + 64 + 12 * 8;
+  // TMEM: kBufs score buffers of 128 columns taken in turn by the products of
+  // both tiles, then O of tile 0 and of tile 1. P goes over the front half of
+  // its scores. A third buffer (head dim 64 leaves the columns) lets a tile's
+  // next scores be computed before its P V.
+  static constexpr int kBufs = D == 128 ? 2 : 3;
+  static constexpr uint32_t kTmemO = kBufs * 128;
+  static_assert(kTmemO + 2 * D <= 512, "TMEM columns");
 };
 static_assert(Lay<128>::kSmem <= 227 * 1024, "shared memory");
 
@@ -96,7 +97,7 @@ struct PrefillParams {
   float scale_log2;
   uint32_t* err_word;
   SplitItem* split;  // [CTAs]
-  float* part_o;     // [2 * CTAs, slot_rows, D]
+  float* part_o;     // [2 * CTAs, D / 4, slot_rows, 4]: neighbouring rows (threads) write neighbouring places
   float* part_lse;   // [2 * CTAs, slot_rows]
 };
 
@@ -109,6 +110,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 // True for one lane of a converged warp.
@@ -163,6 +168,33 @@ __device__ __forceinline__ Item load_item(const PrefillParams& p, const Seq& s, 
   return it;
 }
 
+// a / b of non-negative numbers, in 32 bits where they fit.
+__device__ __forceinline__ long long div_units(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// Four lanes hold one row each, as four 16-byte chunks; afterwards lane i of
+// the four holds chunk i of the four rows. A store of the result then covers
+// 64 contiguous bytes of eight rows instead of 16 bytes of 32 rows.
+__device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane) {
+  auto swap = [&](uint4& keep_lo, uint4& keep_hi, int mask, bool hi) {
+    uint4 send = hi ? keep_lo : keep_hi;
+    send.x = __shfl_xor_sync(0xffffffffu, send.x, mask);
+    send.y = __shfl_xor_sync(0xffffffffu, send.y, mask);
+    send.z = __shfl_xor_sync(0xffffffffu, send.z, mask);
+    send.w = __shfl_xor_sync(0xffffffffu, send.w, mask);
+    if (hi)
+      keep_lo = send;
+    else
+      keep_hi = send;
+  };
+  swap(v[0], v[1], 1, lane & 1);
+  swap(v[2], v[3], 1, lane & 1);
+  swap(v[0], v[2], 2, lane & 2);
+  swap(v[1], v[3], 2, lane & 2);
+}
+
 // A piece of the CTA's range: key tiles [t0, t0 + nk) of one item. Warp 11
 // writes them to a ring in shared memory, ahead of the roles that read them.
 struct alignas(16) Piece {
@@ -183,14 +215,37 @@ struct Walk {
   Seq s;
   bool first;  // no piece returned yet
 
-  __device__ __forceinline__ void init(const PrefillParams& p, const int* start) {
-    left = start[4];
-    b = start[0];
-    h = start[1];
-    block = start[2];
-    rem = start[3];
+  // A whole warp finds the item: unit `off` of sequence b0, `n` units to walk.
+  __device__ __forceinline__ void init(const PrefillParams& p, int b0, long long off, int n, int lane) {
+    left = n;
+    b = b0;
     first = true;
-    if (left > 0) s = load_seq(p, b);
+    h = block = rem = 0;
+    if (n <= 0) return;
+    s = load_seq(p, b);
+    long long c = 0;  // units of one kv head
+    for (int i = lane; i < s.blocks; i += 32) c += load_item(p, s, i).nt + kItemUnits;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    h = static_cast<int>(div_units(off, c));
+    off -= h * c;
+    for (int base = 0; base < s.blocks; base += 32) {
+      const int mine = base + lane < s.blocks ? load_item(p, s, base + lane).nt + kItemUnits : 0;
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, off < incl);
+      if (hit != 0u) {
+        const int at = __ffs(hit) - 1;
+        block = base + at;
+        rem = static_cast<int>(off) - __shfl_sync(0xffffffffu, incl - mine, at);
+        return;
+      }
+      off -= __shfl_sync(0xffffffffu, incl, 31);
+    }
   }
   // The next piece; also whether the item goes on in later CTAs from its first
   // key tile here (then `rest` is the number of its key tiles there).
@@ -259,25 +314,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     if (tid == 0) set_device_error(p.err_word, TS_DEVERR_SMEM_ALIGN);
     return;
   }
+  constexpr int kBufs = L::kBufs;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
-  auto b_full = [&](int s) { return smem_u32(&bars[s]); };
-  auto b_empty = [&](int s) { return smem_u32(&bars[kRing + s]); };
-  auto b_sfull = [&](int t) { return smem_u32(&bars[2 * kRing + t]); };
-  auto b_pfull = [&](int t, int half) { return smem_u32(&bars[2 * kRing + 18 + 2 * t + half]); };
-  auto b_sfree = [&](int t) { return smem_u32(&bars[2 * kRing + 2 + t]); };
-  auto b_pvdone = [&](int t) { return smem_u32(&bars[2 * kRing + 4 + t]); };
-  auto b_ofree = [&](int t) { return smem_u32(&bars[2 * kRing + 6 + t]); };
-  const uint32_t b_qfull = smem_u32(&bars[2 * kRing + 8]), b_qempty = smem_u32(&bars[2 * kRing + 9]);
-  auto b_piece = [&](int s) { return smem_u32(&bars[2 * kRing + 10 + s]); };
-  auto b_taken = [&](int s) { return smem_u32(&bars[2 * kRing + 10 + kPieces + s]); };
-  static_assert(kPieces == 4 && (2 * kRing + 22) * 8 <= 320, "mbarriers fit their slot");
+  auto b_full = [&](int i) { return smem_u32(&bars[i]); };                 // K or V tile landed
+  auto b_empty = [&](int i) { return smem_u32(&bars[kRing + i]); };        // and no longer needed
+  // scores, weights of tile t's product number n (of the CTA's): kBufs barriers
+  // each in turn. They are a tile's own, so that a tile without rows in some
+  // pieces cannot see another's phases pass.
+  auto b_sfull = [&](int t, uint32_t n) { return smem_u32(&bars[2 * kRing + t * kBufs + n % kBufs]); };
+  auto b_pfull = [&](int t, uint32_t n) { return smem_u32(&bars[2 * kRing + (2 + t) * kBufs + n % kBufs]); };
+  auto buf_phase = [&](uint32_t n) { return (n / kBufs) & 1; };
+  constexpr int kBar0 = 2 * kRing + 4 * kBufs;
+  auto b_pvdone = [&](int t) { return smem_u32(&bars[kBar0 + t]); };     // O of tile t has its last P V
+  auto b_ofree = [&](int t) { return smem_u32(&bars[kBar0 + 2 + t]); };  // O of tile t has been read out
+  const uint32_t b_qfull = smem_u32(&bars[kBar0 + 4]), b_qempty = smem_u32(&bars[kBar0 + 5]);
+  auto b_piece = [&](int i) { return smem_u32(&bars[kBar0 + 6 + i]); };
+  auto b_taken = [&](int i) { return smem_u32(&bars[kBar0 + 6 + kPieces + i]); };
+  static_assert((kBar0 + 6 + 2 * kPieces) * 8 <= L::kOffBad - L::kOffBar, "mbarriers fit their place");
   static_assert(kPieces * sizeof(Piece) == L::kOffMisc - L::kOffPieces, "piece ring");
   Piece* ring = reinterpret_cast<Piece*>(smem + L::kOffPieces);
   volatile uint32_t* bad_ring = reinterpret_cast<volatile uint32_t*>(smem + L::kOffBad);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
-  int* start = reinterpret_cast<int*>(smem + L::kOffMisc + 16);
-  long long* cut = reinterpret_cast<long long*>(smem + L::kOffMisc + 64);  // the batch's cut: range end, q, r
-  long long* warp_tot = reinterpret_cast<long long*>(smem + L::kOffMisc + 128);
+  int* start_seq = reinterpret_cast<int*>(smem + L::kOffMisc + 16);
+  long long* start_off = reinterpret_cast<long long*>(smem + L::kOffMisc + 24);
+  long long* warp_tot = reinterpret_cast<long long*>(smem + L::kOffMisc + 64);
 
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
@@ -285,10 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       mbar_init(b_empty(i), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(b_sfull(t), 2);  // the products' commit and the issuer's own arrival
-      mbar_init(b_pfull(t, 0), 4);
-      mbar_init(b_pfull(t, 1), 4);
-      mbar_init(b_sfree(t), 4);
+      for (int i = 0; i < kBufs; ++i) {
+        mbar_init(b_sfull(t, i), 2);  // the products' commit and the issuer's own arrival
+        mbar_init(b_pfull(t, i), 4);
+      }
       mbar_init(b_pvdone(t), 1);
       mbar_init(b_ofree(t), 4);
     }
@@ -300,18 +360,38 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     }
     fence_mbar_init();
   }
+  if (warp == 8 && lane == 0) {
+    prefetch_map(&qmap);
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   if (warp == 0) tmem_alloc(smem_u32(tmem_slot), 512);
 
   // ---- prologue: this CTA's range of units --------------------------------
-  const int chunk = (p.B + kThreads - 1) / kThreads;
-  const int lo = min(p.B, tid * chunk), hi = min(p.B, lo + chunk);
-  auto seq_cost = [&](const Seq& s) {  // of one kv head
+  // Units of every sequence, by 32 lanes (up to 12 sequences), 8 (48) or one
+  // each, and their prefix sums over the threads; the sums of a sequence are
+  // kept in the K/V area, free until the first copy, for the search.
+  const int lps = p.B <= kThreads / 32 ? 32 : p.B <= kThreads / 8 ? 8 : 1;
+  const int chunk = (p.B + kThreads / lps - 1) / (kThreads / lps);
+  const int lo = min(p.B, tid / lps * chunk), hi = min(p.B, lo + chunk);
+  long long* kept = reinterpret_cast<long long*>(smem + L::kOffKV);
+  const bool keep = p.B <= 8192;  // 64 KB
+  auto seq_units = [&](int b, int first, int step) {
+    const Seq s = load_seq(p, b);
     long long c = 0;
-    for (int i = 0; i < s.blocks; ++i) c += load_item(p, s, i).nt + kItemUnits;
-    return c;
+    for (int i = first; i < s.blocks; i += step) c += load_item(p, s, i).nt + kItemUnits;
+    return c * p.H_kv;
   };
   long long mine = 0;
-  for (int b = lo; b < hi; ++b) mine += seq_cost(load_seq(p, b)) * p.H_kv;
+  for (int x = 0; x < chunk; ++x) {
+    const int b = lo + x;
+    long long c = b < hi ? seq_units(b, tid % lps, lps) : 0;
+    for (int o = lps / 2; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    if (tid % lps == 0 && b < hi) {
+      if (keep) kept[b] = c;
+      mine += c;
+    }
+  }
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -329,40 +409,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     total += v;
   }
   const long long excl = wbase + incl - mine;
-  const long long G = max(1ll, min(static_cast<long long>(gridDim.x), total / p.min_units));
-  const long long q_units = total / G, r_units = total % G;
+  const long long G = max(1ll, min(static_cast<long long>(gridDim.x), div_units(total, p.min_units)));
+  const long long q_units = div_units(total, G), r_units = total - q_units * G;
   const long long u0 = k < G ? k * q_units + min(static_cast<long long>(k), r_units) : total;
   const long long u1 = k < G ? u0 + q_units + (k < r_units ? 1 : 0) : total;
-  if (tid == 0) {
-    start[4] = static_cast<int>(u1 - u0);
-    cut[0] = u1;
-    cut[1] = q_units;
-    cut[2] = r_units;
-  }
   if (u0 < u1 && excl <= u0 && u0 < excl + mine) {
     long long off = excl;
     for (int b = lo; b < hi; ++b) {
-      const Seq s = load_seq(p, b);
-      const long long c = seq_cost(s);
-      if (u0 < off + c * p.H_kv) {
-        int rem_h = static_cast<int>((u0 - off) / c);
-        long long rem = (u0 - off) - rem_h * c;
-        int i = 0;
-        while (true) {
-          const int ci = load_item(p, s, i).nt + kItemUnits;
-          if (rem < ci) break;
-          rem -= ci;
-          ++i;
-        }
-        start[0] = b;
-        start[1] = rem_h;
-        start[2] = i;
-        start[3] = static_cast<int>(rem);
+      const long long c = keep ? kept[b] : seq_units(b, 0, 1);
+      if (u0 < off + c) {
+        *start_seq = b;
+        *start_off = u0 - off;
         break;
       }
-      off += c * p.H_kv;
+      off += c;
     }
   }
+  fence_async_smem();  // the sums' place is written by copies next
   __syncthreads();
   constexpr uint32_t tmem = 0;  // all 512 columns: there is no other place for them
   const uint32_t sQ = smem_u32(smem + L::kOffQ), sKV = smem_u32(smem + L::kOffKV);
@@ -377,9 +440,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 11) {
       // ---------------- pieces ------------------------------------------------
+      Walk w;
+      w.init(p, *start_seq, *start_off, static_cast<int>(u1 - u0), lane);
       if (lane == 0) {
-        Walk w;
-        w.init(p, start);
         p.split[k].row0 = -1;
         bool more = true;
         uint32_t pieces = 0;  // with queries
@@ -408,11 +471,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
             ++pieces;
           }
           if (more && rest > 0) {  // its last key tile lies `rest` units behind this CTA's range
-            const long long qu = cut[1], r = cut[2], big = r * (qu + 1), last = cut[0] + rest - 1;
+            const long long big = r_units * (q_units + 1), last = u1 + rest - 1;
             SplitItem si;
             si.tokens = q.tokens;
             si.head = q.head;
-            si.parts = static_cast<int>(last < big ? last / (qu + 1) : r + (last - big) / max(qu, 1ll)) - k + 1;
+            si.parts =
+                static_cast<int>(last < big ? div_units(last, q_units + 1)
+                                            : r_units + div_units(last - big, max(q_units, 1ll))) - k + 1;
             si.slot = q.slot;
             si.row0 = q.row0;
             p.split[k] = si;
@@ -495,113 +560,99 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       // difference in 16-byte units, which stays within the address field
       const uint64_t dQ = desc_sw128(sQ), dK = desc_sw128(sKV), dV = desc_sw128(sKV, kAtom, 1024);
       constexpr uint64_t kTileStep = kTile >> 4;
-      uint32_t seq = 0;     // K tile of the current step in the ring (V: the one after it)
+      uint32_t seq = 0;     // ring tile of the piece's first K tile
       uint32_t pieces = 0;  // with products
-      uint32_t sn0 = 0, sn1 = 0, pn0 = 0, pn1 = 0, used0 = 0, used1 = 0;  // S, P V products, pieces of each tile
-      auto landed = [&](uint32_t x) { return mbar_wait(b_full(x % kRing), (x / kRing) & 1); };
-      // S of tile t from ring tile x; `last`: no other product reads it, `q_last`: nor the queries
-      auto issue_s = [&](int t, uint32_t x, bool last, bool q_last) {
+      uint32_t used0 = 0, used1 = 0;                  // pieces of each tile
+      uint32_t sn0 = 0, sn1 = 0, pn0 = 0, pn1 = 0;    // S and P V products of each tile
+      uint32_t sb = 0, pb = 0;                        // buffer of the next S, of the next P V
+      auto full_bar = [&](uint32_t x) { return b_full(x % kRing); };
+      auto full_phase = [&](uint32_t x) { return (x / kRing) & 1; };
+      // S of tile t from ring tile x into buffer sb (one lane)
+      auto issue_s = [&](int t, uint32_t x, bool k_last, bool q_last) {
         const uint64_t q = dQ + t * kTileStep, kb = dK + (x % kRing) * kTileStep;
-        tc_fence_after();
-        if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            constexpr uint64_t kAtomStep = kAtom >> 4;
-            const uint64_t off = (ks >> 2) * kAtomStep + (ks & 3) * 2;
-            mma_bf16(t * 128, q + off, kb + off, iS, ks > 0);
-          }
-          mma_commit(b_sfull(t));
-          // the arrival carries what the key tile's barrier carried here: the
-          // softmax reads the tile's bad-page mask after it
-          mbar_arrive(b_sfull(t));
-          if (last) mma_commit(b_empty(x % kRing));
-          if (q_last) mma_commit(b_qempty);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          constexpr uint64_t kAtomStep = kAtom >> 4;
+          const uint64_t off = (ks >> 2) * kAtomStep + (ks & 3) * 2;
+          mma_bf16(sb * 128, q + off, kb + off, iS, ks > 0);
         }
-        __syncwarp();
+        const uint32_t done = b_sfull(t, t == 0 ? sn0 : sn1);
+        mma_commit(done);
+        // the arrival carries what the key tile's barrier carried here: the
+        // softmax reads the tile's bad-page mask after it
+        mbar_arrive(done);
+        if (k_last) mma_commit(b_empty(x % kRing));
+        if (q_last) mma_commit(b_qempty);
       };
-      // half of P V of tile t (64 keys), V in ring tile x; `last` as above
-      auto issue_pv = [&](int t, int half, uint32_t x, uint32_t add, bool last) {
-        const uint64_t vb = dV + (x % kRing) * kTileStep + half * 512;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < kBN / 32; ++ks)
-            mma_bf16_tmem_a(L::kTmemO + t * D, L::kTmemP + t * L::kTmemPStep + half * 32 + ks * 8, vb + ks * 128, iO,
-                            ks > 0 ? 1u : add);
-          if (half == 1) mma_commit(b_pvdone(t));
-          if (last) mma_commit(b_empty(x % kRing));
-        }
-        __syncwarp();
-      };
-      // S may be overwritten once the softmax has read it (with P over it: once
-      // P V is issued, which it is by then)
-      auto s_free = [&](int t, uint32_t sn) { return !L::kOwnP || sn == 0 || mbar_wait(b_sfree(t), (sn - 1) & 1); };
       for (uint32_t n = 0;; ++n) {
         ok = __all_sync(0xffffffffu, piece_ready(n));
         if (!ok) break;
         // a reduction's result is known to be the same in all lanes
         const int nk = __reduce_max_sync(0xffffffffu, ring[n % kPieces].nk);
-        const bool two = __reduce_max_sync(0xffffffffu, ring[n % kPieces].tokens) > tt;
+        const int nq = __reduce_max_sync(0xffffffffu, ring[n % kPieces].tokens) > tt ? 2 : 1;
         if (lane == 0) mbar_arrive(b_taken(n % kPieces));
         __syncwarp();
         if (nk < 0) break;
         if (nk == 0) continue;
-        ok = __all_sync(0xffffffffu, mbar_wait(b_qfull, pieces & 1) && landed(seq) && s_free(0, sn0));
-        if (!ok) break;
-        issue_s(0, seq, !two, !two && nk == 1);
-        ++sn0;
-        if (two) {
-          ok = __all_sync(0xffffffffu, s_free(1, sn1));
-          if (!ok) break;
-          issue_s(1, seq, true, nk == 1);
-          ++sn1;
-        }
-        for (int i = 0; i < nk; ++i) {
-          const bool more = i + 1 < nk, q_last = i + 2 == nk;
-          const uint32_t add = i > 0 ? 1u : 0u;
-          bool good = landed(seq + 1) && (!more || landed(seq + 2));
-          if (i == 0) {  // O of the last piece has been read
-            if (used0 > 0) good = good && mbar_wait(b_ofree(0), (used0 - 1) & 1);
-            if (two && used1 > 0) good = good && mbar_wait(b_ofree(1), (used1 - 1) & 1);
+        int si = 0, st = 0;  // key tile and query tile of the next S
+        auto next_s = [&]() {
+          (st == 0 ? sn0 : sn1) += 1;
+          if (++st == nq) {
+            st = 0;
+            ++si;
           }
-          if constexpr (L::kOwnP) {
-            if (more) {
-              ok = __all_sync(0xffffffffu, good && s_free(0, sn0));
-              if (!ok) break;
-              issue_s(0, seq + 2, !two, !two && q_last);
-              ++sn0;
-              if (two) {
-                good = s_free(1, sn1);
-                ok = __all_sync(0xffffffffu, good);
-                if (!ok) break;
-                issue_s(1, seq + 2, true, q_last);
-                ++sn1;
-              }
+          if (++sb == kBufs) sb = 0;
+        };
+        ok = __all_sync(0xffffffffu, mbar_wait(b_qfull, pieces & 1));
+        for (int x = 0; ok && x < kBufs && si < nk; ++x) {
+          const uint32_t kt = seq + 2 * si;
+          ok = __all_sync(0xffffffffu, st > 0 || mbar_wait(full_bar(kt), full_phase(kt)));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) issue_s(st, kt, st + 1 == nq, st + 1 == nq && si + 1 == nk);
+          __syncwarp();
+          next_s();
+        }
+        if (!ok) break;
+        for (int i = 0; i < nk && ok; ++i) {
+          for (int t = 0; t < nq; ++t) {
+            // what this P V and the S behind it wait for: asked for all at once
+            const uint32_t vt = seq + 2 * i + 1, kt = seq + 2 * si;
+            const bool more = si < nk, need_k = more && st == 0, need_v = t == 0;
+            const bool have_v = !need_v || mbar_try_wait(full_bar(vt), full_phase(vt));
+            const bool have_k = !need_k || mbar_try_wait(full_bar(kt), full_phase(kt));
+            const uint32_t pn = t == 0 ? pn0 : pn1;
+            const bool have_p = mbar_try_wait(b_pfull(t, pn), buf_phase(pn));
+            bool good = have_v || mbar_wait(full_bar(vt), full_phase(vt));
+            good = good && (have_k || mbar_wait(full_bar(kt), full_phase(kt)));
+            if (i == 0) {  // O of the tile's last piece has been read out
+              const uint32_t u = t == 0 ? used0 : used1;
+              if (u > 0) good = good && mbar_wait(b_ofree(t), (u - 1) & 1);
             }
-          }
-          ok = __all_sync(0xffffffffu, good && mbar_wait(b_pfull(0, 0), pn0 & 1));
-          if (!ok) break;
-          issue_pv(0, 0, seq + 1, add, false);
-          ok = __all_sync(0xffffffffu, mbar_wait(b_pfull(0, 1), pn0 & 1));
-          if (!ok) break;
-          issue_pv(0, 1, seq + 1, 1u, !two);
-          ++pn0;
-          if (!L::kOwnP && more) issue_s(0, seq + 2, !two, !two && q_last);
-          if (two) {
-            ok = __all_sync(0xffffffffu, mbar_wait(b_pfull(1, 0), pn1 & 1));
+            good = good && (have_p || mbar_wait(b_pfull(t, pn), buf_phase(pn)));
+            ok = __all_sync(0xffffffffu, good);
             if (!ok) break;
-            issue_pv(1, 0, seq + 1, add, false);
-            ok = __all_sync(0xffffffffu, mbar_wait(b_pfull(1, 1), pn1 & 1));
-            if (!ok) break;
-            issue_pv(1, 1, seq + 1, 1u, true);
-            ++pn1;
-            if (!L::kOwnP && more) issue_s(1, seq + 2, true, q_last);
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t vb = dV + (vt % kRing) * kTileStep;
+#pragma unroll
+              for (int ks = 0; ks < kBN / 16; ++ks)
+                mma_bf16_tmem_a(L::kTmemO + t * D, pb * 128 + ks * 8, vb + ks * 128, iO, (i > 0 || ks > 0) ? 1u : 0u);
+              mma_commit(b_pvdone(t));
+              if (t + 1 == nq) mma_commit(b_empty(vt % kRing));
+              // this S goes into a buffer whose P V was issued before it
+              if (more) issue_s(st, kt, st + 1 == nq, st + 1 == nq && si + 1 == nk);
+            }
+            __syncwarp();
+            if (more) next_s();
+            (t == 0 ? pn0 : pn1) += 1;
+            if (++pb == kBufs) pb = 0;
           }
-          seq += 2;
         }
         if (!ok) break;
+        seq += 2 * nk;
         ++used0;
-        if (two) ++used1;
+        if (nq == 2) ++used1;
         ++pieces;
       }
       if (!ok && lane == 0) set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
@@ -611,9 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     // ---------------- softmax: one query row per thread -----------------------
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + L::kTmemO + t * D;
-    const uint32_t tP = tmem + lanes + L::kTmemP + t * L::kTmemPStep;
-    uint32_t steps = 0, tiles = 0;  // P V products of this tile; key tiles of the CTA
+    const uint32_t tO = tmem + lanes + L::kTmemO + t * D;
+    uint32_t steps = 0, tiles = 0, prods = 0;  // products of this tile; key tiles, products of the CTA's pieces so far
     for (uint32_t n = 0;; ++n) {
       ok = __all_sync(0xffffffffu, piece_ready(n));
       if (!ok) break;
@@ -624,14 +674,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         __syncwarp();
         if (lane == 0) mbar_arrive(b_taken(n % kPieces));
         tiles += nk;
+        prods += nk;
         continue;
       }
       const int pos = q.p0 + t * tt + r / p.g;  // this row's token
+      const int nq = q.tokens > tt ? 2 : 1;
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < nk; ++i) {
         const int ti = q.t0 + i;
         const int k0 = (ti < q.ns ? ti : q.w0 + ti - q.ns) * kBN;
-        ok = __all_sync(0xffffffffu, mbar_wait(b_sfull(t), steps & 1));
+        const uint32_t tS = tmem + lanes + (prods + i * nq + t) % kBufs * 128;
+        ok = __all_sync(0xffffffffu, mbar_wait(b_sfull(t, steps), buf_phase(steps)));
         if (!ok) break;
         tc_fence_after();
         float s[kBN];
@@ -644,11 +697,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
                           (p.window == 0 || k0 > plast - p.window || k0 + kBN <= p.sinks);
         float f = p.scale_log2;  // what the scores are still to be multiplied by
         tmem_wait_ld();
-        if constexpr (L::kOwnP) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_sfree(t));
-        }
         float mx = -INFINITY;
         if (full) {
           float mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
@@ -718,11 +766,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           }
           fence_async_smem();
         }
-        if (L::kOwnP && steps > 0) {  // P V has read the last P
-          ok = __all_sync(0xffffffffu, mbar_wait(b_pvdone(t), (steps - 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-        }
         const float ms = m == -INFINITY ? 0.f : m;
         const float2 f2 = make_float2(f, f), nm = make_float2(-ms, -ms);
         float2 l2 = make_float2(0.f, 0.f);
@@ -736,37 +779,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
             pk[c / 2] = float2_to_bf16x2(e.x, e.y);
             l2 = __fadd2_rn(l2, e);
           }
-          tmem_st16(tP + c0 / 2, pk);
-          if (c0 == 32 || c0 == 96) {  // half of P is there: its product may start
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_pfull(t, c0 / 64));
-          }
+          tmem_st16(tS + c0 / 2, pk);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_pfull(t, steps));
         l += l2.x + l2.y;
         ++steps;
         ++tiles;
       }
       if (!ok) break;
+      prods += nk * nq;
       // epilogue: O / sum and the LSE (no key: O = 0, LSE = -inf)
-      if (nk > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(b_pvdone(t), (steps - 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
-      }
       const float inv = l > 0.f ? 1.0f / l : 0.f;
       const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
       const int rt = r / p.g, j = t * tt + rt;  // token of the tile, of the item
       const bool real = rt < tt && j < q.tokens;
       const int slot = q.slot;
       const int64_t row = static_cast<int64_t>(q.row0 + j) * p.H_q + q.head * p.g + r % p.g;
-      const int64_t prow = static_cast<int64_t>(slot) * p.slot_rows + t * kBM + r;
       __syncwarp();
       if (lane == 0) mbar_arrive(b_taken(n % kPieces));
-#pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        float o[32];
+      if (nk > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(b_pvdone(t), (steps - 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      auto read_o = [&](int c0, float* o) {
         if (nk > 0) {
           tmem_ld32(tO + c0, reinterpret_cast<uint32_t*>(o));
           tmem_wait_ld();
@@ -776,20 +815,42 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         }
 #pragma unroll
         for (int x = 0; x < 32; ++x) o[x] *= inv;
-        if (real && slot < 0) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + c0);
+      };
+      if (slot < 0) {
+        // lane i of each four writes chunk i of the four's rows
+        long long rows[4];
 #pragma unroll
-          for (int x = 0; x < 32; x += 8)
-            dst[x / 8] = make_uint4(float2_to_bf16x2(o[x], o[x + 1]), float2_to_bf16x2(o[x + 2], o[x + 3]),
-                                    float2_to_bf16x2(o[x + 4], o[x + 5]), float2_to_bf16x2(o[x + 6], o[x + 7]));
-        } else if (real) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c0);
+        for (int x = 0; x < 4; ++x)
+          rows[x] = __shfl_sync(0xffffffffu, real ? static_cast<long long>(row) : -1ll, (lane & ~3) + x);
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float o[32];
+          read_o(c0, o);
+          uint4 v[4];
 #pragma unroll
-          for (int x = 0; x < 32; x += 4) dst[x / 4] = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+          for (int x = 0; x < 4; ++x)
+            v[x] = make_uint4(float2_to_bf16x2(o[8 * x], o[8 * x + 1]), float2_to_bf16x2(o[8 * x + 2], o[8 * x + 3]),
+                              float2_to_bf16x2(o[8 * x + 4], o[8 * x + 5]),
+                              float2_to_bf16x2(o[8 * x + 6], o[8 * x + 7]));
+          transpose4(v, lane);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (rows[x] >= 0) *reinterpret_cast<uint4*>(p.out + rows[x] * D + c0 + (lane & 3) * 8) = v[x];
         }
+        if (real && p.lse) p.lse[row] = lse2 * kLn2C;
+      } else {
+        float* dst = p.part_o + (static_cast<int64_t>(slot) * (D / 4) * p.slot_rows + t * kBM + r) * 4;
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float o[32];
+          read_o(c0, o);
+          if (real) {
+#pragma unroll
+            for (int x = 0; x < 32; x += 4)
+              *reinterpret_cast<float4*>(dst + static_cast<int64_t>(c0 + x) * p.slot_rows) =
+                  make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+          }
+        }
+        if (real) p.part_lse[static_cast<int64_t>(slot) * p.slot_rows + t * kBM + r] = lse2 * kLn2C;
       }
-      if (real && slot >= 0) p.part_lse[prow] = lse2 * kLn2C;
-      if (real && slot < 0 && p.lse) p.lse[row] = lse2 * kLn2C;
       if (nk > 0) {
         tc_fence_before();
         __syncwarp();
@@ -807,42 +868,57 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
 }
 
 // Joins the states of the items cut between CTAs: block (x, k) takes 32 rows
-// of the item whose first part CTA k holds, a warp one row at a time.
+// of the item whose first part CTA k holds. Lane r of every warp holds row r,
+// warp w its columns 4 (w + 8 i); the joined rows leave through shared memory.
 template <int D>
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams p) {
+  constexpr int kN = D / 32;  // groups of four columns per thread
+  __shared__ uint2 rows_s[32][D / 4 + 1];
   pdl_launch_dependents();
   pdl_wait_primary();
   const int k = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const SplitItem si = p.split[k];
-  if (si.row0 < 0) return;
-  constexpr int kV = D / 32;  // values per lane
-  for (int rr = warp; rr < 32; rr += 8) {
-    const int r = blockIdx.x * 32 + rr;
-    const int rt = (r % kBM) / p.g, j = (r / kBM) * p.tile_tokens + rt;
-    if (rt >= p.tile_tokens || j >= si.tokens) continue;
-    float mx = -INFINITY;
-    for (int i = 0; i < si.parts; ++i) {
-      const int slot = i == 0 ? si.slot : 2 * (k + i);
-      mx = fmaxf(mx, p.part_lse[static_cast<int64_t>(slot) * p.slot_rows + r]);
-    }
-    const float ms = mx == -INFINITY ? 0.f : mx;
-    float a[kV], sum = 0.f;
+  const int r = blockIdx.x * 32 + lane;  // row of the slot
+  const int tile = r / kBM, rt = r % kBM / p.g, j = tile * p.tile_tokens + rt;
+  const bool real = rt < p.tile_tokens && j < si.tokens;
+  if (si.row0 < 0 || !__syncthreads_or(real)) return;
+  float mx = -INFINITY;
+  auto at = [&](int i) { return static_cast<int64_t>(i == 0 ? si.slot : 2 * (k + i)) * p.slot_rows; };
+#pragma unroll 4
+  for (int i = 0; i < si.parts; ++i) mx = fmaxf(mx, real ? p.part_lse[at(i) + r] : -INFINITY);
+  const float ms = mx == -INFINITY ? 0.f : mx;
+  float4 a[kN];
+  float sum = 0.f;
 #pragma unroll
-    for (int x = 0; x < kV; ++x) a[x] = 0.f;
+  for (int x = 0; x < kN; ++x) a[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (real) {
+#pragma unroll 2
     for (int i = 0; i < si.parts; ++i) {
-      const int64_t row = static_cast<int64_t>(i == 0 ? si.slot : 2 * (k + i)) * p.slot_rows + r;
-      const float wt = __expf(p.part_lse[row] - ms);
-      const float* o = p.part_o + row * D + lane * kV;
+      const float wt = __expf(p.part_lse[at(i) + r] - ms);
+      const float4* o = reinterpret_cast<const float4*>(p.part_o) + at(i) * (D / 4) + r;
       sum += wt;
 #pragma unroll
-      for (int x = 0; x < kV; ++x) a[x] += wt * o[x];
+      for (int x = 0; x < kN; ++x) {
+        const float4 v = o[static_cast<int64_t>(warp + 8 * x) * p.slot_rows];
+        a[x].x += wt * v.x;
+        a[x].y += wt * v.y;
+        a[x].z += wt * v.z;
+        a[x].w += wt * v.w;
+      }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int64_t out = static_cast<int64_t>(si.row0 + j) * p.H_q + si.head * p.g + r % kBM % p.g;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + out * D) + lane * (kV / 2);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int x = 0; x < kV; x += 2) dst[x / 2] = float2_to_bf16x2(a[x] * inv, a[x + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[out] = sum > 0.f ? ms + logf(sum) : -INFINITY;
+  for (int x = 0; x < kN; ++x)
+    rows_s[lane][warp + 8 * x] =
+        make_uint2(float2_to_bf16x2(a[x].x * inv, a[x].y * inv), float2_to_bf16x2(a[x].z * inv, a[x].w * inv));
+  const int64_t out = real ? static_cast<int64_t>(si.row0 + j) * p.H_q + si.head * p.g + r % kBM % p.g : -1;
+  if (warp == 0 && real && p.lse) p.lse[out] = sum > 0.f ? ms + logf(sum) : -INFINITY;
+  __syncthreads();
+  // warp w writes rows w, w + 8, ...: one row of D / 4 pairs of words at a time
+  for (int rr = warp; rr < 32; rr += 8) {
+    const long long to = __shfl_sync(0xffffffffu, static_cast<long long>(out), rr);
+    if (to >= 0 && lane < D / 4) reinterpret_cast<uint2*>(p.out + to * D)[lane] = rows_s[rr][lane];
   }
 }
 

@@ -27,12 +27,14 @@
 // where it is the A operand of O += P V. Products of one thread complete in
 // order, so S(j + 1) of a tile may follow its P V(j) without a wait, and the
 // two tiles take turns: while one tile's softmax runs, the tensor pipe works
-// on the other. The running maximum moves only when a score exceeds it by more
-// than 2^8 (a row's weights stay below that), so O in TMEM is rescaled rarely.
+// on the other. A row's reference for the exponents is the maximum of its first
+// key tile and moves only when a later tile's weights grow past 2^30, so most
+// tiles need no maximum, and O in TMEM is rescaled rarely.
 // P is rounded to bf16 because the product's operands share one type; O is
-// divided by the sum of the rounded weights, the LSE takes the exact sum.
+// divided by the sum of the weights before that rounding.
 #include <cmath>
 #include <cstdlib>
+#include <type_traits>
 
 #include "ts_tcgen05.cuh"
 
@@ -47,7 +49,7 @@ constexpr int kItemUnits = 1;     // units an item counts beyond its key tiles
 constexpr int kBadRing = 16;      // key tiles whose bad-page mask is kept
 constexpr float kLog2eC = 1.4426950408889634f;
 constexpr float kLn2C = 0.6931471805599453f;
-constexpr float kSlack = 8.0f;
+constexpr float kMostSum = 1073741824.f;  // 2^30: sum of a tile's weights at which a row's reference moves
 // 256 threads of softmax and 128 others: 256 * 216 + 128 * 72 == 384 * 168.
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
@@ -110,6 +112,28 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Waits for this thread's loads from TMEM. It takes the registers of one of
+// them, so that the compiler neither reads nor copies them before.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
@@ -194,6 +218,20 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane) {
   swap(v[0], v[2], 2, lane & 2);
   swap(v[1], v[3], 2, lane & 2);
 }
+
+// A place in a ring and the phase of its barrier.
+struct Turn {
+  uint32_t at, phase;
+  __device__ __forceinline__ explicit Turn(uint32_t a) : at(a), phase(0) {}
+  template <uint32_t kPlaces, uint32_t kStep = 1>
+  __device__ __forceinline__ void next() {
+    at += kStep;
+    if (at >= kPlaces) {
+      at -= kPlaces;
+      phase ^= 1;
+    }
+  }
+};
 
 // A piece of the CTA's range: key tiles [t0, t0 + nk) of one item. Warp 11
 // writes them to a ring in shared memory, ahead of the roles that read them.
@@ -560,99 +598,116 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       // difference in 16-byte units, which stays within the address field
       const uint64_t dQ = desc_sw128(sQ), dK = desc_sw128(sKV), dV = desc_sw128(sKV, kAtom, 1024);
       constexpr uint64_t kTileStep = kTile >> 4;
-      uint32_t seq = 0;     // ring tile of the piece's first K tile
-      uint32_t pieces = 0;  // with products
-      uint32_t used0 = 0, used1 = 0;                  // pieces of each tile
-      uint32_t sn0 = 0, sn1 = 0, pn0 = 0, pn1 = 0;    // S and P V products of each tile
-      uint32_t sb = 0, pb = 0;                        // buffer of the next S, of the next P V
-      auto full_bar = [&](uint32_t x) { return b_full(x % kRing); };
-      auto full_phase = [&](uint32_t x) { return (x / kRing) & 1; };
-      // S of tile t from ring tile x into buffer sb (one lane)
-      auto issue_s = [&](int t, uint32_t x, bool k_last, bool q_last) {
-        const uint64_t q = dQ + t * kTileStep, kb = dK + (x % kRing) * kTileStep;
+      // Counters are kept as (place, phase) pairs and tile numbers are compile-
+      // time: what this warp computes between two products delays them.
+      Turn kt(0), vt(1);                            // ring places of the next K and V tile
+      Turn st[2] = {Turn(0), Turn(0)}, pt[2] = {Turn(0), Turn(0)};  // barriers of each tile's next S and P V
+      uint32_t pieces = 0, used[2] = {0, 0};        // with products; of each tile
+      auto run_piece = [&](auto tiles_tag, const int nk) {
+        constexpr int NQ = decltype(tiles_tag)::value;  // tiles with rows
+        int left = nk;         // K tiles whose S products are not all issued
+        uint32_t sb = 0, pb = 0;  // buffers of the next S and P V: the last piece's products are all issued
+        // S of tile t; the last tile's hands the K tile back, the last K tile's the queries
+        auto issue_s = [&](auto tag) {
+          constexpr int t = decltype(tag)::value;
+          const uint64_t q = dQ + t * kTileStep, kb = dK + kt.at * kTileStep;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          constexpr uint64_t kAtomStep = kAtom >> 4;
-          const uint64_t off = (ks >> 2) * kAtomStep + (ks & 3) * 2;
-          mma_bf16(sb * 128, q + off, kb + off, iS, ks > 0);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            constexpr uint64_t kAtomStep = kAtom >> 4;
+            const uint64_t off = (ks >> 2) * kAtomStep + (ks & 3) * 2;
+            mma_bf16(sb * 128, q + off, kb + off, iS, ks > 0);
+          }
+          const uint32_t done = b_sfull(t, st[t].at);
+          mma_commit(done);
+          // the arrival carries what the key tile's barrier carried here: the
+          // softmax reads the tile's bad-page mask after it
+          mbar_arrive(done);
+          if (t == NQ - 1) {
+            mma_commit(b_empty(kt.at));
+            if (left == 1) mma_commit(b_qempty);
+          }
+        };
+        auto after_s = [&](auto tag) {
+          constexpr int t = decltype(tag)::value;
+          st[t].template next<kBufs>();
+          if (++sb == kBufs) sb = 0;
+          if (t == NQ - 1) {
+            kt.template next<kRing, 2>();
+            --left;
+          }
+        };
+        using T0 = std::integral_constant<int, 0>;
+        using T1 = std::integral_constant<int, NQ - 1>;
+        auto prime = [&](auto tag) {
+          constexpr int t = decltype(tag)::value;
+          if (!ok || left == 0) return;
+          if (t == 0) ok = __all_sync(0xffffffffu, mbar_wait(b_full(kt.at), kt.phase));
+          if (!ok) return;
+          tc_fence_after();
+          if (elect_one()) issue_s(tag);
+          __syncwarp();
+          after_s(tag);
+        };
+        prime(T0());
+        prime(T1());
+        if (kBufs == 3) prime(T0());
+        auto step = [&](auto tag, const bool first) {  // P V of tile t and the S product that it makes room for
+          constexpr int t = decltype(tag)::value;
+          constexpr int ts = NQ == 1 ? 0 : (t + kBufs) % 2;  // whose S
+          const bool more = left > 0;
+          // what they wait for, asked for all at once
+          const uint32_t vbar = b_full(vt.at), kbar = b_full(kt.at), pbar = b_pfull(t, pt[t].at);
+          const bool have_v = t > 0 || mbar_try_wait(vbar, vt.phase);
+          const bool have_k = ts > 0 || !more || mbar_try_wait(kbar, kt.phase);
+          const bool have_p = mbar_try_wait(pbar, pt[t].phase);
+          bool good = have_v && have_k && have_p;
+          if (!good)
+            good = (have_v || mbar_wait(vbar, vt.phase)) && (have_k || mbar_wait(kbar, kt.phase)) &&
+                   (have_p || mbar_wait(pbar, pt[t].phase));
+          // O of the tile's last piece has been read out
+          if (first && used[t] > 0) good = good && mbar_wait(b_ofree(t), (used[t] - 1) & 1);
+          ok = __all_sync(0xffffffffu, good);
+          if (!ok) return;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t vb = dV + vt.at * kTileStep;
+#pragma unroll
+            for (int ks = 0; ks < kBN / 16; ++ks)
+              mma_bf16_tmem_a(L::kTmemO + t * D, pb * 128 + ks * 8, vb + ks * 128, iO, (!first || ks > 0) ? 1u : 0u);
+            mma_commit(b_pvdone(t));
+            if (t == NQ - 1) mma_commit(b_empty(vt.at));
+            if (more) issue_s(std::integral_constant<int, ts>());
+          }
+          __syncwarp();
+          if (more) after_s(std::integral_constant<int, ts>());
+          pt[t].template next<kBufs>();
+          if (++pb == kBufs) pb = 0;
+          if (t == NQ - 1) vt.template next<kRing, 2>();
+        };
+        for (int i = 0; ok && i < nk; ++i) {
+          step(T0(), i == 0);
+          if (NQ == 2 && ok) step(T1(), i == 0);
         }
-        const uint32_t done = b_sfull(t, t == 0 ? sn0 : sn1);
-        mma_commit(done);
-        // the arrival carries what the key tile's barrier carried here: the
-        // softmax reads the tile's bad-page mask after it
-        mbar_arrive(done);
-        if (k_last) mma_commit(b_empty(x % kRing));
-        if (q_last) mma_commit(b_qempty);
+        ++used[0];
+        if (NQ == 2) ++used[1];
       };
       for (uint32_t n = 0;; ++n) {
         ok = __all_sync(0xffffffffu, piece_ready(n));
         if (!ok) break;
         // a reduction's result is known to be the same in all lanes
         const int nk = __reduce_max_sync(0xffffffffu, ring[n % kPieces].nk);
-        const int nq = __reduce_max_sync(0xffffffffu, ring[n % kPieces].tokens) > tt ? 2 : 1;
+        const bool two = __reduce_max_sync(0xffffffffu, ring[n % kPieces].tokens) > tt;
         if (lane == 0) mbar_arrive(b_taken(n % kPieces));
         __syncwarp();
         if (nk < 0) break;
         if (nk == 0) continue;
-        int si = 0, st = 0;  // key tile and query tile of the next S
-        auto next_s = [&]() {
-          (st == 0 ? sn0 : sn1) += 1;
-          if (++st == nq) {
-            st = 0;
-            ++si;
-          }
-          if (++sb == kBufs) sb = 0;
-        };
         ok = __all_sync(0xffffffffu, mbar_wait(b_qfull, pieces & 1));
-        for (int x = 0; ok && x < kBufs && si < nk; ++x) {
-          const uint32_t kt = seq + 2 * si;
-          ok = __all_sync(0xffffffffu, st > 0 || mbar_wait(full_bar(kt), full_phase(kt)));
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) issue_s(st, kt, st + 1 == nq, st + 1 == nq && si + 1 == nk);
-          __syncwarp();
-          next_s();
-        }
         if (!ok) break;
-        for (int i = 0; i < nk && ok; ++i) {
-          for (int t = 0; t < nq; ++t) {
-            // what this P V and the S behind it wait for: asked for all at once
-            const uint32_t vt = seq + 2 * i + 1, kt = seq + 2 * si;
-            const bool more = si < nk, need_k = more && st == 0, need_v = t == 0;
-            const bool have_v = !need_v || mbar_try_wait(full_bar(vt), full_phase(vt));
-            const bool have_k = !need_k || mbar_try_wait(full_bar(kt), full_phase(kt));
-            const uint32_t pn = t == 0 ? pn0 : pn1;
-            const bool have_p = mbar_try_wait(b_pfull(t, pn), buf_phase(pn));
-            bool good = have_v || mbar_wait(full_bar(vt), full_phase(vt));
-            good = good && (have_k || mbar_wait(full_bar(kt), full_phase(kt)));
-            if (i == 0) {  // O of the tile's last piece has been read out
-              const uint32_t u = t == 0 ? used0 : used1;
-              if (u > 0) good = good && mbar_wait(b_ofree(t), (u - 1) & 1);
-            }
-            good = good && (have_p || mbar_wait(b_pfull(t, pn), buf_phase(pn)));
-            ok = __all_sync(0xffffffffu, good);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint64_t vb = dV + (vt % kRing) * kTileStep;
-#pragma unroll
-              for (int ks = 0; ks < kBN / 16; ++ks)
-                mma_bf16_tmem_a(L::kTmemO + t * D, pb * 128 + ks * 8, vb + ks * 128, iO, (i > 0 || ks > 0) ? 1u : 0u);
-              mma_commit(b_pvdone(t));
-              if (t + 1 == nq) mma_commit(b_empty(vt % kRing));
-              // this S goes into a buffer whose P V was issued before it
-              if (more) issue_s(st, kt, st + 1 == nq, st + 1 == nq && si + 1 == nk);
-            }
-            __syncwarp();
-            if (more) next_s();
-            (t == 0 ? pn0 : pn1) += 1;
-            if (++pb == kBufs) pb = 0;
-          }
-        }
+        if (two)
+          run_piece(std::integral_constant<int, 2>(), nk);
+        else
+          run_piece(std::integral_constant<int, 1>(), nk);
         if (!ok) break;
-        seq += 2 * nk;
-        ++used0;
-        if (nq == 2) ++used1;
         ++pieces;
       }
       if (!ok && lane == 0) set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
@@ -663,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + lanes + L::kTmemO + t * D;
-    uint32_t steps = 0, tiles = 0, prods = 0;  // products of this tile; key tiles, products of the CTA's pieces so far
+    uint32_t steps = 0, tiles = 0;  // products of this tile; key tiles of the CTA's pieces so far
     for (uint32_t n = 0;; ++n) {
       ok = __all_sync(0xffffffffu, piece_ready(n));
       if (!ok) break;
@@ -674,89 +729,44 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         __syncwarp();
         if (lane == 0) mbar_arrive(b_taken(n % kPieces));
         tiles += nk;
-        prods += nk;
         continue;
       }
-      const int pos = q.p0 + t * tt + r / p.g;  // this row's token
+      const int rt = r / p.g, j = t * tt + rt;  // this row's token of the tile, of the item
+      const int pos = q.p0 + j;
+      const bool real = rt < tt && j < q.tokens;
       const int nq = q.tokens > tt ? 2 : 1;
       float m = -INFINITY, l = 0.f;
+      const int klo = q.klo, khi = q.khi, ns = q.ns, w0 = q.w0, t0 = q.t0;
+      const int pfirst = q.p0 + t * tt, plast = pfirst + tt - 1;  // positions of the tile's rows
+      bool fresh = true;  // some row has no reference yet
       for (int i = 0; i < nk; ++i) {
-        const int ti = q.t0 + i;
-        const int k0 = (ti < q.ns ? ti : q.w0 + ti - q.ns) * kBN;
-        const uint32_t tS = tmem + lanes + (prods + i * nq + t) % kBufs * 128;
+        // before the scores are there: what is known of the key tile
+        const int k0 = (t0 + i < ns ? t0 + i : w0 + t0 + i - ns) * kBN;
+        const int first = (p.window > 0 && pos >= p.window) ? pos - p.window + 1 - k0 : 0;
+        const int end = min(pos + 1, khi) - k0, keep = p.sinks - k0;
+        // every row of the tile sees every key: no masks
+        const bool all = k0 + kBN - 1 <= pfirst && k0 + kBN <= khi && p.scale_log2 > 0.f &&
+                         (p.window == 0 || k0 > plast - p.window || k0 + kBN <= p.sinks);
+        auto cuts_page = [&](int x) { return x > k0 && x < k0 + kBN && (x & (p.page_size - 1)) != 0; };
+        const bool ragged = cuts_page(khi) || cuts_page(klo) || (klo > 0 && cuts_page(p.sinks));
+        const uint32_t tS = tmem + lanes + (i * nq + t) % kBufs * 128;
         ok = __all_sync(0xffffffffu, mbar_wait(b_sfull(t, steps), buf_phase(steps)));
         if (!ok) break;
         tc_fence_after();
         float s[kBN];
 #pragma unroll
         for (int c = 0; c < kBN; c += 32) tmem_ld32(tS + c, reinterpret_cast<uint32_t*>(s) + c);
-        const uint32_t bad = bad_ring[tiles % kBadRing];
-        // every row of the tile sees every key: no masks
-        const int pfirst = q.p0 + t * tt, plast = pfirst + tt - 1;
-        const bool full = k0 + kBN - 1 <= pfirst && k0 + kBN <= q.khi && bad == 0u && p.scale_log2 > 0.f &&
-                          (p.window == 0 || k0 > plast - p.window || k0 + kBN <= p.sinks);
-        float f = p.scale_log2;  // what the scores are still to be multiplied by
-        tmem_wait_ld();
-        float mx = -INFINITY;
-        if (full) {
-          float mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < kBN; c += 8) {
-            mx = fmax3(mx, s[c], s[c + 1]);
-            mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
-            mx2 = fmax3(mx2, s[c + 4], s[c + 5]);
-            mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
-          }
-          mx = fmaxf(fmaxf(mx, mx1), fmaxf(mx2, mx3)) * f;
-        } else {
-          const int first = (p.window > 0 && pos >= p.window) ? pos - p.window + 1 - k0 : 0;
-          const int end = min(pos + 1, q.khi) - k0, keep = p.sinks - k0;
-#pragma unroll
-          for (int c0 = 0; c0 < kBN; c0 += 32) {
-            uint32_t vis = ones(end - c0) & (~ones(first - c0) | ones(keep - c0));
-            if (bad != 0u) {
-              for (int c = 0; c < 32; c += p.page_size)
-                if ((bad >> ((c0 + c) / p.page_size)) & 1u) vis &= ~(ones(c + p.page_size) & ~ones(c));
-            }
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              s[c0 + c] = (vis >> c) & 1u ? s[c0 + c] * f : -INFINITY;
-              mx = fmaxf(mx, s[c0 + c]);
-            }
-          }
-          f = 1.f;
-        }
-        if (i == 0) {
-          m = mx;
-        } else if (__any_sync(0xffffffffu, mx > m + kSlack)) {
-          ok = __all_sync(0xffffffffu, mbar_wait(b_pvdone(t), (steps - 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          const float mnew = fmaxf(m, mx);
-          const float alpha = m == -INFINITY ? 0.f : fast_exp2(m - mnew);
-          m = mnew;
-          l *= alpha;
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t u[16];
-            tmem_ld16(tO + c0, u);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(__uint_as_float(u[x]) * alpha);
-            tmem_st16(tO + c0, u);
-          }
-        }
         // Rows of a loaded page that no row sees (past the sequence's end, in
         // front of the window, behind the first tokens) may hold anything, and
         // 0 * NaN is NaN in the product: zero them once landed. Both tiles'
-        // warps do, each before its own product.
-        auto cuts_page = [&](int x) { return x > k0 && x < k0 + kBN && (x & (p.page_size - 1)) != 0; };
-        if (cuts_page(q.khi) || cuts_page(q.klo) || (q.klo > 0 && cuts_page(p.sinks))) {
+        // warps do, each before its own product. (Not before the scores: a tile
+        // without rows in some pieces may be pieces ahead of the copies.)
+        if (ragged) {
           const uint32_t vseq = 2 * tiles + 1;
           ok = __all_sync(0xffffffffu, mbar_wait(b_full(vseq % kRing), (vseq / kRing) & 1));
           if (!ok) break;
           const int key = k0 + r;
-          if (!(key < q.khi && (key >= q.klo || key < p.sinks))) {
+          if (!(key < khi && (key >= klo || key < p.sinks))) {
             unsigned char* v = smem + L::kOffKV + (vseq % kRing) * kTile + r * 128;
 #pragma unroll
             for (int a = 0; a < kAtoms; ++a)
@@ -766,11 +776,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           }
           fence_async_smem();
         }
-        const float ms = m == -INFINITY ? 0.f : m;
-        const float2 f2 = make_float2(f, f), nm = make_float2(-ms, -ms);
-        float2 l2 = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c0 = 0; c0 < kBN; c0 += 32) {
+        const uint32_t bad = bad_ring[tiles % kBadRing];
+        const bool full = all && bad == 0u;
+        const float f = full ? p.scale_log2 : 1.f;  // what the scores are still to be multiplied by
+        auto weigh = [&](int c0, float ms, float2& l2) {  // weights of 32 keys, written as bf16
+          const float2 f2 = make_float2(f, f), nm = make_float2(-ms, -ms);
           uint32_t pk[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
@@ -780,22 +790,78 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
             l2 = __fadd2_rn(l2, e);
           }
           tmem_st16(tS + c0 / 2, pk);
+        };
+        // The reference m is a maximum over earlier keys, and any reference
+        // gives the same quotient while nothing overflows: a tile's weights are
+        // taken against the old one without looking for the tile's maximum, and
+        // only where a row's sum reaches kMostSum is it moved. Rows that no one
+        // reads do not count.
+        bool move = fresh;
+        float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kBN; c += 32) tmem_wait_ld32(reinterpret_cast<uint32_t*>(s) + c);
+        if (!full) {
+#pragma unroll
+          for (int c0 = 0; c0 < kBN; c0 += 32) {
+            uint32_t vis = ones(end - c0) & (~ones(first - c0) | ones(keep - c0));
+            if (bad != 0u) {
+              for (int c = 0; c < 32; c += p.page_size)
+                if ((bad >> ((c0 + c) / p.page_size)) & 1u) vis &= ~(ones(c + p.page_size) & ~ones(c));
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c0 + c] = (vis >> c) & 1u ? s[c0 + c] * p.scale_log2 : -INFINITY;
+          }
         }
+        if (!move) {
+#pragma unroll
+          for (int c0 = 0; c0 < kBN; c0 += 32) weigh(c0, m, l2);
+          move = __any_sync(0xffffffffu, real && !(l2.x + l2.y < kMostSum));
+        }
+        if (move) {
+          float mx = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kBN; c += 8) {
+            mx = fmax3(mx, s[c], s[c + 1]);
+            mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
+            mx2 = fmax3(mx2, s[c + 4], s[c + 5]);
+            mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
+          }
+          mx = fmaxf(fmaxf(mx, mx1), fmaxf(mx2, mx3)) * f;
+          const float mnew = fmaxf(m, mx);
+          if (i > 0) {  // O so far is rescaled: every P V of it must be done
+            ok = __all_sync(0xffffffffu, mbar_wait(b_pvdone(t), (steps - 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const float alpha = m == -INFINITY ? 0.f : fast_exp2(m - mnew);
+            l *= alpha;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t u[32];
+              tmem_ld32(tO + c0, u);
+              tmem_wait_ld32(u);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) u[x] = __float_as_uint(__uint_as_float(u[x]) * alpha);
+              tmem_st32(tO + c0, u);
+            }
+          }
+          m = mnew;
+          fresh = __any_sync(0xffffffffu, real && m == -INFINITY);
+          l2 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c0 = 0; c0 < kBN; c0 += 32) weigh(c0, m == -INFINITY ? 0.f : m, l2);
+        }
+        l += l2.x + l2.y;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_pfull(t, steps));
-        l += l2.x + l2.y;
         ++steps;
         ++tiles;
       }
       if (!ok) break;
-      prods += nk * nq;
       // epilogue: O / sum and the LSE (no key: O = 0, LSE = -inf)
       const float inv = l > 0.f ? 1.0f / l : 0.f;
       const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
-      const int rt = r / p.g, j = t * tt + rt;  // token of the tile, of the item
-      const bool real = rt < tt && j < q.tokens;
       const int slot = q.slot;
       const int64_t row = static_cast<int64_t>(q.row0 + j) * p.H_q + q.head * p.g + r % p.g;
       __syncwarp();
@@ -808,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       auto read_o = [&](int c0, float* o) {
         if (nk > 0) {
           tmem_ld32(tO + c0, reinterpret_cast<uint32_t*>(o));
-          tmem_wait_ld();
+          tmem_wait_ld32(reinterpret_cast<uint32_t*>(o));
         } else {
 #pragma unroll
           for (int x = 0; x < 32; ++x) o[x] = 0.f;

@@ -182,8 +182,15 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# The current stream's handle without building a Stream object (3 us on the
+# host of a GB300, as much as a launch), where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -194,9 +201,29 @@ def _rows(t: torch.Tensor):
     """Pointer and row step (elements) of a [rows, heads, D] tensor whose rows are contiguous."""
     rows, heads, D = t.shape
     step, head_step, unit = t.stride()
-    if (D > 1 and unit != 1) or (heads > 1 and head_step != D):
+    if (unit != 1 and D > 1) or (head_step != D and heads > 1):
         raise ValueError("the heads of a row must be contiguous")
     return t.data_ptr(), step if rows > 1 else heads * D
+
+
+def _pointers(*tensors):
+    """Pointers of contiguous tensors (None stays None). The library launches on the
+    current device: every tensor must live there."""
+    device = -2
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        at = t.get_device()
+        if at != device:
+            if at < 0 or device != -2 or at != torch.cuda.current_device():
+                raise ValueError(f"tensors must be on the current CUDA device (got {t.device})")
+            device = at
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        out.append(t.data_ptr())
+    return out
 
 
 def _require_i32(*ts):
@@ -273,31 +300,25 @@ def ts_paged_decode_sink_attn(q, k_pool, v_pool, block_table, seq_lens, scale: f
                               out=None, lse=None, workspace=None, stream=None, return_lse: bool = False):
     """Decode attention over a sliding window whose sequence's first ``sinks`` tokens stay
     visible; returns ``out`` (and ``lse``)."""
-    _require_i32(block_table, seq_lens)
     B, H_q, D = q.shape
     P, ps, H_kv, _ = k_pool.shape
+    _require_chunks(seq_lens, None, block_table)
     _require_cache(q, k_pool, v_pool)
+    if seq_lens.numel() != B:
+        raise ValueError("a batch of B sequences has B queries, B lengths and B block-table rows")
     if out is None:
         out = torch.empty(B, H_q, D, dtype=q.dtype, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty(B, H_q, dtype=torch.float32, device=q.device)
     _require_result(out, lse, q)
-    _require_current_device(q, k_pool, v_pool, block_table, seq_lens, out, lse, workspace)
+    qp, kp, vp, bt, lens, op, lp, wp = _pointers(q, k_pool, v_pool, block_table, seq_lens, out, lse, workspace)
     if workspace is None:
         workspace = new_workspace(ts_paged_decode_workspace_size(B, H_q, D), q.device)
-    _check(lib().ts_paged_decode_sink_attn(_ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
-                                           block_table.shape[1], _ptr(seq_lens), B, H_q, H_kv, D, ps, P,
-                                           int(window), int(sinks), float(scale), _dt(q), _ptr(out), _ptr(lse),
-                                           _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                           _stream(stream)))
+        wp = workspace.data_ptr()
+    _check(lib().ts_paged_decode_sink_attn(qp, kp, vp, bt, block_table.shape[1], lens, B, H_q, H_kv, D, ps, P,
+                                           int(window), int(sinks), float(scale), _dt(q), op, lp, wp,
+                                           workspace.nbytes, _stream(stream)))
     return (out, lse) if return_lse else out
-
-
-def _require_current_device(*tensors):
-    """The library launches on the current device: every tensor must live there."""
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != torch.cuda.current_device()):
-            raise ValueError(f"tensors must be on the current CUDA device (got {t.device})")
 
 
 def _require_cache(q, k_pool, v_pool):
@@ -309,30 +330,37 @@ def _require_cache(q, k_pool, v_pool):
 
 
 def _require_result(out, lse, q):
-    if out.shape != q.shape or out.dtype != q.dtype:
+    if out.dtype != q.dtype or out.shape != q.shape:
         raise ValueError("out must have the queries' shape and dtype")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2]):
         raise ValueError("lse must be float32 of the queries' rows and heads")
 
 
+_INT32 = torch.int32
+
+
 def _require_chunks(seq_lens, indptr, block_table):
-    """Ragged batches: indptr has one entry more than there are sequences."""
-    _require_i32(seq_lens, indptr, block_table)
-    B = seq_lens.shape[0]
-    if indptr.shape != (B + 1,) or block_table.shape[0] != B:
+    """int32 metadata of B sequences: B lengths, B block-table rows, B + 1 row offsets."""
+    if seq_lens.dtype != _INT32 or block_table.dtype != _INT32 or (indptr is not None and indptr.dtype != _INT32):
+        raise TypeError("block tables, lengths and row offsets must be int32")
+    B = seq_lens.numel()
+    if block_table.shape[0] != B or (indptr is not None and indptr.numel() != B + 1):
         raise ValueError("a batch of B sequences has B lengths, B block-table rows and B + 1 row offsets")
     return B
 
 
 def _chunk_rows(k_new, v_new, k_pool, v_pool):
     """Pointers and common row step of new K and V rows [T, H_kv, D] for pools [P, ps, H_kv, D]."""
-    if k_new.shape != v_new.shape or k_new.dtype != v_new.dtype:
+    if k_new.dtype != v_new.dtype or k_new.shape != v_new.shape:
         raise ValueError("k_new and v_new must be alike")
     if k_pool.shape != v_pool.shape or k_pool.shape[2:] != k_new.shape[1:]:
         raise ValueError("pools must be [num_pages, page_size, H_kv, D] with the new rows' H_kv and D")
-    (k, step), (v, v_step) = _rows(k_new), _rows(v_new)
+    k, step = _rows(k_new)
+    v, v_step = _rows(v_new)
     if step != v_step:
         raise ValueError("k_new and v_new rows must be equally far apart")
+    if k_new.get_device() != k_pool.get_device() or v_new.get_device() != k_pool.get_device():
+        raise ValueError("new rows and pools must be on one device")
     return k, v, step
 
 
@@ -344,11 +372,10 @@ def ts_kv_append_chunk(k_new, v_new, k_pool, v_pool, block_table, seq_lens, q_in
     if k_pool.dtype != k_new.dtype or v_pool.dtype != k_new.dtype:
         raise TypeError("new rows and pools must have one dtype")
     k, v, step = _chunk_rows(k_new, v_new, k_pool, v_pool)
-    _require_current_device(k_new, v_new, k_pool, v_pool, block_table, seq_lens, q_indptr)
-    T, H_kv, D = k_new.shape
-    _check(lib().ts_kv_append_chunk(k, v, _ptr(k_pool), _ptr(v_pool), _ptr(block_table), block_table.shape[1],
-                                    _ptr(seq_lens), _ptr(q_indptr), step, T, B, H_kv, D, k_pool.shape[1],
-                                    k_pool.shape[0], _dt(k_new), _stream(stream)))
+    kp, vp, bt, lens, ptr = _pointers(k_pool, v_pool, block_table, seq_lens, q_indptr)
+    P, ps, H_kv, D = k_pool.shape
+    _check(lib().ts_kv_append_chunk(k, v, kp, vp, bt, block_table.shape[1], lens, ptr, step, k_new.shape[0], B, H_kv,
+                                    D, ps, P, _dt(k_new), _stream(stream)))
 
 
 def ts_kv_append_chunk_fp8(k_new, v_new, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, q_indptr,
@@ -358,12 +385,10 @@ def ts_kv_append_chunk_fp8(k_new, v_new, k_pool, v_pool, k_scale, v_scale, block
     B = _require_chunks(seq_lens, q_indptr, block_table)
     _require_fp8_cache(k_pool, v_pool, k_scale, v_scale)
     k, v, step = _chunk_rows(k_new, v_new, k_pool, v_pool)
-    _require_current_device(k_new, v_new, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, q_indptr)
-    T, H_kv, D = k_new.shape
-    _check(lib().ts_kv_append_chunk_fp8(k, v, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
-                                        _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(q_indptr),
-                                        step, T, B, H_kv, D, k_pool.shape[1], k_pool.shape[0], _dt(k_new),
-                                        _stream(stream)))
+    kp, vp, ks, vs, bt, lens, ptr = _pointers(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, q_indptr)
+    P, ps, H_kv, D = k_pool.shape
+    _check(lib().ts_kv_append_chunk_fp8(k, v, kp, vp, ks, vs, bt, block_table.shape[1], lens, ptr, step,
+                                        k_new.shape[0], B, H_kv, D, ps, P, _dt(k_new), _stream(stream)))
 
 
 def ts_kv_read_fp8(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, kv_indptr, k_out, v_out,
@@ -372,15 +397,15 @@ def ts_kv_read_fp8(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, kv_i
     or f32) becomes token t of sequence b; other rows stay as they were (see ts_attn.h)."""
     B = _require_chunks(seq_lens, kv_indptr, block_table)
     _require_fp8_cache(k_pool, v_pool, k_scale, v_scale)
-    if k_pool.shape != v_pool.shape or k_out.shape != v_out.shape or k_out.dtype != v_out.dtype or \
-            k_out.shape[1:] != k_pool.shape[2:]:
-        raise ValueError("k_out and v_out must be [rows, H_kv, D] with the pools' H_kv and D")
-    _require_current_device(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, kv_indptr, k_out, v_out)
     rows, H_kv, D = k_out.shape
-    _check(lib().ts_kv_read_fp8(_ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-                                block_table.shape[1], _ptr(seq_lens), _ptr(kv_indptr), rows, B, H_kv, D,
-                                k_pool.shape[1], k_pool.shape[0], _dt(k_out), _ptr(k_out), _ptr(v_out),
-                                _stream(stream)))
+    P, ps, H_pool, D_pool = k_pool.shape
+    if k_out.dtype != v_out.dtype or k_out.shape != v_out.shape or k_pool.shape != v_pool.shape or \
+            H_kv != H_pool or D != D_pool:
+        raise ValueError("k_out and v_out must be [rows, H_kv, D] with the pools' H_kv and D")
+    kp, vp, ks, vs, bt, lens, ptr, ko, vo = _pointers(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens,
+                                                      kv_indptr, k_out, v_out)
+    _check(lib().ts_kv_read_fp8(kp, vp, ks, vs, bt, block_table.shape[1], lens, ptr, rows, B, H_kv, D, ps, P,
+                                _dt(k_out), ko, vo, _stream(stream)))
 
 
 def ts_paged_prefill_workspace_size(T: int, B: int, H_q: int, H_kv: int, D: int) -> int:
@@ -404,14 +429,16 @@ def ts_paged_prefill_attn(q, k_pool, v_pool, block_table, seq_lens, q_indptr, sc
     if lse is None and return_lse:
         lse = torch.empty(T, H_q, dtype=torch.float32, device=q.device)
     _require_result(out, lse, q)
-    _require_current_device(q, k_pool, v_pool, block_table, seq_lens, q_indptr, out, lse, workspace)
+    if q.get_device() != k_pool.get_device():
+        raise ValueError("queries and pools must be on one device")
+    kp, vp, bt, lens, ptr, op, lp, wp = _pointers(k_pool, v_pool, block_table, seq_lens, q_indptr, out, lse,
+                                                  workspace)
     if workspace is None:
         workspace = new_workspace(ts_paged_prefill_workspace_size(T, B, H_q, H_kv, D), q.device)
-    _check(lib().ts_paged_prefill_attn(qp, step, _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
-                                       block_table.shape[1], _ptr(seq_lens), _ptr(q_indptr), T, B, H_q, H_kv, D, ps,
-                                       P, int(window), int(sinks), float(scale), _dt(q), _ptr(out), _ptr(lse),
-                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                       _stream(stream)))
+        wp = workspace.data_ptr()
+    _check(lib().ts_paged_prefill_attn(qp, step, kp, vp, bt, block_table.shape[1], lens, ptr, T, B, H_q, H_kv, D, ps,
+                                       P, int(window), int(sinks), float(scale), _dt(q), op, lp, wp,
+                                       workspace.nbytes, _stream(stream)))
     return (out, lse) if return_lse else out
 
 

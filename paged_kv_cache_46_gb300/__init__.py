@@ -495,7 +495,7 @@ def _require_fp8_cache(k_pool, v_pool, k_scale, v_scale):
         raise TypeError("fp8 pools hold e4m3fn codes as uint8")
     if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
         raise TypeError("fp8 scales are float32 [num_pages, page_size, H_kv]")
-    if tuple(k_scale.shape) != tuple(k_pool.shape[:3]) or tuple(v_scale.shape) != tuple(v_pool.shape[:3]):
+    if k_scale.shape != k_pool.shape[:3] or v_scale.shape != v_pool.shape[:3]:
         raise ValueError("scales must be [num_pages, page_size, H_kv] of their pool")
 
 

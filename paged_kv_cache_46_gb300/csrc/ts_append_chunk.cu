@@ -7,10 +7,10 @@
 // seq_lens[b] - n + j, in page block_table[b][pos / page_size] at row pos %
 // page_size (SwiftLLM page, section 3.1).
 //
-// Both kernels take one warp per row, K and V: the row's sequence is found by
-// a 32-way search over q_indptr, so no plan is made on the host and none has
-// to be kept, and a short chunk spreads over as many SMs as it has rows / 8.
-// Both are bound by HBM: each value is read once and written once.
+// A warp takes a row (K and V, or one of them where they are quantized) and
+// finds the row's sequence by a 32-way search over q_indptr: no plan is made on
+// the host and none has to be kept. Both are bound by HBM: each value is read
+// once and written once.
 #include <cuda_fp8.h>
 
 #include "ts_ragged.cuh"
@@ -18,14 +18,15 @@
 namespace ts {
 namespace {
 
-constexpr int kWarps = 8;  // rows per CTA
+constexpr int kWarps = 8;  // per CTA
 constexpr float kE4M3Max = 448.0f;
 
 struct ChunkRows {
   const int32_t* block_table;
   const int32_t* seq_lens;
   const int32_t* q_indptr;
-  int32_t bt_stride, T, B, H_kv, page_size, num_pages;
+  int32_t bt_stride, T, B, H_kv, num_pages;
+  PageSize page_size;
 };
 
 // Pool row of batch row r, or -1 if it has none (no sequence, a position in
@@ -76,70 +77,183 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_chunk_kernel(const uint
   }
 }
 
-// Eight values of a lane, widened.
+// Eight values of a lane as they are stored: four or eight words.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Eight {
+  uint32_t w[2 * sizeof(T)];
+  __device__ __forceinline__ void load(const T* p) {
+    const uint4* v = reinterpret_cast<const uint4*>(p);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = bf16x2_to_float2(w[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+      const uint4 a = v[i];
+      w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
     }
-  } else {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (sizeof(T) == 2)
+      return bf16x2_to_float2(w[i]);
+    else
+      return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+  // The sign bits of values 4 i .. 4 i + 3, as those of four codes.
+  __device__ __forceinline__ uint32_t signs(int i) const {
+    if constexpr (sizeof(T) == 2)
+      return __byte_perm(w[2 * i], w[2 * i + 1], 0x7531) & 0x80808080u;
+    else
+      return __byte_perm(__byte_perm(w[4 * i], w[4 * i + 1], 0x0073), __byte_perm(w[4 * i + 2], w[4 * i + 3], 0x0073),
+                         0x5410) & 0x80808080u;
+  }
+  // The largest magnitude's float32 bits. Magnitudes order as their bits do,
+  // with infinities and NaN above all others.
+  __device__ __forceinline__ uint32_t largest() const {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t m = 0x7fff7fffu;
+      const uint32_t a = __vmaxu2(__vmaxu2(w[0] & m, w[1] & m), __vmaxu2(w[2] & m, w[3] & m));
+      return max(a << 16, a & 0xffff0000u);
+    } else {
+      uint32_t a = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a = max(a, w[i] & 0x7fffffffu);
+      return a;
+    }
+  }
+};
+
+// The codes of a lane's eight values by the definition: one quotient each.
+template <typename T>
+__device__ __forceinline__ uint2 codes_by_definition(const Eight<T>& x, float scale) {
+  uint32_t code[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = x.pair(i / 2);
+    const float y = fminf(fmaxf(__fdiv_rn(i % 2 ? f.y : f.x, scale), -kE4M3Max), kE4M3Max);
+    code[i / 4] |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3)) << (8 * (i % 4));
+  }
+  return make_uint2(code[0], code[1]);
 }
+
+// Quotients rounded to nearest even by Markstein's theorems ("Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990), each
+// operation rounded once:
+//   - from a y within one unit in the last place of 1 / s, y + (1 - y s) y is
+//     the rounded reciprocal, unless s's significand is all ones;
+//   - from a q within one unit of x / s and the rounded reciprocal, q + (x - q s)
+//     times it is the rounded quotient.
+// x times the reciprocal may be off by one and a half units; a first step
+// brings it within one. The residuals have to be exact, which they are for s
+// >= 1e-10 / 448 and quotients of 2^-11 or more; smaller ones are off by units
+// of their last place and far below half of the smallest code.
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+  float q = x * inv;
+  q = fmaf(fmaf(-q, s, x), inv, q);
+  return fmaf(fmaf(-q, s, x), inv, q);
+}
+__device__ __forceinline__ float2 quotients(float2 x, float2 neg_s, float2 inv) {
+  float2 q = __fmul2_rn(x, inv);
+  q = __ffma2_rn(__ffma2_rn(q, neg_s, x), inv, q);
+  return __ffma2_rn(__ffma2_rn(q, neg_s, x), inv, q);
+}
+__device__ __forceinline__ float reciprocal(float s) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));  // within one unit
+  return fmaf(fmaf(-s, y, 1.f), y, y);
+}
+__device__ __forceinline__ bool all_ones(float s) { return (~__float_as_uint(s) & 0x007fffffu) == 0u; }
 
 // Quantization as ts_kv_append_fp8, bit for bit: a group is the D values of
 // one (token, kv head); scale = max(max |x|, 1e-10) / 448, code =
 // e4m3(clamp(x / scale, -448, 448)), in float32 rounded to nearest even.
-// D / 8 lanes hold a group, eight values each, so that a warp quantizes two
-// (D = 128) or four (D = 64) groups at a time and stores 8 bytes of codes per
-// lane. src_step: elements between rows of k_new (and of v_new).
+//
+// One warp per row of K, of V or of both. D / 8 lanes hold a group, eight values each,
+// so that a warp takes two (D = 128) or four (D = 64) groups at a time, and
+// loads kBatch times that before the first of it is quantized. A group shares
+// one divisor, so its quotients take a reciprocal and five multiply-adds each
+// instead of a division each. Groups that hold an infinity or NaN, or whose
+// scale's reciprocal may not be the rounded one, take the definition's divisions.
+// src_step: elements between rows of k_new (and of v_new).
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) kv_append_chunk_fp8_kernel(
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 5 : 4) kv_append_chunk_fp8_kernel(
     const T* __restrict__ k_new, const T* __restrict__ v_new, uint8_t* __restrict__ k_pool,
     uint8_t* __restrict__ v_pool, float* __restrict__ k_scale, float* __restrict__ v_scale, ChunkRows c,
-    int64_t src_step) {
+    int64_t src_step, int32_t both) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  constexpr int kLanes = D / 8, kPerStep = 32 / kLanes;
+  constexpr int kLanes = D / 8, kPerStep = 32 / kLanes, kBatch = 4;
   const int lane = threadIdx.x & 31;
-  const int r = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int w = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int r = both ? w : w >> 1;
   if (r >= c.T) return;
+  bool is_v = !both && (w & 1) != 0;
+  const int at = (lane % kLanes) * 8;
+  const T* src = (is_v ? v_new : k_new) + r * src_step + at;
+  Eight<T> x[kBatch];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = h0 + u * kPerStep + lane / kLanes;
+      if (h < c.H_kv) {
+        x[u].load(src + h * D);
+      } else {
+#pragma unroll
+        for (uint32_t& w : x[u].w) w = 0u;
+      }
+    }
+  };
+  load(0);  // the values do not wait for the row's place
   const int64_t row = chunk_pool_row(c, r, lane);
   if (row < 0) return;
-  const int at = (lane % kLanes) * 8;
-  // groups 0 .. H_kv - 1 are K's heads, the others V's
-  for (int g0 = 0; g0 < 2 * c.H_kv; g0 += kPerStep) {
-    const int gi = g0 + lane / kLanes;
-    const bool real = gi < 2 * c.H_kv;
-    const bool is_v = gi >= c.H_kv;
-    const int h = is_v ? gi - c.H_kv : gi;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (real) load8((is_v ? v_new : k_new) + r * src_step + h * D + at, x);
-    float amax = 0.f;
+  uint8_t* pool = (is_v ? v_pool : k_pool) + row * c.H_kv * D + at;
+  float* scales = (is_v ? v_scale : k_scale) + row * c.H_kv;
+  for (int h0 = 0;;) {
+    uint32_t top[kBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    for (int u = 0; u < kBatch; ++u) top[u] = x[u].largest();
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float scale = __fdiv_rn(fmaxf(amax, 1e-10f), kE4M3Max);
-    uint32_t code[2] = {0u, 0u};
+    for (int o = kLanes / 2; o > 0; o >>= 1)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float y = fminf(fmaxf(__fdiv_rn(x[i], scale), -kE4M3Max), kE4M3Max);
-      code[i / 4] |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3)) << (8 * (i % 4));
+      for (int u = 0; u < kBatch; ++u) top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = h0 + u * kPerStep + lane / kLanes;
+      float scale = quotient(fmaxf(__uint_as_float(top[u]), 1e-10f), kE4M3Max, 1.f / kE4M3Max);
+      const float inv = reciprocal(scale);
+      uint32_t two[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        two[i] = __nv_cvt_float2_to_fp8x2(
+            quotients(x[u].pair(i), make_float2(-scale, -scale), make_float2(inv, inv)), __NV_SATFINITE, __NV_E4M3);
+      // (the steps above lose the sign of a zero)
+      uint2 code = make_uint2(two[0] | two[1] << 16 | x[u].signs(0), two[2] | two[3] << 16 | x[u].signs(1));
+      if (__any_sync(0xffffffffu, top[u] >= 0x7f800000u || all_ones(scale))) {
+        if (top[u] >= 0x7f800000u) {  // as fmaxf takes the maximum: NaN do not count
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(x[u].pair(i).x), fabsf(x[u].pair(i).y)));
+          top[u] = __float_as_uint(amax);
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) {  // of finite groups: the same again
+          const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, top[u], o));
+          top[u] = __float_as_uint(fmaxf(__uint_as_float(top[u]), other));
+        }
+        scale = __fdiv_rn(fmaxf(__uint_as_float(top[u]), 1e-10f), kE4M3Max);
+        code = codes_by_definition(x[u], scale);
+      }
+      if (h < c.H_kv) {
+        *reinterpret_cast<uint2*>(pool + h * D) = code;
+        if (at == 0) scales[h] = scale;
+      }
     }
-    if (real) {
-      const int64_t cell = row * c.H_kv + h;
-      *reinterpret_cast<uint2*>((is_v ? v_pool : k_pool) + cell * D + at) = make_uint2(code[0], code[1]);
-      if (at == 0) (is_v ? v_scale : k_scale)[cell] = scale;
+    h0 += kBatch * kPerStep;
+    if (h0 >= c.H_kv) {
+      if (!both || is_v) return;
+      is_v = true;
+      h0 = 0;
+      src = v_new + r * src_step + at;
+      pool = v_pool + row * c.H_kv * D + at;
+      scales = v_scale + row * c.H_kv;
     }
+    load(h0);
   }
 }
 
@@ -177,10 +291,10 @@ ts_status check(const char* who, const void* k_new, const void* v_new, const voi
 struct RowLaunch {
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = {};
-  RowLaunch(int32_t rows, cudaStream_t stream) {
+  RowLaunch(int32_t rows, int per_cta, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>((rows - 1) / kWarps + 1));
+    cfg.gridDim = dim3(static_cast<unsigned>((rows - 1) / per_cta + 1));
     cfg.blockDim = dim3(kWarps * 32);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -191,12 +305,16 @@ struct RowLaunch {
 template <typename T>
 ts_status launch_fp8(int D, const void* k_new, const void* v_new, void* k_pool, void* v_pool, float* k_scale,
                      float* v_scale, const ChunkRows& c, int64_t new_stride, cudaStream_t stream) {
-  RowLaunch l(c.T, stream);
+  // A warp takes a row's K and V where that alone fills the device twice over
+  // (half as many searches: 22 us against 23 for 15,000 rows), one of them below
+  // (33 rows: 2.9 us against 3.6).
+  const int both = c.T >= 2 * 40 * device_sm_count() ? 1 : 0;
+  RowLaunch l(c.T, both ? kWarps : kWarps / 2, stream);
   auto kern = D == 64 ? kv_append_chunk_fp8_kernel<T, 64> : kv_append_chunk_fp8_kernel<T, 128>;
   LaunchTrace trace("kv_append_chunk_fp8_kernel", stream);
   return cuda_check(cudaLaunchKernelEx(&l.cfg, kern, static_cast<const T*>(k_new), static_cast<const T*>(v_new),
                                        static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool), k_scale,
-                                       v_scale, c, new_stride),
+                                       v_scale, c, new_stride, both),
                     "ts_kv_append_chunk_fp8: launch");
 }
 
@@ -214,8 +332,8 @@ extern "C" ts_status ts_kv_append_chunk(const void* k_new, const void* v_new, vo
                              q_indptr, new_stride, T, B, H_kv, D, page_size, num_pages, dtype, &enqueue);
   if (st != TS_OK || !enqueue) return st;
   const int64_t es = dtype == TS_F32 ? 4 : 2;
-  const ChunkRows c{block_table, seq_lens, q_indptr, bt_stride, T, B, H_kv, page_size, num_pages};
-  RowLaunch l(T, static_cast<cudaStream_t>(stream));
+  const ChunkRows c{block_table, seq_lens, q_indptr, bt_stride, T, B, H_kv, num_pages, PageSize(page_size)};
+  RowLaunch l(T, kWarps, static_cast<cudaStream_t>(stream));
   LaunchTrace trace("kv_append_chunk_kernel", l.cfg.stream);
   return cuda_check(cudaLaunchKernelEx(&l.cfg, kv_append_chunk_kernel, static_cast<const uint4*>(k_new),
                                        static_cast<const uint4*>(v_new), static_cast<uint4*>(k_pool),
@@ -241,7 +359,7 @@ extern "C" ts_status ts_kv_append_chunk_fp8(const void* k_new, const void* v_new
   for (const void* p : {k_scale, v_scale})
     if (reinterpret_cast<uintptr_t>(p) % 4 != 0)
       return fail(TS_ERR_INVALID_ARG, "%s: scale arrays must be 4-byte aligned", who);
-  const ChunkRows c{block_table, seq_lens, q_indptr, bt_stride, T, B, H_kv, page_size, num_pages};
+  const ChunkRows c{block_table, seq_lens, q_indptr, bt_stride, T, B, H_kv, num_pages, PageSize(page_size)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == TS_BF16)
     return launch_fp8<__nv_bfloat16>(D, k_new, v_new, k_pool, v_pool, k_scale, v_scale, c, new_stride, s);

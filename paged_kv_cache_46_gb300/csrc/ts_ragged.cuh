@@ -23,16 +23,26 @@ __device__ __forceinline__ int ragged_sequence(const int32_t* __restrict__ indpt
   return indptr[lo] <= row && row < indptr[lo + 1] ? lo : -1;
 }
 
-// Pool row (page * page_size + row in it) of the token at `pos` of sequence b;
-// -1 where its block-table slot or page id is out of range.
+// A page size and its logarithm (-1 where it is no power of two, which any call
+// but the appends refuses): a division per row is a fifth of a short row's work.
+struct PageSize {
+  int32_t rows, shift;
+  explicit PageSize(int32_t r) : rows(r), shift(-1) {
+    for (int32_t i = 0; i < 31; ++i)
+      if (r == (1 << i)) shift = i;
+  }
+};
+
+// Pool row (page * rows + row in it) of the token at `pos` of sequence b; -1
+// where its block-table slot or page id is out of range.
 __device__ __forceinline__ int64_t pool_row(const int32_t* __restrict__ block_table, int bt_stride, int b, int pos,
-                                            int page_size, int num_pages) {
+                                            PageSize page_size, int num_pages) {
   if (pos < 0) return -1;
-  const int slot = pos / page_size;
+  const int slot = page_size.shift >= 0 ? pos >> page_size.shift : pos / page_size.rows;
   if (slot >= bt_stride) return -1;
   const int page = block_table[static_cast<int64_t>(b) * bt_stride + slot];
   if (page < 0 || page >= num_pages) return -1;
-  return static_cast<int64_t>(page) * page_size + (pos - slot * page_size);
+  return static_cast<int64_t>(page) * page_size.rows + (pos - slot * page_size.rows);
 }
 
 }  // namespace ts

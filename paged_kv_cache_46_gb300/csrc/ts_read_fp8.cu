@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_fp8_kernel(
     const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool, const float* __restrict__ k_scale,
     const float* __restrict__ v_scale, const int32_t* __restrict__ block_table, int32_t bt_stride,
     const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ kv_indptr, int32_t rows, int32_t B,
-    int32_t H_kv, int32_t page_size, int32_t num_pages, T* __restrict__ k_out, T* __restrict__ v_out) {
+    int32_t H_kv, PageSize page_size, int32_t num_pages, T* __restrict__ k_out, T* __restrict__ v_out) {
   // Programmatic dependent launch as in ts_kv_append.
   pdl_wait_primary();
   pdl_launch_dependents();
@@ -107,7 +107,7 @@ ts_status launch(int D, const void* k_pool, const void* v_pool, const float* k_s
   LaunchTrace trace("kv_read_fp8_kernel", stream);
   return cuda_check(cudaLaunchKernelEx(&cfg, kern, static_cast<const uint8_t*>(k_pool),
                                        static_cast<const uint8_t*>(v_pool), k_scale, v_scale, block_table, bt_stride,
-                                       seq_lens, kv_indptr, rows, B, H_kv, page_size, num_pages,
+                                       seq_lens, kv_indptr, rows, B, H_kv, PageSize(page_size), num_pages,
                                        static_cast<T*>(k_out), static_cast<T*>(v_out)),
                     "ts_kv_read_fp8: launch");
 }

@@ -281,3 +281,29 @@ def test_appends_and_attention_captured_together():
             assert np.array_equal(got.double().cpu().numpy(), ref, equal_nan=True)
         assert ts.ts_read_device_error(ws) == 0
         check_attention(out, lse, case.oracle(torch.from_numpy(want[0]), torch.from_numpy(want[1])), 64, 80, "bf16")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_fp8_append_of_infinities_nan_and_extremes_is_the_single_tokens(dtype, D):
+    """Groups with infinities, NaN, both, the type's largest and smallest values, all equal."""
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(40, 3, D, generator=g)
+    inf, nan, top = float("inf"), float("nan"), torch.finfo(dtype).max
+    for row, (i, value) in enumerate([(0, inf), (5, -inf), (D - 1, nan), (3, -nan), (7, top), (8, -top),
+                                      (9, torch.finfo(dtype).tiny)]):
+        x[row, 0, i] = value
+        x[row + 7, 1] = value
+    x[14, 2, 3], x[14, 2, 4] = inf, nan
+    x[15], x[16] = 1e-30, -0.0
+    x[17] = torch.finfo(dtype).tiny
+    x = x.to(dtype).to(DEV)
+    bt = torch.randperm(5, generator=g).to(torch.int32)[None].to(DEV)
+    new = [torch.zeros(5, 8, 3, D, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    new += [torch.zeros(5, 8, 3, device=DEV) for _ in range(2)]
+    old = [torch.zeros_like(t) for t in new]
+    ts.ts_kv_append_chunk_fp8(x, -x, *new, bt, _i32([40]), _i32([0, 40]))
+    ts.ts_kv_append_fp8(x, -x, *old, bt.expand(40, -1).contiguous(), torch.arange(40, dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    for a, b in zip(new, old):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))

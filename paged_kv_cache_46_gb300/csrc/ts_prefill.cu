@@ -467,7 +467,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
   __syncthreads();
   constexpr uint32_t tmem = 0;  // all 512 columns: there is no other place for them
   const uint32_t sQ = smem_u32(smem + L::kOffQ), sKV = smem_u32(smem + L::kOffKV);
-  pdl_wait_primary();
 
   const int tt = p.tile_tokens;
   bool ok = true;
@@ -480,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       // ---------------- pieces ------------------------------------------------
       Walk w;
       w.init(p, *start_seq, *start_off, static_cast<int>(u1 - u0), lane);
+      pdl_wait_primary();  // lengths and row offsets are read before it, all else behind it
       if (lane == 0) {
         p.split[k].row0 = -1;
         bool more = true;
@@ -524,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       }
     } else if (warp != 9) {
       // ---------------- K (warp 8) and V (warp 10): lane i holds page i of the key tile
+      pdl_wait_primary();
       const bool is_v = warp == 10;
       const CUtensorMap* map = is_v ? &vmap : &kmap;
       const int npg = kBN / p.page_size;
@@ -715,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---------------- softmax: one query row per thread -----------------------
+    pdl_wait_primary();
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + lanes + L::kTmemO + t * D;
@@ -940,6 +942,7 @@ template <int D>
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams p) {
   constexpr int kN = D / 32;  // groups of four columns per thread
   __shared__ uint2 rows_s[32][D / 4 + 1];
+  __shared__ float top_s[8][32];
   pdl_launch_dependents();
   pdl_wait_primary();
   const int k = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -948,28 +951,45 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams 
   const int tile = r / kBM, rt = r % kBM / p.g, j = tile * p.tile_tokens + rt;
   const bool real = rt < p.tile_tokens && j < si.tokens;
   if (si.row0 < 0 || !__syncthreads_or(real)) return;
+  // the rows' largest LSE: the parts shared out among the warps
   float mx = -INFINITY;
   auto at = [&](int i) { return static_cast<int64_t>(i == 0 ? si.slot : 2 * (k + i)) * p.slot_rows; };
-#pragma unroll 4
-  for (int i = 0; i < si.parts; ++i) mx = fmaxf(mx, real ? p.part_lse[at(i) + r] : -INFINITY);
+  if (real)
+    for (int i = warp; i < si.parts; i += 8) mx = fmaxf(mx, p.part_lse[at(i) + r]);
+  top_s[warp][lane] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) mx = fmaxf(mx, top_s[w][lane]);
   const float ms = mx == -INFINITY ? 0.f : mx;
   float4 a[kN];
   float sum = 0.f;
 #pragma unroll
   for (int x = 0; x < kN; ++x) a[x] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (real) {
-#pragma unroll 2
-    for (int i = 0; i < si.parts; ++i) {
-      const float wt = __expf(p.part_lse[at(i) + r] - ms);
-      const float4* o = reinterpret_cast<const float4*>(p.part_o) + at(i) * (D / 4) + r;
-      sum += wt;
+    // four parts' loads in flight: with one, an item cut 20 times took 20 us
+    for (int i0 = 0; i0 < si.parts; i0 += 4) {
+      float lse[4];
+      float4 v[4][kN];
 #pragma unroll
-      for (int x = 0; x < kN; ++x) {
-        const float4 v = o[static_cast<int64_t>(warp + 8 * x) * p.slot_rows];
-        a[x].x += wt * v.x;
-        a[x].y += wt * v.y;
-        a[x].z += wt * v.z;
-        a[x].w += wt * v.w;
+      for (int u = 0; u < 4; ++u) {
+        const int i = min(i0 + u, si.parts - 1);
+        const float4* o = reinterpret_cast<const float4*>(p.part_o) + at(i) * (D / 4) + r;
+        lse[u] = i0 + u < si.parts ? p.part_lse[at(i) + r] : -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kN; ++x) v[u][x] = o[static_cast<int64_t>(warp + 8 * x) * p.slot_rows];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (i0 + u >= si.parts) break;
+        const float wt = __expf(lse[u] - ms);
+        sum += wt;
+#pragma unroll
+        for (int x = 0; x < kN; ++x) {
+          a[x].x += wt * v[u][x].x;
+          a[x].y += wt * v[u][x].y;
+          a[x].z += wt * v[u][x].z;
+          a[x].w += wt * v[u][x].w;
+        }
       }
     }
   }

@@ -11,7 +11,7 @@
 // g) tokens) of one kv head of one sequence, and 128 keys at a time.
 //
 // Split. Items have 1 to thousands of key tiles, so the key tiles of all items
-// (in order of sequence, kv head, token block; one extra unit per item for its
+// (in order of sequence, kv head, token block; some extra units per item for its
 // queries and epilogue) are cut into equal contiguous ranges, one per SM. Each
 // CTA computes the cut in its prologue from the lengths. An item cut between
 // CTAs leaves float32 states that prefill_merge_kernel joins by LSE
@@ -45,7 +45,6 @@ constexpr int kBM = 128;  // query rows per tile
 constexpr int kBN = 128;  // keys per tile
 constexpr int kThreads = 384;
 constexpr int kAtom = kBN * 128;  // one [128 rows x 64 bf16] SW128 atom
-constexpr int kItemUnits = 1;     // units an item counts beyond its key tiles
 constexpr int kBadRing = 16;      // key tiles whose bad-page mask is kept
 constexpr float kLog2eC = 1.4426950408889634f;
 constexpr float kLn2C = 0.6931471805599453f;
@@ -94,6 +93,7 @@ struct PrefillParams {
   const int32_t* q_indptr;     // [B + 1]
   int32_t T, B, bt_stride, H_q, H_kv, g, page_size, num_pages, window, sinks;
   int32_t tile_tokens;  // tokens per tile: 128 / g
+  int32_t item_units;   // units an item counts beyond its key tiles
   int32_t min_units;    // units a CTA takes at least, while there are any
   int32_t slot_rows;    // rows of a partial state: 128 or 256
   float scale_log2;
@@ -262,13 +262,13 @@ struct Walk {
     if (n <= 0) return;
     s = load_seq(p, b);
     long long c = 0;  // units of one kv head
-    for (int i = lane; i < s.blocks; i += 32) c += load_item(p, s, i).nt + kItemUnits;
+    for (int i = lane; i < s.blocks; i += 32) c += load_item(p, s, i).nt + p.item_units;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
     h = static_cast<int>(div_units(off, c));
     off -= h * c;
     for (int base = 0; base < s.blocks; base += 32) {
-      const int mine = base + lane < s.blocks ? load_item(p, s, base + lane).nt + kItemUnits : 0;
+      const int mine = base + lane < s.blocks ? load_item(p, s, base + lane).nt + p.item_units : 0;
       int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -290,10 +290,10 @@ struct Walk {
   __device__ __forceinline__ bool next(const PrefillParams& p, int k, Piece& q, int& rest) {
     while (left > 0) {
       const Item it = load_item(p, s, block);
-      const int cost = it.nt + kItemUnits;
+      const int cost = it.nt + p.item_units;
       const int here = min(cost - rem, left);
       const bool owner = rem == 0;
-      const int t0 = max(0, rem - kItemUnits), t1 = max(t0, rem + here - kItemUnits);
+      const int t0 = max(0, rem - p.item_units), t1 = max(t0, rem + here - p.item_units);
       q.nk = t1 - t0;
       q.t0 = t0;
       q.ns = it.ns;
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
   auto seq_units = [&](int b, int first, int step) {
     const Seq s = load_seq(p, b);
     long long c = 0;
-    for (int i = first; i < s.blocks; i += step) c += load_item(p, s, i).nt + kItemUnits;
+    for (int i = first; i < s.blocks; i += step) c += load_item(p, s, i).nt + p.item_units;
     return c * p.H_kv;
   };
   long long mine = 0;
@@ -718,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     // ---------------- softmax: one query row per thread -----------------------
     pdl_wait_primary();
     const int t = warp >> 2, r = tid & 127;
+    const int rt = r / p.g, rh = r - rt * p.g, j = t * tt + rt;  // its token of the tile, head, token of the item
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + lanes + L::kTmemO + t * D;
     uint32_t steps = 0, tiles = 0;  // products of this tile; key tiles of the CTA's pieces so far
@@ -733,7 +734,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         tiles += nk;
         continue;
       }
-      const int rt = r / p.g, j = t * tt + rt;  // this row's token of the tile, of the item
       const int pos = q.p0 + j;
       const bool real = rt < tt && j < q.tokens;
       const int nq = q.tokens > tt ? 2 : 1;
@@ -865,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       const float inv = l > 0.f ? 1.0f / l : 0.f;
       const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
       const int slot = q.slot;
-      const int64_t row = static_cast<int64_t>(q.row0 + j) * p.H_q + q.head * p.g + r % p.g;
+      const int64_t row = static_cast<int64_t>(q.row0 + j) * p.H_q + q.head * p.g + rh;
       __syncwarp();
       if (lane == 0) mbar_arrive(b_taken(n % kPieces));
       if (nk > 0) {
@@ -1164,6 +1164,13 @@ extern "C" ts_status ts_paged_prefill_attn(const void* q, int64_t q_stride, cons
   prm.window = window;
   prm.sinks = sinks;
   prm.tile_tokens = kBM / g;
+  // An item's queries, first scores and epilogue take about as long as three of
+  // its key tiles (4.3 us against 1.5 at head dim 128): with more items than
+  // CTAs that is what balances them (16 ragged prompts: 298 us with one unit,
+  // 283 with two, 269 with three, 266 with four). With fewer, every item is cut
+  // and each part has that cost anyway (33 tokens: 15.8 us with one, 16.5 with four).
+  const int64_t items = static_cast<int64_t>(H_kv) * T / (2 * prm.tile_tokens);
+  prm.item_units = items >= ctas ? 4 : 1;
   prm.min_units = 2;
   prm.slot_rows = slot_rows_of(T, g);
   prm.scale_log2 = scale * kLog2eC;

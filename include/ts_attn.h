@@ -361,7 +361,7 @@ TS_API size_t ts_paged_prefill_workspace_size(int32_t T, int32_t B, int32_t H_q,
  *
  * bf16 runs on tcgen05 with float32 accumulation and softmax statistics; the
  * softmax weights are rounded to bf16 for the product with V, and O is divided
- * by the sum of the rounded weights. float32 runs on the CUDA cores. Long
+ * by the sum of the unrounded ones. float32 runs on the CUDA cores. Long
  * key ranges are cut over the SMs and joined by LSE; the cut depends only on
  * lengths and the device, so equal calls give equal bits.
  *
@@ -380,7 +380,7 @@ TS_API size_t ts_paged_prefill_workspace_size(int32_t T, int32_t B, int32_t H_q,
  * Pages that no row of a call sees are never read, nor are rows of a seen
  * page that lie past the sequence's end or outside every row's window. The
  * tokens of a page whose id is out of range, or past the block table's row,
- * count as absent and set TS_DEVERR_PAGE_RANGE. A V row that some rows of a
+ * (or its first 2^30 tokens) count as absent and set TS_DEVERR_PAGE_RANGE. A V row that some rows of a
  * 128-key tile see and others do not must be finite (the others weigh it by 0).
  * Supported: D in {64, 128}, H_q / H_kv up to 64, page_size in {8, 16, 32},
  * T up to 2^30, q_stride a multiple of 16 bytes.

@@ -28,7 +28,7 @@
 // order, so S(j + 1) of a tile may follow its P V(j) without a wait, and the
 // two tiles take turns: while one tile's softmax runs, the tensor pipe works
 // on the other. A row's reference for the exponents is the maximum of its first
-// key tile and moves only when a later tile's weights grow past 2^30, so most
+// key tile and moves only when a later tile's weights sum up to 2^14, so most
 // tiles need no maximum, and O in TMEM is rescaled rarely.
 // P is rounded to bf16 because the product's operands share one type; O is
 // divided by the sum of the weights before that rounding.
@@ -48,7 +48,7 @@ constexpr int kAtom = kBN * 128;  // one [128 rows x 64 bf16] SW128 atom
 constexpr int kBadRing = 16;      // key tiles whose bad-page mask is kept
 constexpr float kLog2eC = 1.4426950408889634f;
 constexpr float kLn2C = 0.6931471805599453f;
-constexpr float kMostSum = 1073741824.f;  // 2^30: sum of a tile's weights at which a row's reference moves
+constexpr float kMostSum = 16384.f;  // sum of a tile's weights at which a row's reference moves
 // 256 threads of softmax and 128 others: 256 * 216 + 128 * 72 == 384 * 168.
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
@@ -175,20 +175,22 @@ __device__ __forceinline__ Seq load_seq(const PrefillParams& p, int b) {
   return s;
 }
 
+__device__ __forceinline__ int tiles_of(int keys) { return keys > 0 ? (keys - 1) / kBN + 1 : 0; }
+
 __device__ __forceinline__ Item load_item(const PrefillParams& p, const Seq& s, int block) {
   Item it;
   it.j0 = block * 2 * p.tile_tokens;
   it.tokens = min(s.n - it.j0, 2 * p.tile_tokens);
   it.p0 = s.L - s.n + it.j0;
   // keys past the block table's row do not exist
-  const long long cap = static_cast<long long>(p.bt_stride) * p.page_size;
+  const long long cap = min(static_cast<long long>(p.bt_stride) * p.page_size, 1ll << 30);
   const int end = it.p0 + it.tokens;
   it.khi = static_cast<int>(min(static_cast<long long>(max(end, 0)), cap));
   it.klo = (p.window > 0 && it.p0 >= p.window) ? it.p0 - p.window + 1 : 0;
   if (it.klo <= p.sinks) it.klo = 0;  // the window meets the first tokens
   it.w0 = it.klo / kBN;
-  it.ns = it.klo > 0 ? min((p.sinks + kBN - 1) / kBN, it.w0) : 0;
-  it.nt = it.ns + max(0, (it.khi + kBN - 1) / kBN - it.w0);
+  it.ns = it.klo > 0 ? min(tiles_of(p.sinks), it.w0) : 0;
+  it.nt = it.ns + max(0, tiles_of(it.khi) - it.w0);
   return it;
 }
 
@@ -1085,7 +1087,8 @@ ts_status launch_prefill_f32(const float* q, int64_t q_stride, const float* k_po
                              const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
                              const int32_t* q_indptr, int32_t T, int32_t B, int32_t H_q, int32_t H_kv, int32_t D,
                              int32_t page_size, int32_t num_pages, int32_t window, int32_t sinks, float scale,
-                             float* out, float* lse, uint32_t* err_word, cudaStream_t stream);
+                             float* out, float* lse, uint32_t* err_word, float* part_o, float* part_lse, int32_t ctas,
+                             cudaStream_t stream);
 
 }  // namespace ts
 
@@ -1141,12 +1144,16 @@ extern "C" ts_status ts_paged_prefill_attn(const void* q, int64_t q_stride, cons
                 need);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t* err_word = static_cast<uint32_t*>(workspace);
+  const int ctas = paged_decode_ctas();
+  const WsLayout ws = workspace_layout(ctas, slot_rows_of(T, g), D);
+  unsigned char* wsb = static_cast<unsigned char*>(workspace);
+  float* part_o = reinterpret_cast<float*>(wsb + ws.part_o);
+  float* part_lse = reinterpret_cast<float*>(wsb + ws.part_lse);
   if (dtype == TS_F32)
     return launch_prefill_f32(static_cast<const float*>(q), q_stride, static_cast<const float*>(k_pool),
                               static_cast<const float*>(v_pool), block_table, bt_stride, seq_lens, q_indptr, T, B, H_q,
                               H_kv, D, page_size, num_pages, window, sinks, scale, static_cast<float*>(out), lse,
-                              err_word, s);
-  const int ctas = paged_decode_ctas();
+                              err_word, part_o, part_lse, ctas, s);
   PrefillParams prm;
   prm.out = static_cast<__nv_bfloat16*>(out);
   prm.lse = lse;
@@ -1175,11 +1182,9 @@ extern "C" ts_status ts_paged_prefill_attn(const void* q, int64_t q_stride, cons
   prm.slot_rows = slot_rows_of(T, g);
   prm.scale_log2 = scale * kLog2eC;
   prm.err_word = err_word;
-  const WsLayout ws = workspace_layout(ctas, prm.slot_rows, D);
-  unsigned char* wsb = static_cast<unsigned char*>(workspace);
   prm.split = reinterpret_cast<SplitItem*>(wsb + ws.split);
-  prm.part_o = reinterpret_cast<float*>(wsb + ws.part_o);
-  prm.part_lse = reinterpret_cast<float*>(wsb + ws.part_lse);
+  prm.part_o = part_o;
+  prm.part_lse = part_lse;
   CUtensorMap qmap, kmap, vmap;
   ts_status st = make_map(&qmap, q, D, H_q, D, T, q_stride, g, prm.tile_tokens);
   const uint64_t rows = static_cast<uint64_t>(num_pages) * page_size, width = static_cast<uint64_t>(H_kv) * D;

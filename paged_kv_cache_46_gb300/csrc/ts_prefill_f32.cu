@@ -1,21 +1,30 @@
 // ts_paged_prefill_attn, float32: the tensor pipe has no float32 product, so
 // this path runs on the CUDA cores and keeps float32 accuracy.
 //
-// A CTA takes 64 query rows (64 / g tokens times the g heads of one kv head)
+// A CTA takes 128 query rows (128 / g tokens times the g heads of one kv head)
 // and walks the keys that some of them sees in tiles of 64. Thread (y, x) of
-// 16 x 16 holds a 4 x 4 patch of the scores and 4 rows x D / 16 columns of O
-// in registers; K and V tiles are gathered page by page into shared memory,
-// padded so that 16-byte reads of different keys fall into different banks.
-// Running maximum and sum per row, in float32. What bounds it: the packed
-// float32 FMA rate and the shared-memory reads that feed it.
+// 16 x 16 holds an 8 x 4 patch of the scores and 8 rows x D / 16 columns of O
+// in registers, as pairs for the packed multiply-add; K and V tiles are
+// gathered page by page into shared memory, rows padded by 16 bytes so that
+// 16-byte reads of different keys fall into different banks. Running maximum
+// and sum per row, in float32.
+//
+// What bounds it: the packed float32 FMA rate. 12 16-byte shared reads feed 64
+// packed multiply-adds of the scores; a 4 x 4 patch (24 TFLOP/s at 1024 tokens
+// over 8192, 32 heads, D = 128) was bound by the reads instead.
+//
+// Few rows over a long context leave most SMs idle, so each CTA's keys are
+// split over as many CTAs as the device has room for twice over; the parts are
+// joined by LSE (16 tokens over 28,000: one part 5.5 ms).
+#include <algorithm>
 #include <cmath>
 
-#include "ts_common.cuh"
+#include "ts_ragged.cuh"
 
 namespace ts {
 namespace {
 
-constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+constexpr int kRows = 128, kKeys = 64, kThreads = 256;
 constexpr float kLog2eC = 1.4426950408889634f;
 constexpr float kLn2C = 0.6931471805599453f;
 
@@ -30,6 +39,9 @@ struct F32Params {
   const int32_t* q_indptr;
   int64_t q_stride;
   int32_t T, B, bt_stride, H_q, H_kv, g, page_size, num_pages, window, sinks, tile_tokens;
+  int32_t parts;    // CTAs that share a block's keys
+  float* part_o;    // [parts, T, H_q, D], used from two parts on
+  float* part_lse;  // [parts, T, H_q]
   float scale_log2;
   uint32_t* err_word;
 };
@@ -45,11 +57,13 @@ struct Smem {
   int seq, block;
 };
 
+__device__ __forceinline__ int tiles_of(int keys) { return keys > 0 ? (keys - 1) / kKeys + 1 : 0; }
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) prefill_f32_kernel(const F32Params p) {
+__global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(const F32Params p) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
-  constexpr int kStep = Smem<D>::kStep, kCols = D / 16;
+  constexpr int kStep = Smem<D>::kStep, kCols = D / 16, kPStep = kRows + 4;
   const int tid = threadIdx.x, lane = tid & 31;
   pdl_wait_primary();
   pdl_launch_dependents();
@@ -84,19 +98,22 @@ __global__ void __launch_bounds__(kThreads) prefill_f32_kernel(const F32Params p
     }
   }
   __syncthreads();
-  const int b = sm.seq, h = blockIdx.y;
+  const int b = sm.seq, h = blockIdx.y, part = blockIdx.z;
   if (b < 0) return;
   const int row0 = p.q_indptr[b], n = p.q_indptr[b + 1] - row0, L = max(p.seq_lens[b], 0);
   const int j0 = sm.block * p.tile_tokens, tokens = min(n - j0, p.tile_tokens);
   const int p0 = L - n + j0;
-  const long long cap = static_cast<long long>(p.bt_stride) * p.page_size;
+  const long long cap = min(static_cast<long long>(p.bt_stride) * p.page_size, 1ll << 30);
   const int khi = static_cast<int>(min(static_cast<long long>(max(p0 + tokens, 0)), cap));
   int klo = (p.window > 0 && p0 >= p.window) ? p0 - p.window + 1 : 0;
   if (klo <= p.sinks) klo = 0;
   const int w0 = klo / kKeys;
-  const int ns = klo > 0 ? min((p.sinks + kKeys - 1) / kKeys, w0) : 0;
-  const int nt = ns + max(0, (khi + kKeys - 1) / kKeys - w0);
-  if (tid == 0 && p0 + tokens > khi && p0 + tokens > 0) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
+  const int ns = klo > 0 ? min(tiles_of(p.sinks), w0) : 0;
+  const int nt = ns + max(0, tiles_of(khi) - w0);
+  if (tid == 0 && part == 0 && p0 + tokens > khi && p0 + tokens > 0)
+    set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
+  const int i0 = static_cast<int>(static_cast<long long>(nt) * part / p.parts);
+  const int i1 = static_cast<int>(static_cast<long long>(nt) * (part + 1) / p.parts);
 
   const int rows = tokens * p.g;
   for (int i = tid; i < kRows * (D / 4); i += kThreads) {
@@ -109,17 +126,18 @@ __global__ void __launch_bounds__(kThreads) prefill_f32_kernel(const F32Params p
     *reinterpret_cast<float4*>(sm.q + r * kStep + c) = v;
   }
   const int x = tid & 15, y = tid >> 4;
-  float m[4], l[4], o[4][kCols];
-  int pos[4];
+  float m[8], l[8];
+  float2 o[8][kCols / 2];
+  int pos[8];
 #pragma unroll
-  for (int a = 0; a < 4; ++a) {
+  for (int a = 0; a < 8; ++a) {
     m[a] = -INFINITY;
     l[a] = 0.f;
-    pos[a] = p0 + (y * 4 + a) / p.g;
+    pos[a] = p0 + (y * 8 + a) / p.g;
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) o[a][c] = 0.f;
+    for (int c = 0; c < kCols / 2; ++c) o[a][c] = make_float2(0.f, 0.f);
   }
-  for (int i = 0; i < nt; ++i) {
+  for (int i = i0; i < i1; ++i) {
     const int k0 = (i < ns ? i : w0 + i - ns) * kKeys;
     __syncthreads();  // the previous tile's reads are done
     if (tid < kKeys) {
@@ -135,47 +153,61 @@ __global__ void __launch_bounds__(kThreads) prefill_f32_kernel(const F32Params p
       sm.row[tid] = row;
     }
     __syncthreads();
-    for (int e = tid; e < kKeys * (D / 4); e += kThreads) {
-      const int key = e / (D / 4), c = e % (D / 4) * 4;
-      const int row = sm.row[key];
-      float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-      if (row >= 0) {
-        const int64_t at = (static_cast<int64_t>(row) * p.H_kv + h) * D + c;
-        kv = *reinterpret_cast<const float4*>(p.k_pool + at);
-        vv = *reinterpret_cast<const float4*>(p.v_pool + at);
+    // four rows' loads in flight per thread
+    constexpr int kVecs = kKeys * (D / 4);
+#pragma unroll
+    for (int e0 = 0; e0 < kVecs; e0 += 4 * kThreads) {
+      float4 kv[4], vv[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = e0 + u * kThreads + tid, key = e / (D / 4), c = e % (D / 4) * 4;
+        const int row = sm.row[key];
+        kv[u] = vv[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row >= 0) {
+          const int64_t at = (static_cast<int64_t>(row) * p.H_kv + h) * D + c;
+          kv[u] = *reinterpret_cast<const float4*>(p.k_pool + at);
+          vv[u] = *reinterpret_cast<const float4*>(p.v_pool + at);
+        }
       }
-      *reinterpret_cast<float4*>(sm.k + key * kStep + c) = kv;
-      *reinterpret_cast<float4*>(sm.v + key * kStep + c) = vv;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = e0 + u * kThreads + tid, key = e / (D / 4), c = e % (D / 4) * 4;
+        *reinterpret_cast<float4*>(sm.k + key * kStep + c) = kv[u];
+        *reinterpret_cast<float4*>(sm.v + key * kStep + c) = vv[u];
+      }
     }
     __syncthreads();
-    float s[4][4] = {};
-#pragma unroll 4
-    for (int d = 0; d < D; d += 4) {
-      float4 qa[4], kb[4];
+    float2 s2[8][4];  // sums over even and over odd columns
 #pragma unroll
-      for (int a = 0; a < 4; ++a) qa[a] = *reinterpret_cast<const float4*>(sm.q + (y * 4 + a) * kStep + d);
+    for (int a = 0; a < 8; ++a)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s2[a][c] = make_float2(0.f, 0.f);
+#pragma unroll 2
+    for (int d = 0; d < D; d += 4) {
+      float4 kb[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) kb[c] = *reinterpret_cast<const float4*>(sm.k + (x + 16 * c) * kStep + d);
 #pragma unroll
-      for (int a = 0; a < 4; ++a)
+      for (int a = 0; a < 8; ++a) {
+        const float4 qa = *reinterpret_cast<const float4*>(sm.q + (y * 8 + a) * kStep + d);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          s[a][c] = fmaf(qa[a].x, kb[c].x, s[a][c]);
-          s[a][c] = fmaf(qa[a].y, kb[c].y, s[a][c]);
-          s[a][c] = fmaf(qa[a].z, kb[c].z, s[a][c]);
-          s[a][c] = fmaf(qa[a].w, kb[c].w, s[a][c]);
+          s2[a][c] = __ffma2_rn(make_float2(qa.x, qa.y), make_float2(kb[c].x, kb[c].y), s2[a][c]);
+          s2[a][c] = __ffma2_rn(make_float2(qa.z, qa.w), make_float2(kb[c].z, kb[c].w), s2[a][c]);
         }
+      }
     }
+    float e[8][4];
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
+    for (int a = 0; a < 8; ++a) {
       const int first = (p.window > 0 && pos[a] >= p.window) ? pos[a] - p.window + 1 : 0;
       float mx = -INFINITY;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int key = x + 16 * c, t = k0 + key;
         const bool vis = sm.row[key] >= 0 && t <= pos[a] && (t >= first || t < p.sinks);
-        s[a][c] = vis ? s[a][c] * p.scale_log2 : -INFINITY;
-        mx = fmaxf(mx, s[a][c]);
+        e[a][c] = vis ? (s2[a][c].x + s2[a][c].y) * p.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, e[a][c]);
       }
 #pragma unroll
       for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
@@ -186,46 +218,93 @@ __global__ void __launch_bounds__(kThreads) prefill_f32_kernel(const F32Params p
       float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const float e = exp2f(s[a][c] - ms);
-        sm.p[(x + 16 * c) * (kRows + 4) + y * 4 + a] = e;
-        sum += e;
+        e[a][c] = exp2f(e[a][c] - ms);
+        sum += e[a][c];
       }
 #pragma unroll
       for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
       l[a] = l[a] * alpha + sum;
+      const float2 al = make_float2(alpha, alpha);
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) o[a][c] *= alpha;
+      for (int c = 0; c < kCols / 2; ++c) o[a][c] = __fmul2_rn(o[a][c], al);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float4* to = reinterpret_cast<float4*>(sm.p + (x + 16 * c) * kPStep + y * 8);
+      to[0] = make_float4(e[0][c], e[1][c], e[2][c], e[3][c]);
+      to[1] = make_float4(e[4][c], e[5][c], e[6][c], e[7][c]);
     }
     __syncwarp();  // a row's weights are written and read by one half warp
-#pragma unroll 4
+#pragma unroll 2
     for (int key = 0; key < kKeys; ++key) {
-      const float4 w = *reinterpret_cast<const float4*>(sm.p + key * (kRows + 4) + y * 4);
-      const float wa[4] = {w.x, w.y, w.z, w.w};
+      const float4 wa = *reinterpret_cast<const float4*>(sm.p + key * kPStep + y * 8);
+      const float4 wb = *reinterpret_cast<const float4*>(sm.p + key * kPStep + y * 8 + 4);
+      const float w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
       for (int c = 0; c < kCols; c += 4) {
         const float4 v = *reinterpret_cast<const float4*>(sm.v + key * kStep + c * 16 + x * 4);
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          o[a][c] = fmaf(wa[a], v.x, o[a][c]);
-          o[a][c + 1] = fmaf(wa[a], v.y, o[a][c + 1]);
-          o[a][c + 2] = fmaf(wa[a], v.z, o[a][c + 2]);
-          o[a][c + 3] = fmaf(wa[a], v.w, o[a][c + 3]);
+        for (int a = 0; a < 8; ++a) {
+          const float2 w2 = make_float2(w[a], w[a]);
+          o[a][c / 2] = __ffma2_rn(w2, make_float2(v.x, v.y), o[a][c / 2]);
+          o[a][c / 2 + 1] = __ffma2_rn(w2, make_float2(v.z, v.w), o[a][c / 2 + 1]);
         }
       }
     }
   }
+  const bool whole = p.parts == 1;
+  const int64_t all = static_cast<int64_t>(p.T) * p.H_q * part;
 #pragma unroll
-  for (int a = 0; a < 4; ++a) {
-    const int r = y * 4 + a;
+  for (int a = 0; a < 8; ++a) {
+    const int r = y * 8 + a;
     if (r >= rows) continue;
     const int64_t row = static_cast<int64_t>(row0 + j0 + r / p.g) * p.H_q + h * p.g + r % p.g;
     const float inv = l[a] > 0.f ? 1.f / l[a] : 0.f;
+    float* to = whole ? p.out + row * D : p.part_o + (all + row) * D;
 #pragma unroll
     for (int c = 0; c < kCols; c += 4)
-      *reinterpret_cast<float4*>(p.out + row * D + c * 16 + x * 4) =
-          make_float4(o[a][c] * inv, o[a][c + 1] * inv, o[a][c + 2] * inv, o[a][c + 3] * inv);
-    if (x == 0 && p.lse) p.lse[row] = l[a] > 0.f ? (m[a] + log2f(l[a])) * kLn2C : -INFINITY;
+      *reinterpret_cast<float4*>(to + c * 16 + x * 4) =
+          make_float4(o[a][c / 2].x * inv, o[a][c / 2].y * inv, o[a][c / 2 + 1].x * inv, o[a][c / 2 + 1].y * inv);
+    if (x == 0) {
+      const float lse = l[a] > 0.f ? (m[a] + log2f(l[a])) * kLn2C : -INFINITY;
+      if (!whole)
+        p.part_lse[all + row] = lse;
+      else if (p.lse)
+        p.lse[row] = lse;
+    }
   }
+}
+
+// Joins the parts of every row: a warp per (token, head).
+template <int D>
+__global__ void __launch_bounds__(256) prefill_f32_merge_kernel(const F32Params p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t rows = static_cast<int64_t>(p.T) * p.H_q;
+  if (row >= rows) return;
+  if (ragged_sequence(p.q_indptr, p.B, static_cast<int>(row / p.H_q), lane) < 0) return;  // no sequence's row
+  float mx = -INFINITY;
+  for (int i = lane; i < p.parts; i += 32) mx = fmaxf(mx, p.part_lse[i * rows + row]);
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+  const float ms = mx == -INFINITY ? 0.f : mx;
+  constexpr int kV = D / 32;  // values per lane
+  float a[kV], sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < kV; ++c) a[c] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < p.parts; ++i) {
+    const float w = expf(p.part_lse[i * rows + row] - ms);
+    sum += w;
+#pragma unroll
+    for (int c = 0; c < kV; ++c) a[c] = fmaf(w, p.part_o[(i * rows + row) * D + c * 32 + lane], a[c]);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int c = 0; c < kV; ++c) p.out[row * D + c * 32 + lane] = a[c] * inv;
+  if (lane == 0 && p.lse) p.lse[row] = sum > 0.f ? ms + logf(sum) : -INFINITY;
 }
 
 template <int D>
@@ -239,23 +318,32 @@ ts_status launch(const F32Params& prm, int blocks, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(prm.H_kv));
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(prm.H_kv), static_cast<unsigned>(prm.parts));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Smem<D>);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  LaunchTrace trace("prefill_f32_kernel", s);
-  return cuda_check(cudaLaunchKernelEx(&cfg, prefill_f32_kernel<D>, prm), "float32 prefill launch");
+  {
+    LaunchTrace trace("prefill_f32_kernel", s);
+    st = cuda_check(cudaLaunchKernelEx(&cfg, prefill_f32_kernel<D>, prm), "float32 prefill launch");
+  }
+  if (st != TS_OK || prm.parts == 1) return st;
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(prm.T) * prm.H_q + 7) / 8));
+  cfg.dynamicSmemBytes = 0;
+  LaunchTrace trace("prefill_f32_merge_kernel", s);
+  return cuda_check(cudaLaunchKernelEx(&cfg, prefill_f32_merge_kernel<D>, prm), "float32 prefill merge launch");
 }
 
 }  // namespace
 
+// part_o and part_lse have room for 2 * ctas blocks of 128 rows.
 ts_status launch_prefill_f32(const float* q, int64_t q_stride, const float* k_pool, const float* v_pool,
                              const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
                              const int32_t* q_indptr, int32_t T, int32_t B, int32_t H_q, int32_t H_kv, int32_t D,
                              int32_t page_size, int32_t num_pages, int32_t window, int32_t sinks, float scale,
-                             float* out, float* lse, uint32_t* err_word, cudaStream_t stream) {
+                             float* out, float* lse, uint32_t* err_word, float* part_o, float* part_lse, int32_t ctas,
+                             cudaStream_t stream) {
   F32Params prm;
   prm.q = q;
   prm.k_pool = k_pool;
@@ -277,11 +365,16 @@ ts_status launch_prefill_f32(const float* q, int64_t q_stride, const float* k_po
   prm.window = window;
   prm.sinks = sinks;
   prm.tile_tokens = kRows / prm.g;
+  prm.part_o = part_o;
+  prm.part_lse = part_lse;
   prm.scale_log2 = scale * kLog2eC;
   prm.err_word = err_word;
-  // one block per token block and kv head; a sequence's last may be partial
+  // one block per token block and kv head; a sequence's last may be partial.
+  // They hold T * H_q rows in blocks * H_kv * 128 places, so that as many parts
+  // as keep 2 * ctas blocks fit the places for parts.
   const long long blocks = T / prm.tile_tokens + static_cast<long long>(B < T ? B : T);
   if (blocks > INT32_MAX) return fail(TS_ERR_UNSUPPORTED, "ts_paged_prefill_attn: T=%d, B=%d", T, B);
+  prm.parts = static_cast<int32_t>(std::max(1ll, std::min(256ll, 2ll * ctas / (blocks * H_kv))));
   return D == 64 ? launch<64>(prm, static_cast<int>(blocks), stream) : launch<128>(prm, static_cast<int>(blocks), stream);
 }
 

@@ -24,9 +24,8 @@
 //   warp 11         walks the range, hands its pieces to the others, loads queries
 // S = Q K^T goes to TMEM (128 columns a tile); the softmax takes its row into
 // registers and writes P, as bf16, over the front half of the same columns,
-// where it is the A operand of O += P V. Products of one thread complete in
-// order, so S(j + 1) of a tile may follow its P V(j) without a wait, and the
-// two tiles take turns: while one tile's softmax runs, the tensor pipe works
+// where it is the A operand of O += P V; the next S into those columns waits
+// until that product has completed. The two tiles take turns: while one tile's softmax runs, the tensor pipe works
 // on the other. A row's reference for the exponents is the maximum of its first
 // key tile and moves only when a later tile's weights sum up to 2^14, so most
 // tiles need no maximum, and O in TMEM is rescaled rarely.
@@ -606,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       Turn kt(0), vt(1);                            // ring places of the next K and V tile
       Turn st[2] = {Turn(0), Turn(0)}, pt[2] = {Turn(0), Turn(0)};  // barriers of each tile's next S and P V
       uint32_t pieces = 0, used[2] = {0, 0};        // with products; of each tile
+      uint32_t pvs[2] = {0, 0};                     // P V products of each tile
       auto run_piece = [&](auto tiles_tag, const int nk) {
         constexpr int NQ = decltype(tiles_tag)::value;  // tiles with rows
         int left = nk;         // K tiles whose S products are not all issued
@@ -651,12 +651,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           __syncwarp();
           after_s(tag);
         };
+        // Products on different accumulators may overlap, so a buffer's next S
+        // waits until the P V that read its weights has completed.
+        auto pv_done = [&](int t) { return pvs[t] == 0 || mbar_wait(b_pvdone(t), (pvs[t] - 1) & 1); };
+        ok = __all_sync(0xffffffffu, pv_done(0) && pv_done(1));
         prime(T0());
         prime(T1());
-        if (kBufs == 3) prime(T0());
-        auto step = [&](auto tag, const bool first) {  // P V of tile t and the S product that it makes room for
+        // P V of tile t, and the S of its key tile after the next: with three
+        // buffers into that of the P V before, with two into its own
+        auto step = [&](auto tag, const bool first) {
           constexpr int t = decltype(tag)::value;
-          constexpr int ts = NQ == 1 ? 0 : (t + kBufs) % 2;  // whose S
+          constexpr int ts = NQ == 1 ? 0 : t, before = NQ == 1 ? 0 : 1 - t;
           const bool more = left > 0;
           // what they wait for, asked for all at once
           const uint32_t vbar = b_full(vt.at), kbar = b_full(kt.at), pbar = b_pfull(t, pt[t].at);
@@ -667,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           if (!good)
             good = (have_v || mbar_wait(vbar, vt.phase)) && (have_k || mbar_wait(kbar, kt.phase)) &&
                    (have_p || mbar_wait(pbar, pt[t].phase));
+          if (kBufs == 3 && more) good = good && pv_done(before);
           // O of the tile's last piece has been read out
           if (first && used[t] > 0) good = good && mbar_wait(b_ofree(t), (used[t] - 1) & 1);
           ok = __all_sync(0xffffffffu, good);
@@ -679,9 +685,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
               mma_bf16_tmem_a(L::kTmemO + t * D, pb * 128 + ks * 8, vb + ks * 128, iO, (!first || ks > 0) ? 1u : 0u);
             mma_commit(b_pvdone(t));
             if (t == NQ - 1) mma_commit(b_empty(vt.at));
-            if (more) issue_s(std::integral_constant<int, ts>());
+            if (kBufs == 3 && more) issue_s(std::integral_constant<int, ts>());
           }
           __syncwarp();
+          ++pvs[t];
+          if (kBufs == 2 && more) {
+            ok = __all_sync(0xffffffffu, pv_done(t));
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) issue_s(std::integral_constant<int, ts>());
+            __syncwarp();
+          }
           if (more) after_s(std::integral_constant<int, ts>());
           pt[t].template next<kBufs>();
           if (++pb == kBufs) pb = 0;

@@ -14,6 +14,7 @@ is no CPU fallback: a missing library raises immediately.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -197,6 +198,17 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _made_for(stream):
+    """Context in which tensors belong to the call's stream: torch hands a freed workspace on
+    in the order of the stream it was made for, and zeroes a new one there."""
+    if stream is None:
+        return _HERE
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
 def _rows(t: torch.Tensor):
     """Pointer and row step (elements) of a [rows, heads, D] tensor whose rows are contiguous."""
     rows, heads, D = t.shape
@@ -306,14 +318,16 @@ def ts_paged_decode_sink_attn(q, k_pool, v_pool, block_table, seq_lens, scale: f
     _require_cache(q, k_pool, v_pool)
     if seq_lens.numel() != B:
         raise ValueError("a batch of B sequences has B queries, B lengths and B block-table rows")
-    if out is None:
-        out = torch.empty(B, H_q, D, dtype=q.dtype, device=q.device)
-    if lse is None and return_lse:
-        lse = torch.empty(B, H_q, dtype=torch.float32, device=q.device)
+    with _made_for(stream):
+        if out is None:
+            out = torch.empty(B, H_q, D, dtype=q.dtype, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty(B, H_q, dtype=torch.float32, device=q.device)
     _require_result(out, lse, q)
     qp, kp, vp, bt, lens, op, lp, wp = _pointers(q, k_pool, v_pool, block_table, seq_lens, out, lse, workspace)
     if workspace is None:
-        workspace = new_workspace(ts_paged_decode_workspace_size(B, H_q, D), q.device)
+        with _made_for(stream):
+            workspace = new_workspace(ts_paged_decode_workspace_size(B, H_q, D), q.device)
         wp = workspace.data_ptr()
     _check(lib().ts_paged_decode_sink_attn(qp, kp, vp, bt, block_table.shape[1], lens, B, H_q, H_kv, D, ps, P,
                                            int(window), int(sinks), float(scale), _dt(q), op, lp, wp,
@@ -424,17 +438,19 @@ def ts_paged_prefill_attn(q, k_pool, v_pool, block_table, seq_lens, q_indptr, sc
     P, ps, H_kv, _ = k_pool.shape
     _require_cache(q, k_pool, v_pool)
     qp, step = _rows(q)
-    if out is None:
-        out = torch.empty(T, H_q, D, dtype=q.dtype, device=q.device)
-    if lse is None and return_lse:
-        lse = torch.empty(T, H_q, dtype=torch.float32, device=q.device)
+    with _made_for(stream):
+        if out is None:
+            out = torch.empty(T, H_q, D, dtype=q.dtype, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty(T, H_q, dtype=torch.float32, device=q.device)
     _require_result(out, lse, q)
     if q.get_device() != k_pool.get_device():
         raise ValueError("queries and pools must be on one device")
     kp, vp, bt, lens, ptr, op, lp, wp = _pointers(k_pool, v_pool, block_table, seq_lens, q_indptr, out, lse,
                                                   workspace)
     if workspace is None:
-        workspace = new_workspace(ts_paged_prefill_workspace_size(T, B, H_q, H_kv, D), q.device)
+        with _made_for(stream):
+            workspace = new_workspace(ts_paged_prefill_workspace_size(T, B, H_q, H_kv, D), q.device)
         wp = workspace.data_ptr()
     _check(lib().ts_paged_prefill_attn(qp, step, kp, vp, bt, block_table.shape[1], lens, ptr, T, B, H_q, H_kv, D, ps,
                                        P, int(window), int(sinks), float(scale), _dt(q), op, lp, wp,

@@ -249,13 +249,13 @@ constexpr int kPieceReaders = 11;  // warps that read each piece
 
 // The CTA's range of units, walked piece by piece.
 struct Walk {
-  int left;              // units of the range still to walk
+  long long left;        // units of the range still to walk
   int b, h, block, rem;  // the next unit: item, and unit within it
   Seq s;
   bool first;  // no piece returned yet
 
   // A whole warp finds the item: unit `off` of sequence b0, `n` units to walk.
-  __device__ __forceinline__ void init(const PrefillParams& p, int b0, long long off, int n, int lane) {
+  __device__ __forceinline__ void init(const PrefillParams& p, int b0, long long off, long long n, int lane) {
     left = n;
     b = b0;
     first = true;
@@ -292,7 +292,7 @@ struct Walk {
     while (left > 0) {
       const Item it = load_item(p, s, block);
       const int cost = it.nt + p.item_units;
-      const int here = min(cost - rem, left);
+      const int here = static_cast<int>(min(static_cast<long long>(cost - rem), left));
       const bool owner = rem == 0;
       const int t0 = max(0, rem - p.item_units), t1 = max(t0, rem + here - p.item_units);
       q.nk = t1 - t0;
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     if (warp == 11) {
       // ---------------- pieces ------------------------------------------------
       Walk w;
-      w.init(p, *start_seq, *start_off, static_cast<int>(u1 - u0), lane);
+      w.init(p, *start_seq, *start_off, u1 - u0, lane);
       pdl_wait_primary();  // lengths and row offsets are read before it, all else behind it
       if (lane == 0) {
         p.split[k].row0 = -1;
@@ -590,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       }
     } else if (warp == 9) {
       // ---------------- products --------------------------------------------
+      pdl_wait_primary();  // no bounded wait runs while the previous kernel does
       // The whole warp runs this code and one elected lane issues: descriptors
       // and loop counts stay in uniform registers, as the instruction wants
       // them. (Run by one lane in a branch of its own, every product moved its

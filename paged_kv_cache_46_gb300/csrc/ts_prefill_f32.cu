@@ -284,7 +284,8 @@ __global__ void __launch_bounds__(256) prefill_f32_merge_kernel(const F32Params 
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int64_t rows = static_cast<int64_t>(p.T) * p.H_q;
   if (row >= rows) return;
-  if (ragged_sequence(p.q_indptr, p.B, static_cast<int>(row / p.H_q), lane) < 0) return;  // no sequence's row
+  const int b = ragged_sequence(p.q_indptr, p.B, static_cast<int>(row / p.H_q), lane);
+  if (b < 0 || p.q_indptr[b] < 0 || p.q_indptr[b + 1] > p.T) return;  // no sequence's row, no parts
   float mx = -INFINITY;
   for (int i = lane; i < p.parts; i += 32) mx = fmaxf(mx, p.part_lse[i * rows + row]);
 #pragma unroll

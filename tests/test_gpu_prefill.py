@@ -260,3 +260,46 @@ def test_chunk_by_chunk_equals_whole_prompt():
         check_attention(out, lse, o, 128, 300, "bf16", f"chunk at {at}")
         at += n
     _check(whole, ref, ref_lse)
+
+
+@pytest.mark.parametrize("D,window,sinks", [(64, 0, 0), (64, 1024, 64), (128, 0, 0), (128, 1024, 64)])
+def test_many_key_tiles_in_flight(D, window, sinks):
+    """Long runs of products, whose scores, weights and sums take turns in the same columns: an
+    order that is not enforced shows as rare wrong rows that differ from call to call."""
+    case = ChunkCase(D + window, [1100, 900, 700], [2500, 1200, 0], 16, 4, D, window=window, sinks=sinks)
+    ref = case.oracle()
+    first, first_lse = _run(case)
+    check_attention(first, first_lse, ref, D, int(case.L.max()), "bf16")
+    for _ in range(20):
+        out, lse = _run(case)
+        assert torch.equal(out, first) and torch.equal(lse, first_lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sequences_that_share_pages(dtype):
+    """Two rows of the block table with the same pages: one prompt, two different chunks of it."""
+    case = ChunkCase(21, [70], [130], 8, 2, 64, dtype=dtype)
+    case.bt = np.repeat(case.bt, 2, axis=0)
+    case.n, case.L = np.array([20, 50]), np.array([200, 100])
+    case.indptr = np.array([0, 20, 70], dtype=np.int32)
+    _check(case, *_run(case))
+
+
+def test_what_a_call_allocates_belongs_to_its_stream(monkeypatch):
+    """Memory freed while a call runs on a stream of its own is handed on in that stream's order."""
+    case = ChunkCase(22, [64], [64], 8, 2, 64)
+    s = torch.cuda.Stream()
+    a = case.device()
+    torch.cuda.synchronize()
+    made = []
+    new = ts.new_workspace
+    monkeypatch.setattr(ts, "new_workspace", lambda *x: made.append(torch.cuda.current_stream()) or new(*x))
+    for stream in (s, s.cuda_stream):
+        out, lse = ts.ts_paged_prefill_attn(**a, stream=stream, return_lse=True)
+        s.synchronize()
+        _check(case, out, lse)
+    q = a["q"][:1].contiguous()
+    ts.ts_paged_decode_sink_attn(q, a["k_pool"], a["v_pool"], a["block_table"], a["seq_lens"], case.scale, 32, 4,
+                                 stream=s)
+    s.synchronize()
+    assert [x.cuda_stream for x in made] == [s.cuda_stream] * 3

@@ -25,8 +25,23 @@
 // S = Q K^T goes to TMEM (128 columns a tile); the softmax takes its row into
 // registers and writes P, as bf16, over the front half of the same columns,
 // where it is the A operand of O += P V; the next S into those columns waits
-// until that product has completed. The two tiles take turns: while one tile's softmax runs, the tensor pipe works
-// on the other. A row's reference for the exponents is the maximum of its first
+// until that product has completed. The two tiles take turns: while one tile's
+// softmax runs, the tensor pipe works on the other.
+//
+// What bounds it, measured inside a 32k-token run at head dim 128 (clocks of a
+// step of both tiles, 3,000 in all; the products alone take 2,048): each tile's
+// own chain of S (512, and 350 until the softmax sees it), loads from TMEM
+// (470), weights (980: two exponentials and a conversion per eight clocks and
+// warp), issue and run of P V (512 + 540), since TMEM has room for one score
+// tile per query tile there. 4096 tokens over 32,768, 32 / 8 heads of 128: 1.39
+// ms, 1.48 PFLOP/s at 1.77 GHz under the power limit. At head dim 64 a third
+// score buffer takes S off the chain (window 1024, 7,600 tokens: 132 us). Tried
+// against this: products of 64 keys with four score buffers (1.73 ms: an N = 64
+// product costs 47 clocks, not 32), the second half of P through shared memory
+// (1.63 ms), a row's keys over two warps (1.45 ms), scores loaded 32 at a time
+// between the weights (1.56 ms).
+//
+// A row's reference for the exponents is the maximum of its first
 // key tile and moves only when a later tile's weights sum up to 2^14, so most
 // tiles need no maximum, and O in TMEM is rescaled rarely.
 // P is rounded to bf16 because the product's operands share one type; O is
@@ -364,12 +379,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
   auto b_pfull = [&](int t, uint32_t n) { return smem_u32(&bars[2 * kRing + (2 + t) * kBufs + n % kBufs]); };
   auto buf_phase = [&](uint32_t n) { return (n / kBufs) & 1; };
   constexpr int kBar0 = 2 * kRing + 4 * kBufs;
-  auto b_pvdone = [&](int t) { return smem_u32(&bars[kBar0 + t]); };     // O of tile t has its last P V
-  auto b_ofree = [&](int t) { return smem_u32(&bars[kBar0 + 2 + t]); };  // O of tile t has been read out
-  const uint32_t b_qfull = smem_u32(&bars[kBar0 + 4]), b_qempty = smem_u32(&bars[kBar0 + 5]);
-  auto b_piece = [&](int i) { return smem_u32(&bars[kBar0 + 6 + i]); };
-  auto b_taken = [&](int i) { return smem_u32(&bars[kBar0 + 6 + kPieces + i]); };
-  static_assert((kBar0 + 6 + 2 * kPieces) * 8 <= L::kOffBad - L::kOffBar, "mbarriers fit their place");
+  auto b_ofree = [&](int t) { return smem_u32(&bars[kBar0 + t]); };  // O of tile t has been read out
+  // Tile t's P V number n has completed. With three score buffers the one before
+  // may be running still when it is asked for: two barriers in turn.
+  constexpr uint32_t kDone = kBufs == 3 ? 2 : 1;
+  auto b_pvdone = [&](int t, uint32_t n) { return smem_u32(&bars[kBar0 + 2 + 2 * t + n % kDone]); };
+  auto pv_phase = [&](uint32_t n) { return (n / kDone) & 1; };
+  const uint32_t b_qfull = smem_u32(&bars[kBar0 + 6]), b_qempty = smem_u32(&bars[kBar0 + 7]);
+  auto b_piece = [&](int i) { return smem_u32(&bars[kBar0 + 8 + i]); };
+  auto b_taken = [&](int i) { return smem_u32(&bars[kBar0 + 8 + kPieces + i]); };
+  static_assert((kBar0 + 8 + 2 * kPieces) * 8 <= L::kOffBad - L::kOffBar, "mbarriers fit their place");
   static_assert(kPieces * sizeof(Piece) == L::kOffMisc - L::kOffPieces, "piece ring");
   Piece* ring = reinterpret_cast<Piece*>(smem + L::kOffPieces);
   volatile uint32_t* bad_ring = reinterpret_cast<volatile uint32_t*>(smem + L::kOffBad);
@@ -388,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         mbar_init(b_sfull(t, i), 2);  // the products' commit and the issuer's own arrival
         mbar_init(b_pfull(t, i), 4);
       }
-      mbar_init(b_pvdone(t), 1);
+      for (int i = 0; i < 2; ++i) mbar_init(b_pvdone(t, i), 1);
       mbar_init(b_ofree(t), 4);
     }
     mbar_init(b_qfull, 1);
@@ -654,26 +673,35 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         };
         // Products on different accumulators may overlap, so a buffer's next S
         // waits until the P V that read its weights has completed.
-        auto pv_done = [&](int t) { return pvs[t] == 0 || mbar_wait(b_pvdone(t), (pvs[t] - 1) & 1); };
+        auto pv_done = [&](int t) { return pvs[t] == 0 || mbar_wait(b_pvdone(t, pvs[t] - 1), pv_phase(pvs[t] - 1)); };
         ok = __all_sync(0xffffffffu, pv_done(0) && pv_done(1));
         prime(T0());
         prime(T1());
-        // P V of tile t, and the S of its key tile after the next: with three
-        // buffers into that of the P V before, with two into its own
+        // P V of tile t and the tile's next S. With three buffers S goes into that
+        // of the product before and is issued first, so that it is there when the
+        // softmax has written this step's weights; with two it goes into that of
+        // this P V and comes behind it.
         auto step = [&](auto tag, const bool first) {
           constexpr int t = decltype(tag)::value;
           constexpr int ts = NQ == 1 ? 0 : t, before = NQ == 1 ? 0 : 1 - t;
           const bool more = left > 0;
-          // what they wait for, asked for all at once
           const uint32_t vbar = b_full(vt.at), kbar = b_full(kt.at), pbar = b_pfull(t, pt[t].at);
+          if (kBufs == 3 && more) {
+            ok = __all_sync(0xffffffffu, (ts > 0 || mbar_wait(kbar, kt.phase)) && pv_done(before));
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) issue_s(std::integral_constant<int, ts>());
+            __syncwarp();
+            after_s(std::integral_constant<int, ts>());
+          }
+          // what is left to wait for, asked for all at once
           const bool have_v = t > 0 || mbar_try_wait(vbar, vt.phase);
-          const bool have_k = ts > 0 || !more || mbar_try_wait(kbar, kt.phase);
+          const bool have_k = kBufs == 3 || ts > 0 || !more || mbar_try_wait(kbar, kt.phase);
           const bool have_p = mbar_try_wait(pbar, pt[t].phase);
           bool good = have_v && have_k && have_p;
           if (!good)
             good = (have_v || mbar_wait(vbar, vt.phase)) && (have_k || mbar_wait(kbar, kt.phase)) &&
                    (have_p || mbar_wait(pbar, pt[t].phase));
-          if (kBufs == 3 && more) good = good && pv_done(before);
           // O of the tile's last piece has been read out
           if (first && used[t] > 0) good = good && mbar_wait(b_ofree(t), (used[t] - 1) & 1);
           ok = __all_sync(0xffffffffu, good);
@@ -684,9 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
 #pragma unroll
             for (int ks = 0; ks < kBN / 16; ++ks)
               mma_bf16_tmem_a(L::kTmemO + t * D, pb * 128 + ks * 8, vb + ks * 128, iO, (!first || ks > 0) ? 1u : 0u);
-            mma_commit(b_pvdone(t));
+            mma_commit(b_pvdone(t, pvs[t]));
             if (t == NQ - 1) mma_commit(b_empty(vt.at));
-            if (kBufs == 3 && more) issue_s(std::integral_constant<int, ts>());
           }
           __syncwarp();
           ++pvs[t];
@@ -697,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
             if (elect_one()) issue_s(std::integral_constant<int, ts>());
             __syncwarp();
           }
-          if (more) after_s(std::integral_constant<int, ts>());
+          if (kBufs == 2 && more) after_s(std::integral_constant<int, ts>());
           pt[t].template next<kBufs>();
           if (++pb == kBufs) pb = 0;
           if (t == NQ - 1) vt.template next<kRing, 2>();
@@ -848,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           mx = fmaxf(fmaxf(mx, mx1), fmaxf(mx2, mx3)) * f;
           const float mnew = fmaxf(m, mx);
           if (i > 0) {  // O so far is rescaled: every P V of it must be done
-            ok = __all_sync(0xffffffffu, mbar_wait(b_pvdone(t), (steps - 1) & 1));
+            ok = __all_sync(0xffffffffu, mbar_wait(b_pvdone(t, steps - 1), pv_phase(steps - 1)));
             if (!ok) break;
             tc_fence_after();
             const float alpha = m == -INFINITY ? 0.f : fast_exp2(m - mnew);
@@ -886,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       __syncwarp();
       if (lane == 0) mbar_arrive(b_taken(n % kPieces));
       if (nk > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(b_pvdone(t), (steps - 1) & 1));
+        ok = __all_sync(0xffffffffu, mbar_wait(b_pvdone(t, steps - 1), pv_phase(steps - 1)));
         if (!ok) break;
         tc_fence_after();
       }

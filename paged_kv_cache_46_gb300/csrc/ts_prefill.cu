@@ -31,11 +31,12 @@
 // What bounds it, measured inside a 32k-token run at head dim 128 (clocks of a
 // step of both tiles, 3,000 in all; the products alone take 2,048): each tile's
 // own chain of S (512, and 350 until the softmax sees it), loads from TMEM
-// (470), weights (980: two exponentials and a conversion per eight clocks and
-// warp), issue and run of P V (512 + 540), since TMEM has room for one score
-// tile per query tile there. 4096 tokens over 32,768, 32 / 8 heads of 128: 1.39
-// ms, 1.48 PFLOP/s at 1.77 GHz under the power limit. At head dim 64 a third
-// score buffer takes S off the chain (window 1024, 7,600 tokens: 132 us). Tried
+// (470), weights (980; 710 for a warp that has the SM to itself, 510 of them the
+// exponentials), issue and run of P V (512 + 540), since TMEM has room for one
+// score tile per query tile there. 4096 tokens over 32,768, 32 / 8 heads of 128: 1.39
+// ms, 1.48 PFLOP/s at 1.77 GHz under the power limit; 16 ragged prompts of 7,900
+// tokens in all over up to 4,096 each: 292 us, 1.14 PFLOP/s. At head dim 64 a third
+// score buffer takes S off the chain (window 1024, 7,300 tokens: 132 us). Tried
 // against this: products of 64 keys with four score buffers (1.73 ms: an N = 64
 // product costs 47 clocks, not 32), the second half of P through shared memory
 // (1.63 ms), a row's keys over two warps (1.45 ms), scores loaded 32 at a time
@@ -1010,7 +1011,8 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams 
 #pragma unroll
   for (int x = 0; x < kN; ++x) a[x] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (real) {
-    // four parts' loads in flight: with one, an item cut 20 times took 20 us
+    // four parts' loads in flight (33 tokens over 1,000, cut into 5 parts
+    // each: 16.1 us both kernels, with one in flight 17.6)
     for (int i0 = 0; i0 < si.parts; i0 += 4) {
       float lse[4];
       float4 v[4][kN];
@@ -1215,11 +1217,15 @@ extern "C" ts_status ts_paged_prefill_attn(const void* q, int64_t q_stride, cons
   prm.tile_tokens = kBM / g;
   // An item's queries, first scores and epilogue take about as long as three of
   // its key tiles (4.3 us against 1.5 at head dim 128): with more items than
-  // CTAs that is what balances them (16 ragged prompts: 298 us with one unit,
-  // 283 with two, 269 with three, 266 with four). With fewer, every item is cut
-  // and each part has that cost anyway (33 tokens: 15.8 us with one, 16.5 with four).
+  // CTAs that is what balances them (16 ragged prompts: 310 us with one unit,
+  // 290 with four; 8 of 300 tokens: 62.3 and 60.9). With fewer, every item is cut
+  // and each part has that cost anyway (33 tokens: 15.4 us with one, 15.7 with
+  // four; 512 tokens: 26.4 and 26.6).
   const int64_t items = static_cast<int64_t>(H_kv) * T / (2 * prm.tile_tokens);
   prm.item_units = items >= ctas ? 4 : 1;
+  // Fewer, larger parts where there are few units: a part costs a launch's and
+  // the merge's latency (33 tokens over 1,000: 19.0 us with one unit each, 16.9
+  // with two, 17.9 with three, 19.1 with four, 25.0 with ten).
   prm.min_units = 2;
   prm.slot_rows = slot_rows_of(T, g);
   prm.scale_log2 = scale * kLog2eC;

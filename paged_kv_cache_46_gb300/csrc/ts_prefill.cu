@@ -898,6 +898,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           for (int c0 = 0; c0 < kBN; c0 += 32) weigh(c0, m == -INFINITY ? 0.f : m, l2);
         }
         l += l2.x + l2.y;
+        // The last weights are handed over once the P V before has completed: a
+        // barrier tells its newest phase only from the one before, and a tile that
+        // has the buffers for itself may be two products ahead of a late V tile.
+        if (i > 0 && i == nk - 1) {
+          ok = __all_sync(0xffffffffu, mbar_wait(b_pvdone(t, steps - 1), pv_phase(steps - 1)));
+          if (!ok) break;
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();

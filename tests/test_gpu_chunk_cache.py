@@ -307,3 +307,40 @@ def test_fp8_append_of_infinities_nan_and_extremes_is_the_single_tokens(dtype, D
     torch.cuda.synchronize()
     for a, b in zip(new, old):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H_kv,D", [(5, 64), (3, 128), (8, 128)])
+def test_fp8_append_of_many_rows_equals_that_of_few(dtype, H_kv, D):
+    """From 80 rows per SM on a warp takes a row's K and V; below, one of them."""
+    n = 81 * torch.cuda.get_device_properties(0).multi_processor_count
+    k, v, bt, L, ptr, P = _batch(H_kv + D, [n - 7, 0, 7], [3, 5, 40], H_kv, D, 16, dtype, fused=True)
+    k, v = k.to(DEV), v.to(DEV)
+    caches = []
+    for parts in (1, 3):
+        cache = [torch.full((P, 16, H_kv, D), 0x55, dtype=torch.uint8, device=DEV) for _ in range(2)] + \
+                [torch.full((P, 16, H_kv), -1.0, device=DEV) for _ in range(2)]
+        at = np.linspace(0, n, parts + 1).astype(int)
+        for lo, hi in zip(at[:-1], at[1:]):  # rows lo .. hi of every sequence that has some there
+            own = np.clip(ptr, lo, hi)
+            ts.ts_kv_append_chunk_fp8(k[lo:hi], v[lo:hi], *cache, _i32(bt), _i32(L - (ptr[1:] - own[1:])),
+                                      _i32(own - lo))
+        caches.append(cache)
+    torch.cuda.synchronize()
+    for whole, pieces in zip(*caches):
+        assert torch.equal(whole, pieces)
+    assert (caches[0][2] >= 0).sum().item() == n * H_kv
+
+
+def test_more_sequences_than_two_steps_of_the_search():
+    """The search over row offsets takes three steps from 1025 sequences on."""
+    rng = np.random.default_rng(8)
+    n, ctx = rng.integers(0, 3, size=1500), rng.integers(0, 20, size=1500)
+    k, v, bt, L, ptr, P = _batch(8, n, ctx, 2, 64, 8, torch.bfloat16)
+    pools = [torch.full((P, 8, 2, 64), float("nan"), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    before = [_bits(p).cpu().numpy() for p in pools]
+    ts.ts_kv_append_chunk(k.to(DEV), v.to(DEV), *pools, _i32(bt), _i32(L), _i32(ptr))
+    torch.cuda.synchronize()
+    ref = oracle.kv_append_chunk(*before, _bits(k).numpy(), _bits(v).numpy(), bt, L, ptr)
+    for got, want in zip(pools, ref):
+        assert np.array_equal(_bits(got).cpu().numpy(), want)

@@ -89,6 +89,15 @@ def test_many_sequences():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_sequences_than_the_prologue_keeps(dtype):
+    """Above 8192 sequences the units of a sequence are counted twice instead of kept."""
+    rng = np.random.default_rng(6)
+    n = (rng.random(8300) < 0.2).astype(int) * rng.integers(1, 4, size=8300)
+    case = ChunkCase(6, n, rng.integers(0, 20, size=8300), 2, 1, 64, ps=8, dtype=dtype)
+    _check(case, *_run(case), "8300 sequences")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rows_of_a_fused_projection_and_padding(dtype):
     """Strided query rows; rows behind the last sequence stay as they were."""
     case = ChunkCase(8, [40, 0, 90], [17, 3, 0], 8, 2, 64, dtype=dtype, fused=True, pad_rows=21)

@@ -318,10 +318,11 @@ def ts_paged_decode_sink_attn(q, k_pool, v_pool, block_table, seq_lens, scale: f
     _require_cache(q, k_pool, v_pool)
     if seq_lens.numel() != B:
         raise ValueError("a batch of B sequences has B queries, B lengths and B block-table rows")
-    with _made_for(stream):
-        if out is None:
+    if out is None:
+        with _made_for(stream):
             out = torch.empty(B, H_q, D, dtype=q.dtype, device=q.device)
-        if lse is None and return_lse:
+    if lse is None and return_lse:
+        with _made_for(stream):
             lse = torch.empty(B, H_q, dtype=torch.float32, device=q.device)
     _require_result(out, lse, q)
     qp, kp, vp, bt, lens, op, lp, wp = _pointers(q, k_pool, v_pool, block_table, seq_lens, out, lse, workspace)
@@ -438,10 +439,11 @@ def ts_paged_prefill_attn(q, k_pool, v_pool, block_table, seq_lens, q_indptr, sc
     P, ps, H_kv, _ = k_pool.shape
     _require_cache(q, k_pool, v_pool)
     qp, step = _rows(q)
-    with _made_for(stream):
-        if out is None:
+    if out is None:
+        with _made_for(stream):
             out = torch.empty(T, H_q, D, dtype=q.dtype, device=q.device)
-        if lse is None and return_lse:
+    if lse is None and return_lse:
+        with _made_for(stream):
             lse = torch.empty(T, H_q, dtype=torch.float32, device=q.device)
     _require_result(out, lse, q)
     if q.get_device() != k_pool.get_device():

@@ -28,23 +28,23 @@
 // until that product has completed. The two tiles take turns: while one tile's
 // softmax runs, the tensor pipe works on the other.
 //
-// What bounds it, measured inside a 32k-token run at head dim 128 (clocks of a
-// step of both tiles, 3,000 in all; the products alone take 2,048): each tile's
-// own chain of S (512, and 350 until the softmax sees it), loads from TMEM
-// (470), weights (980; 710 for a warp that has the SM to itself, 510 of them the
-// exponentials), issue and run of P V (512 + 540), since TMEM has room for one
-// score tile per query tile there. 4096 tokens over 32,768, 32 / 8 heads of 128: 1.39
-// ms, 1.48 PFLOP/s at 1.77 GHz under the power limit; 16 ragged prompts of 7,900
-// tokens in all over up to 4,096 each: 292 us, 1.14 PFLOP/s. At head dim 64 a third
-// score buffer takes S off the chain (window 1024, 7,300 tokens: 132 us). Tried
-// against this: products of 64 keys with four score buffers (1.73 ms: an N = 64
-// product costs 47 clocks, not 32), the second half of P through shared memory
-// (1.63 ms), a row's keys over two warps (1.45 ms), scores loaded 32 at a time
-// between the weights (1.56 ms).
+// What bounds it, by clock stamps inside a 32k-token run at head dim 128 (a step
+// of both tiles takes 3,000 clocks, 3,575 with the stamps; the products alone
+// would take 2,048): each tile's own chain of S (512, and 350 until the softmax
+// sees it), loads from TMEM (470), weights (980; 710 for a warp that has the SM
+// to itself, 510 of them the exponentials), issue and run of P V (512 + 540),
+// since TMEM has room for one score tile per query tile there. 4096 tokens over
+// 32,768, 32 / 8 heads of 128: 1.39 ms, 1.48 PFLOP/s at 1.77 GHz under the power
+// limit; 16 ragged prompts of 7,900 tokens in all, over up to 4,096 each: 292 us,
+// 1.14 PFLOP/s. At head dim 64 a third score buffer takes S off the chain (window
+// 1024, 7,300 tokens: 132 us). Tried against this: products of 64 keys with four
+// score buffers (1.73 ms: an N = 64 product costs 47 clocks, not 32), the second
+// half of P through shared memory (1.63 ms), a row's keys over two warps (1.45
+// ms), scores loaded 32 at a time between the weights (1.56 ms).
 //
-// A row's reference for the exponents is the maximum of its first
-// key tile and moves only when a later tile's weights sum up to 2^14, so most
-// tiles need no maximum, and O in TMEM is rescaled rarely.
+// A row's reference for the exponents is the maximum of its first key tile and
+// moves only when a later tile's weights sum up to 2^14, so most tiles need no
+// maximum, and O in TMEM is rescaled rarely.
 // P is rounded to bf16 because the product's operands share one type; O is
 // divided by the sum of the weights before that rounding.
 #include <cmath>

@@ -916,9 +916,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         ++tiles;
       }
       if (!ok) break;
-      // epilogue: O / sum and the LSE (no key: O = 0, LSE = -inf)
-      const float inv = l > 0.f ? 1.0f / l : 0.f;
-      const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+      // epilogue: O / sum and the LSE (no key: O = 0, LSE = -inf; a score that
+      // is NaN or +inf makes the sum NaN, and O and the LSE with it)
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
+      const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
       const int slot = q.slot;
       const int64_t row = static_cast<int64_t>(q.row0 + j) * p.H_q + q.head * p.g + rh;
       __syncwarp();
@@ -1049,13 +1050,13 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams 
       }
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a part's NaN stays one
 #pragma unroll
   for (int x = 0; x < kN; ++x)
     rows_s[lane][warp + 8 * x] =
         make_uint2(float2_to_bf16x2(a[x].x * inv, a[x].y * inv), float2_to_bf16x2(a[x].z * inv, a[x].w * inv));
   const int64_t out = real ? static_cast<int64_t>(si.row0 + j) * p.H_q + si.head * p.g + r % kBM % p.g : -1;
-  if (warp == 0 && real && p.lse) p.lse[out] = sum > 0.f ? ms + logf(sum) : -INFINITY;
+  if (warp == 0 && real && p.lse) p.lse[out] = sum == 0.f ? -INFINITY : ms + logf(sum);
   __syncthreads();
   // warp w writes rows w, w + 8, ...: one row of D / 4 pairs of words at a time
   for (int rr = warp; rr < 32; rr += 8) {

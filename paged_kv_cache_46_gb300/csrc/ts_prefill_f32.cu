@@ -259,14 +259,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(const F32Param
     const int r = y * 8 + a;
     if (r >= rows) continue;
     const int64_t row = static_cast<int64_t>(row0 + j0 + r / p.g) * p.H_q + h * p.g + r % p.g;
-    const float inv = l[a] > 0.f ? 1.f / l[a] : 0.f;
+    const float inv = l[a] == 0.f ? 0.f : 1.f / l[a];  // no key: O = 0, LSE = -inf; a NaN sum stays NaN
     float* to = whole ? p.out + row * D : p.part_o + (all + row) * D;
 #pragma unroll
     for (int c = 0; c < kCols; c += 4)
       *reinterpret_cast<float4*>(to + c * 16 + x * 4) =
           make_float4(o[a][c / 2].x * inv, o[a][c / 2].y * inv, o[a][c / 2 + 1].x * inv, o[a][c / 2 + 1].y * inv);
     if (x == 0) {
-      const float lse = l[a] > 0.f ? (m[a] + log2f(l[a])) * kLn2C : -INFINITY;
+      const float lse = l[a] == 0.f ? -INFINITY : (m[a] + log2f(l[a])) * kLn2C;
       if (!whole)
         p.part_lse[all + row] = lse;
       else if (p.lse)
@@ -302,10 +302,10 @@ __global__ void __launch_bounds__(256) prefill_f32_merge_kernel(const F32Params 
 #pragma unroll
     for (int c = 0; c < kV; ++c) a[c] = fmaf(w, p.part_o[(i * rows + row) * D + c * 32 + lane], a[c]);
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
   for (int c = 0; c < kV; ++c) p.out[row * D + c * 32 + lane] = a[c] * inv;
-  if (lane == 0 && p.lse) p.lse[row] = sum > 0.f ? ms + logf(sum) : -INFINITY;
+  if (lane == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : ms + logf(sum);
 }
 
 template <int D>

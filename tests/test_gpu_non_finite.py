@@ -1,0 +1,83 @@
+"""Scores that are not finite: a query that sees one has no softmax, so its O and LSE are NaN, and
+every other row keeps its bounds. LSE = -inf is for rows that see nothing, which a merge drops."""
+
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_46_gb300 as ts
+from chunk_cases import DEV, ChunkCase, check_attention
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from paged_kv_cache_46_gb300 import build
+    build.build()
+    assert torch.cuda.is_available()
+
+
+def _spoil(case, b, t, head, value):
+    """A copy of the key pool whose column 0 of token t, kv head `head`, of sequence b is `value`."""
+    k = case.k_pool.clone()
+    page, row = case.bt[b, t // case.ps], t % case.ps
+    assert torch.isfinite(k[page, row, head]).all()
+    k[page, row, head, 0] = value
+    return k
+
+
+def _reach(case):
+    """Largest scaled sum |q k| of finite keys and queries, as ChunkCase.oracle gives it."""
+    return case.scale * np.nanmax(case.k_pool.double().abs().sum(-1).numpy()) * case.q.double().abs().max().item()
+
+
+def _check(out, lse, ref, qk, case, what):
+    """Rows whose LSE is NaN in float64 are NaN, the others within their bounds (qk: see _reach)."""
+    o_ref, l_ref, a_ref = (x.copy() for x in ref[:3])
+    bad = np.isnan(l_ref)
+    assert bad.any() and not bad.all(), what
+    where = torch.from_numpy(bad).to(DEV)
+    assert torch.isnan(lse[where]).all(), f"{what}: {lse[where][~torch.isnan(lse[where])][:5]}"
+    assert torch.isnan(out[where]).all(), what
+    o_ref[bad], l_ref[bad], a_ref[bad] = 0.0, 0.0, 0.0
+    check_attention(out.masked_fill(where[..., None], 0.0), lse.masked_fill(where, 0.0), (o_ref, l_ref, a_ref, qk),
+                    case.D, int(case.L.max()), case.dtype, what)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 5)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+def test_prompt_attention_of_keys_that_are_not_finite(dtype, D, value, window, sinks):
+    """Column 0 of a key is infinite or NaN: scores of both signs, for the rows that see the key. Items
+    whole and cut between CTAs, where the merge has to keep them too."""
+    case = ChunkCase(3, [200, 3, 70], [900, 260, 0], 8, 2, D, ps=16, dtype=dtype, window=window, sinks=sinks)
+    k = _spoil(case, 0, 1030, 1, value)
+    with np.errstate(invalid="ignore"):
+        ref = case.oracle(k_pool=k)
+    a = case.device()
+    a["k_pool"] = k.to(DEV)
+    for ctas in (152, 1):
+        os.environ["TS_PAGED_DECODE_CTAS"] = str(ctas)
+        try:
+            out, lse = ts.ts_paged_prefill_attn(**a, return_lse=True)
+        finally:
+            os.environ.pop("TS_PAGED_DECODE_CTAS", None)
+        torch.cuda.synchronize()
+        _check(out, lse, ref, _reach(case), case, f"{value} W {window} {ctas} CTAs")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_query_that_is_not_finite_spoils_its_own_row_only(dtype):
+    case = ChunkCase(4, [140], [300], 8, 2, 64, dtype=dtype)
+    a, qk = case.device(), _reach(case)
+    case.q[77, 3, 5] = float("nan")
+    a["q"] = case.q.to(DEV)
+    with np.errstate(invalid="ignore"):
+        ref = case.oracle()
+    out, lse = ts.ts_paged_prefill_attn(**a, return_lse=True)
+    torch.cuda.synchronize()
+    assert np.isnan(ref[1]).sum() == 1
+    _check(out, lse, ref, qk, case, "query")

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(256) split_merge_kernel(const PagedParams p, i
       a.w += w * o.w;
       wsum += w;
     }
-    const float inv = wsum > 0.f ? 1.0f / wsum : 0.f;
+    const float inv = wsum == 0.f ? 0.f : 1.0f / wsum;  // a part's NaN stays one
     T* out = static_cast<T*>(p.out) + row * D + d0;
     if constexpr (sizeof(T) == 2) {
       uint2 pk;
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(256) split_merge_kernel(const PagedParams p, i
       *reinterpret_cast<float4*>(out) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     }
   }
-  if (lane == 0 && p.lse) p.lse[row] = wsum > 0.f ? ms + logf(wsum) : -INFINITY;
+  if (lane == 0 && p.lse) p.lse[row] = wsum == 0.f ? -INFINITY : ms + logf(wsum);
 }
 
 using KernelFn = void (*)(const PagedParams);

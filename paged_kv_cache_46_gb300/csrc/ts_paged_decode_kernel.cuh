@@ -960,19 +960,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const PagedPa
       // state (0 outside prefix mode), and the row's final LSE (log2 units)
       auto finish = [&](int hh, float& cs, float& cp, float& lse2) {
         const float Mh = pick(M, hh), Lh = pick(Lt, hh);
-        cs = Lh > 0.f ? __fdividef(1.0f, Lh) : 0.f;
+        // (a sum of 0: no key was seen; a score that is NaN or +inf makes the
+        // sum NaN, and O and the LSE with it)
+        cs = Lh == 0.f ? 0.f : __fdividef(1.0f, Lh);
         cp = 0.f;
-        lse2 = Lh > 0.f ? Mh + __log2f(Lh) : -INFINITY;
+        lse2 = Lh == 0.f ? -INFINITY : Mh + __log2f(Lh);
         if (kPfx && grouped && d.out_slot < 0) {
           const float lp2 = p.prefix_lse[row0 + qrow(hh)] * kLog2e;
           const float Mx = fmaxf(lse2, lp2);
           const float ws = lse2 == -INFINITY ? 0.f : fast_exp2(lse2 - Mx);
           const float wp = lp2 == -INFINITY ? 0.f : fast_exp2(lp2 - Mx);
           const float den = ws + wp;
-          const float iden = den > 0.f ? __fdividef(1.0f, den) : 0.f;
+          const float iden = den == 0.f ? 0.f : __fdividef(1.0f, den);
           cs *= ws * iden;
           cp = wp * iden;
-          lse2 = den > 0.f ? Mx + __log2f(den) : -INFINITY;
+          lse2 = den == 0.f ? -INFINITY : Mx + __log2f(den);
         }
       };
 #pragma unroll

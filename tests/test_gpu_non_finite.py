@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import paged_kv_cache_46_gb300 as ts
 from chunk_cases import DEV, ChunkCase, check_attention
 
@@ -81,3 +82,32 @@ def test_a_query_that_is_not_finite_spoils_its_own_row_only(dtype):
     torch.cuda.synchronize()
     assert np.isnan(ref[1]).sum() == 1
     _check(out, lse, ref, qk, case, "query")
+
+
+@pytest.mark.parametrize("window,sinks", [(300, 20), (1000, 4)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f32", 64)])
+def test_decode_with_first_tokens_of_keys_that_are_not_finite(dtype, D, value, window, sinks):
+    """The key is the first one, the window's last but one, one in front of the window; sequences whole
+    and cut between CTAs."""
+    L = np.array([700, 640, 900, 1])
+    case = ChunkCase(5, [1] * 4, L - 1, 8, 2, D, dtype=dtype, window=window, sinks=sinks)
+    k = case.k_pool.clone()
+    for b, t in ((0, 2), (1, 638), (2, 30)):
+        page, row = case.bt[b, t // 16], t % 16
+        k[page, row, b % 2, 0] = value
+    args = (case.bt, case.L, case.scale, window, sinks)
+    q, kd, v = (x.double().numpy() for x in (case.q, k, case.v_pool))
+    with np.errstate(invalid="ignore"):
+        ref = (*oracle.decode_attention_sinks(q, kd, v, *args),
+               oracle.decode_attention_sinks(q, kd, np.abs(v), *args)[0])
+    a = case.device()
+    for ctas in (152, 1):
+        os.environ["TS_PAGED_DECODE_CTAS"] = str(ctas)
+        try:
+            out, lse = ts.ts_paged_decode_sink_attn(a["q"], k.to(DEV), a["v_pool"], a["block_table"], a["seq_lens"],
+                                                    case.scale, window, sinks, return_lse=True)
+        finally:
+            os.environ.pop("TS_PAGED_DECODE_CTAS", None)
+        torch.cuda.synchronize()
+        _check(out, lse, ref, _reach(case), case, f"{value} W {window} {ctas} CTAs")

@@ -45,9 +45,9 @@ __global__ void __launch_bounds__(256) merge_states_kernel(const void* o_a, cons
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
   const float la = lse_a[row], lb = lse_b[row];
-  const float mx = fmaxf(la, lb);
-  const bool empty = mx == -INFINITY;
-  const float ms = empty ? 0.f : mx;
+  const bool empty = la == -INFINITY && lb == -INFINITY;
+  const float mx = fmaxf(la, lb);  // (of a NaN and -inf: -inf)
+  const float ms = mx == -INFINITY ? 0.f : mx;
   const float wa = la == -INFINITY ? 0.f : __expf(la - ms);
   const float wb = lb == -INFINITY ? 0.f : __expf(lb - ms);
   const float wsum = wa + wb;
@@ -60,11 +60,12 @@ __global__ void __launch_bounds__(256) merge_states_kernel(const void* o_a, cons
     if (!empty) {
       const float4 a = Vec4<T>::load(o_a, base + v);
       const float4 b = Vec4<T>::load(o_b, base + v);
-      // an empty side contributes nothing, whatever its O holds
-      r.x = (wa > 0.f ? ca * a.x : 0.f) + (wb > 0.f ? cb * b.x : 0.f);
-      r.y = (wa > 0.f ? ca * a.y : 0.f) + (wb > 0.f ? cb * b.y : 0.f);
-      r.z = (wa > 0.f ? ca * a.z : 0.f) + (wb > 0.f ? cb * b.z : 0.f);
-      r.w = (wa > 0.f ? ca * a.w : 0.f) + (wb > 0.f ? cb * b.w : 0.f);
+      // an empty side contributes nothing, whatever its O holds; one whose
+      // LSE is NaN makes the result NaN
+      r.x = (wa != 0.f ? ca * a.x : 0.f) + (wb != 0.f ? cb * b.x : 0.f);
+      r.y = (wa != 0.f ? ca * a.y : 0.f) + (wb != 0.f ? cb * b.y : 0.f);
+      r.z = (wa != 0.f ? ca * a.z : 0.f) + (wb != 0.f ? cb * b.z : 0.f);
+      r.w = (wa != 0.f ? ca * a.w : 0.f) + (wb != 0.f ? cb * b.w : 0.f);
     }
     Vec4<T>::store(o_out, base + v, r);
   }

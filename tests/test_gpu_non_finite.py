@@ -111,3 +111,19 @@ def test_decode_with_first_tokens_of_keys_that_are_not_finite(dtype, D, value, w
             os.environ.pop("TS_PAGED_DECODE_CTAS", None)
         torch.cuda.synchronize()
         _check(out, lse, ref, _reach(case), case, f"{value} W {window} {ctas} CTAs")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_merge_keeps_a_state_whose_lse_is_nan(dtype):
+    """Beside a finite state, an empty one and another NaN; an empty side's O does not count."""
+    nan, none, D = float("nan"), -float("inf"), 64
+    la = torch.tensor([nan, nan, 0.5, none, nan, none, none, 0.5], device=DEV)
+    lb = torch.tensor([0.5, none, nan, nan, nan, none, 0.5, none], device=DEV)
+    o = [torch.randn(8, D, generator=torch.Generator().manual_seed(i)).to(dtype).to(DEV) for i in range(2)]
+    o[0][torch.isnan(la)], o[1][torch.isnan(lb)] = nan, nan
+    o[0][5:7], o[1][5], o[1][7] = nan, nan, nan  # of empty states
+    out, lse = ts.ts_merge_states(o[0], la, o[1], lb)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[:5]).all() and torch.isnan(lse[:5]).all()
+    assert (out[5] == 0).all() and lse[5].item() == none
+    assert torch.equal(out[6], o[1][6]) and torch.equal(out[7], o[0][7]) and lse[6:].tolist() == [0.5, 0.5]

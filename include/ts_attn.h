@@ -478,7 +478,10 @@ TS_API ts_status ts_paged_decode_tree_attn(const void* q, const void* k_pool, co
  * 딥다이브, fiv.co.kr, section 6-4): a group is one (token, kv head) row of D
  * values; scale = max(max |x|, 1e-10) / 448 and code = e4m3fn(clamp(x / scale,
  * -448, 448)), the scale and the division in float32 rounded to nearest even,
- * the cast rounded to nearest even. Bit-exact with that definition.
+ * the cast rounded to nearest even. Bit-exact with that definition, which
+ * also holds for values that are not finite: a group with a NaN has the scale
+ * and all codes NaN; one with an infinity has the scale infinity, NaN codes for
+ * its infinities and zeros for the rest. Either reads back as NaN.
  *
  *   k_new, v_new    device [B, H_kv, D] of dtype (bf16 or f32)
  *   k_pool, v_pool  device uint8 [num_pages, page_size, H_kv, D] e4m3fn codes (written)

@@ -22,7 +22,6 @@ namespace ts {
 namespace {
 
 constexpr int kWarps = 8;  // per CTA
-constexpr float kE4M3Max = 448.0f;
 
 struct ChunkRows {
   const int32_t* block_table;
@@ -129,7 +128,8 @@ __device__ __forceinline__ uint2 codes_by_definition(const Eight<T>& x, float sc
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 f = x.pair(i / 2);
-    const float y = fminf(fmaxf(__fdiv_rn(i % 2 ? f.y : f.x, scale), -kE4M3Max), kE4M3Max);
+    const float y = __fdiv_rn(i % 2 ? f.y : f.x, scale);
+    // the saturating cast is the clamp, and keeps a NaN
     code[i / 4] |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3)) << (8 * (i % 4));
   }
   return make_uint2(code[0], code[1]);
@@ -165,7 +165,8 @@ __device__ __forceinline__ bool all_ones(float s) { return (~__float_as_uint(s) 
 
 // Quantization as ts_kv_append_fp8, bit for bit: a group is the D values of
 // one (token, kv head); scale = max(max |x|, 1e-10) / 448, code =
-// e4m3(clamp(x / scale, -448, 448)), in float32 rounded to nearest even.
+// e4m3(clamp(x / scale, -448, 448)), in float32 rounded to nearest even. A NaN
+// makes its group's scale and codes NaN, an infinity the scale infinite.
 //
 // One warp per row of K, of V or of both. D / 8 lanes hold a group, eight values each,
 // so that a warp takes two (D = 128) or four (D = 64) groups at a time, and
@@ -228,18 +229,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 5 : 4) kv_append
       // (the steps above lose the sign of a zero)
       uint2 code = make_uint2(two[0] | two[1] << 16 | x[u].signs(0), two[2] | two[3] << 16 | x[u].signs(1));
       if (__any_sync(0xffffffffu, top[u] >= 0x7f800000u || all_ones(scale))) {
-        if (top[u] >= 0x7f800000u) {  // as fmaxf takes the maximum: NaN do not count
-          float amax = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(x[u].pair(i).x), fabsf(x[u].pair(i).y)));
-          top[u] = __float_as_uint(amax);
-        }
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) {  // of finite groups: the same again
-          const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, top[u], o));
-          top[u] = __float_as_uint(fmaxf(__uint_as_float(top[u]), other));
-        }
-        scale = __fdiv_rn(fmaxf(__uint_as_float(top[u]), 1e-10f), kE4M3Max);
+        scale = e4m3_group_scale(top[u]);  // of finite groups: the same again
         code = codes_by_definition(x[u], scale);
       }
       if (h < c.H_kv) {

@@ -7,6 +7,9 @@
 // 448)), the scale and the division in float32 rounded to nearest even and the
 // cast rounded to nearest even. A token group is one (token, kv head) row of D
 // values, so the cache keeps one float32 scale per (page, row, kv head).
+// By the same arithmetic a group with a NaN has the scale NaN and NaN codes,
+// and one with an infinity the scale infinity, NaN codes for its infinities and
+// zeros for the rest: either reads back as NaN.
 //
 // One warp per (sequence, kv head, K or V) group: each lane widens D / 32
 // elements, a butterfly max gives the group maximum, and each lane writes its
@@ -17,8 +20,6 @@
 
 namespace ts {
 namespace {
-
-constexpr float kE4M3Max = 448.0f;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv_append_fp8_kernel(
@@ -45,20 +46,20 @@ __global__ void __launch_bounds__(256) kv_append_fp8_kernel(
   const int row = pos % page_size;
   const T* src = (is_v ? v_new : k_new) + (static_cast<int64_t>(b) * H_kv + h) * D + lane * kPer;
   float x[kPer];
-  float amax = 0.f;
+  uint32_t largest = 0u;  // magnitude's bits
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     x[i] = static_cast<float>(src[i]);
-    amax = fmaxf(amax, fabsf(x[i]));
+    largest = max(largest, __float_as_uint(x[i]) & 0x7fffffffu);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float scale = __fdiv_rn(fmaxf(amax, 1e-10f), kE4M3Max);
+  for (int o = 16; o > 0; o >>= 1) largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+  const float scale = e4m3_group_scale(largest);
   uint32_t packed = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const float y = fminf(fmaxf(__fdiv_rn(x[i], scale), -kE4M3Max), kE4M3Max);
-    const uint32_t c = __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+    // the saturating cast is the clamp, and keeps a NaN
+    const uint32_t c = __nv_cvt_float_to_fp8(__fdiv_rn(x[i], scale), __NV_SATFINITE, __NV_E4M3);
     packed |= c << (8 * i);
   }
   const int64_t cell = (static_cast<int64_t>(page) * page_size + row) * H_kv + h;

@@ -216,6 +216,16 @@ __device__ __forceinline__ uint32_t float2_to_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+constexpr float kE4M3Max = 448.0f;  // e4m3fn's largest finite value
+
+// Scale of a token group quantized to e4m3, max(max |x|, 1e-10) / 448, from the
+// float32 bits of its largest magnitude: they order as the magnitudes do, with
+// NaN above infinity above all others. A group with a NaN has the scale NaN.
+__device__ __forceinline__ float e4m3_group_scale(uint32_t largest) {
+  if (largest > 0x7f800000u) return __uint_as_float(0x7fc00000u);
+  return __fdiv_rn(fmaxf(__uint_as_float(largest), 1e-10f), kE4M3Max);
+}
+
 __device__ __forceinline__ void set_device_error(uint32_t* word, uint32_t bits) {
   if (word != nullptr) atomicOr(word, bits);
 }

@@ -127,3 +127,50 @@ def test_a_merge_keeps_a_state_whose_lse_is_nan(dtype):
     assert torch.isnan(out[:5]).all() and torch.isnan(lse[:5]).all()
     assert (out[5] == 0).all() and lse[5].item() == none
     assert torch.equal(out[6], o[1][6]) and torch.equal(out[7], o[0][7]) and lse[6:].tolist() == [0.5, 0.5]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_quantized_groups_that_are_not_finite_read_back_as_nan(dtype, D):
+    """Codes and scales are the definition's in IEEE arithmetic, from both appends: a NaN spoils its
+    group (max and quotients are NaN), an infinity's own quotient is NaN and the others are zeros of
+    an infinite scale. The groups beside them in the warp are exact."""
+    g = torch.Generator().manual_seed(6)
+    T, H_kv, ps = 24, 3, 8
+    x = torch.randn(T, H_kv, D, generator=g)
+    for t, values in enumerate([(float("inf"),), (-float("inf"),), (float("nan"),), (-float("nan"),),
+                                (float("inf"), float("nan")), (float("inf"), -float("inf"))]):
+        for i, value in enumerate(values):
+            x[2 * t, t % 3, (7 * t + 3 * i) % D] = value
+    x[21] = float("nan")
+    x = x.to(dtype)
+    xs = x.float().numpy()
+    with np.errstate(invalid="ignore"):
+        scale = (np.maximum(np.abs(xs).max(-1), np.float32(1e-10)) / np.float32(448)).astype(np.float32)
+        y = (xs / scale[..., None]).astype(np.float32)
+    nan = np.isnan(y)
+    code = oracle.fp8.e4m3_encode(np.clip(np.where(nan, 0, y), -448, 448))
+    assert nan.any() and np.isnan(scale).sum() == 6 and np.isinf(scale).sum() == 3
+    bt = torch.randperm(T // ps, generator=g).to(torch.int32)[None]
+    where = (bt[0].numpy()[np.arange(T) // ps], np.arange(T) % ps)
+    x = x.to(DEV)
+    lens, ptr = (torch.tensor(v, dtype=torch.int32, device=DEV) for v in ([T], [0, T]))
+    for chunk in (True, False):
+        cache = [torch.zeros(T // ps, ps, H_kv, D, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        cache += [torch.zeros(T // ps, ps, H_kv, device=DEV) for _ in range(2)]
+        if chunk:
+            ts.ts_kv_append_chunk_fp8(x, -x, *cache, bt.to(DEV), lens, ptr)
+        else:
+            ts.ts_kv_append_fp8(x, -x, *cache, bt.expand(T, -1).contiguous().to(DEV),
+                                torch.arange(T, dtype=torch.int32, device=DEV))
+        torch.cuda.synchronize()
+        for i, flip in ((0, 0), (1, 0x80)):
+            got = cache[i].cpu().numpy()[where]
+            assert np.array_equal((got & 0x7f) == 0x7f, nan)
+            assert np.array_equal(got[~nan], code[~nan] ^ flip)
+            assert np.array_equal(cache[2 + i].cpu().numpy()[where], scale, equal_nan=True)
+    out = [torch.zeros(T, H_kv, D, device=DEV) for _ in range(2)]
+    ts.ts_kv_read_fp8(*cache, bt.to(DEV), lens, ptr, *out)
+    torch.cuda.synchronize()
+    for o in out:
+        assert np.array_equal(torch.isnan(o).cpu().numpy(), np.repeat(~np.isfinite(scale)[..., None], D, -1))

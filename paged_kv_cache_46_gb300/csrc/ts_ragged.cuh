@@ -23,8 +23,9 @@ __device__ __forceinline__ int ragged_sequence(const int32_t* __restrict__ indpt
   return indptr[lo] <= row && row < indptr[lo + 1] ? lo : -1;
 }
 
-// A page size and its logarithm (-1 where it is no power of two, which any call
-// but the appends refuses): a division per row is a fifth of a short row's work.
+// A page size and its logarithm (-1 where it is no power of two: the appends and
+// the read-back take pages of any size, the attention calls do not): a division
+// per row is a fifth of a short row's work.
 struct PageSize {
   int32_t rows, shift;
   explicit PageSize(int32_t r) : rows(r), shift(-1) {

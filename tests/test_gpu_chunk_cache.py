@@ -344,3 +344,31 @@ def test_more_sequences_than_two_steps_of_the_search():
     ref = oracle.kv_append_chunk(*before, _bits(k).numpy(), _bits(v).numpy(), bt, L, ptr)
     for got, want in zip(pools, ref):
         assert np.array_equal(_bits(got).cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("ps", [1, 7, 24, 100])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_pages_of_any_size(ps, dtype):
+    """The appends and the read-back take page sizes that are no powers of two (and one row)."""
+    n, ctx, H_kv, D = [130, 0, 1, 50], [0, 31, 100, 23], 2, 64
+    k, v, bt, L, ptr, P = _batch(ps, n, ctx, H_kv, D, ps, dtype, pad=3)
+    dev = (_i32(bt), _i32(L), _i32(ptr))
+    pools = [torch.full((P, ps, H_kv, D), float("nan"), dtype=dtype, device=DEV) for _ in range(2)]
+    before = [_bits(p).cpu().numpy() for p in pools]
+    ts.ts_kv_append_chunk(k.to(DEV), v.to(DEV), *pools, *dev)
+    cache = [torch.full((P, ps, H_kv, D), 0x38, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    cache += [torch.ones(P, ps, H_kv, device=DEV) for _ in range(2)]
+    before8 = [t.cpu().numpy() for t in cache]
+    ts.ts_kv_append_chunk_fp8(k.to(DEV), v.to(DEV), *cache, *dev)
+    starts = np.concatenate([[2], 2 + np.cumsum(L + 1)])
+    outs = [torch.full((int(starts[-1]) + 2, H_kv, D), 7.0, dtype=dtype, device=DEV) for _ in range(2)]
+    ts.ts_kv_read_fp8(*cache, dev[0], dev[1], _i32(starts), *outs)
+    torch.cuda.synchronize()
+    for got, want in zip(pools, oracle.kv_append_chunk(*before, _bits(k).numpy(), _bits(v).numpy(), bt, L, ptr)):
+        assert np.array_equal(_bits(got).cpu().numpy(), want)
+    ref = oracle.kv_append_chunk_fp8(*before8, k.float().numpy(), v.float().numpy(), bt, L, ptr)
+    for got, want in zip(cache, ref):
+        assert np.array_equal(got.cpu().numpy(), want)
+    for i, got in enumerate(outs):
+        want = oracle.kv_read_fp8(ref[i], ref[2 + i], bt, L, starts, np.full(outs[i].shape, 7.0))
+        assert torch.equal(got.cpu(), torch.from_numpy(want).to(dtype))

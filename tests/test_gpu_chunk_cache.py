@@ -372,3 +372,66 @@ def test_pages_of_any_size(ps, dtype):
     for i, got in enumerate(outs):
         want = oracle.kv_read_fp8(ref[i], ref[2 + i], bt, L, starts, np.full(outs[i].shape, 7.0))
         assert torch.equal(got.cpu(), torch.from_numpy(want).to(dtype))
+
+
+def _quantized(x):
+    """Codes and scales of rows x [T, H_kv, D] as both quantizing appends store them, in order of the rows."""
+    T, H_kv, D = x.shape
+    bt = torch.arange(T, dtype=torch.int32, device=DEV)
+    made = []
+    for chunk in (True, False):
+        cache = [torch.zeros(T, 1, H_kv, D, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        cache += [torch.zeros(T, 1, H_kv, device=DEV) for _ in range(2)]
+        if chunk:
+            ts.ts_kv_append_chunk_fp8(x, -x, *cache, bt[None].contiguous(), _i32([T]), _i32([0, T]))
+        else:
+            ts.ts_kv_append_fp8(x, -x, *cache, bt[:, None].contiguous(), torch.zeros_like(bt))
+        torch.cuda.synchronize()
+        assert torch.equal(cache[0] ^ 0x80, cache[1]) and torch.equal(cache[2], cache[3])
+        made.append((cache[0][:, 0].cpu().numpy(), cache[2][:, 0].cpu().numpy()))
+    return made
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_fp8_append_of_every_bf16_ratio_up_to_the_maximum(dtype):
+    """All 2432 bf16 values of 2^-18 up to the group's maximum, times tops of many significands: the last
+    ones are the quotients beside the clamp."""
+    vals = torch.arange(0x3600, 0x3f81, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).float()
+    assert len(vals) == 2433 and vals[-1] == 1.0
+    vals = torch.cat([vals, vals[-1:].expand(-len(vals) % 127)]).view(-1, 127)
+    tops = (1.0, 1.5, 1.0078125, 1.9921875, 7.0, 448.0, 0.33, 3e-10, 2.0 ** 100)
+    x = torch.stack([torch.cat([vals * top, torch.full((len(vals), 1), top)], 1) for top in tops], 1).to(dtype)
+    codes, scales = oracle.quantize_token_groups(x.float().numpy())
+    for got in _quantized(x.to(DEV)):
+        assert np.array_equal(got[0], codes) and np.array_equal(got[1], scales)
+
+
+def test_fp8_append_of_float32_values_beside_every_border():
+    """float32 values within four units in the last place of every border between two codes, and of every
+    code, times scales of random significands, of all ones and of powers of two, over the type's range:
+    the quotients' rounding decides the code."""
+    rng = np.random.default_rng(9)
+    grid = oracle.fp8.e4m3_decode(np.arange(0x7f))  # 0 .. 448
+    borders = np.concatenate([grid[1:], (grid[1:] + grid[:-1]) / 2])
+    ones = np.float32(2.0) - np.float32(2.0 ** -23)
+    rows, exact = [], 0
+    for i in range(700):
+        e = rng.integers(-44, 118)
+        m = (1 + rng.random(), ones, 1.0)[0 if i % 7 > 1 else 1 + i % 7]
+        scale = np.float32(float(m) * 2.0 ** e)
+        top = np.float32(np.float64(scale) * 448)
+        scale = np.float32(max(top, np.float32(1e-10))) / np.float32(448)
+        exact += ((~scale.view(np.uint32)) & 0x7fffff) == 0
+        x = np.abs(borders * np.float64(scale)).astype(np.float32)
+        off = rng.integers(-4, 5, size=x.shape, dtype=np.int32)
+        x = (x.view(np.int32) + off).view(np.float32)
+        x = np.minimum(x, top)
+        x = np.concatenate([x, x[:-len(x) % 127]]).reshape(-1, 127)
+        rows.append(np.concatenate([x, np.full((len(x), 1), top)], 1))
+    assert exact > 50
+    x = np.stack(rows, 1)[:, :, rng.permutation(128)]  # [rows, scales, 128]: four scales a row of the cache
+    x = np.ascontiguousarray(x.reshape(-1, 4, 128))
+    codes, scales = oracle.quantize_token_groups(x)
+    for got in _quantized(torch.from_numpy(x).to(DEV)):
+        assert np.array_equal(got[1], scales)
+        assert np.array_equal(got[0], codes), np.argwhere(got[0] != codes)[:5]

@@ -332,3 +332,24 @@ def test_tiles_with_the_buffers_for_themselves(H_q, n, ctx, window, sinks, D):
             off += (got[0] != out).sum() + (got[1] != lse).sum()
     assert off.item() == 0
     assert all(ts.ts_read_device_error(w) == 0 for w in ws)
+
+
+@pytest.mark.parametrize("indptr", [[0, 50, 20, 60], [-3, 10, 20, 30], [0, 20, 40, 4000], [60, 40, 20, 0],
+                                    [0, 60, 0, 60], [2 ** 31 - 1, -2 ** 31, 0, 60]])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_row_offsets_out_of_order_reach_nothing_else_and_end(indptr, dtype):
+    """Guards behind the workspace's stated size and around O and LSE stay; no role waits its limit out."""
+    case = ChunkCase(14, [20, 20, 20], [400, 5, 1000], 4, 2, 64, dtype=dtype, window=0)
+    a = case.device()
+    a["q_indptr"] = torch.tensor(indptr, dtype=torch.int32, device=DEV)
+    size = ts.ts_paged_prefill_workspace_size(60, 3, 4, 2, 64)
+    room = ts.new_workspace(size + 4096)
+    room[size:] = 0x5a
+    out = torch.full((60 + 128, 4, 64), 7.0, dtype=case.q.dtype, device=DEV)
+    lse = torch.full((60 + 128, 4), 7.0, device=DEV)
+    ts.ts_paged_prefill_attn(**a, out=out[64:124], lse=lse[64:124], workspace=room[:size])
+    torch.cuda.synchronize()
+    assert ts.ts_read_device_error(room) & ts.TS_DEVERR_TIMEOUT == 0
+    assert torch.all(room[size:] == 0x5a)
+    for t in (out, lse):
+        assert torch.all(t[:64] == 7.0) and torch.all(t[124:] == 7.0)

@@ -25,7 +25,10 @@
  *     32-bit TMA coordinates); a larger num_pages is an argument error.
  *   - GQA: query head h reads kv head h / (H_q / H_kv).
  *   - LSE outputs are natural-log log-sum-exp of the scaled scores, float32.
- *     A sequence of length 0 yields O = 0 and LSE = -inf.
+ *     A sequence of length 0 yields O = 0 and LSE = -inf. A query that sees a
+ *     score of NaN or +inf has O = NaN and LSE = NaN in ts_paged_decode_attn,
+ *     its window and first-token forms and ts_paged_prefill_attn, and
+ *     ts_merge_states keeps it.
  *   - Device-side safety: a page id outside [0, num_pages) is never
  *     dereferenced. Attention treats the tokens of such a page as absent and
  *     sets bit TS_DEVERR_PAGE_RANGE in the workspace's error word; the append
@@ -265,11 +268,12 @@ TS_API ts_status ts_paged_decode_sink_attn(const void* q, const void* k_pool, co
  * q_indptr[b] sits at position seq_lens[b] - n + j. The same q_indptr and
  * seq_lens serve ts_kv_append_chunk (or ts_kv_append_chunk_fp8) and then
  * ts_paged_prefill_attn. q_indptr is device int32 [B + 1], not decreasing,
- * within [0, T]; rows outside [q_indptr[0], q_indptr[B]) (padding of a captured
- * graph) are neither read nor written. Entries out of order never cause an
- * access out of range; which rows are then taken is not defined. n == 0 is a
- * sequence without new tokens. Two sequences of one call that write the same
- * page row leave either's values there.
+ * within [0, T]. Rows outside [q_indptr[0], q_indptr[B]) (padding of a captured
+ * graph) are memory like the others, of the inputs too: inputs there may be
+ * read, whatever they hold has no effect, and no result is written there.
+ * Entries out of order never cause an access out of range; which rows are then
+ * taken is not defined. n == 0 is a sequence without new tokens. Two sequences
+ * of one call that write the same page row leave either's values there.
  */
 
 /*
@@ -285,8 +289,9 @@ TS_API ts_status ts_paged_decode_sink_attn(const void* q, const void* k_pool, co
  *   seq_lens      device int32 [B], q_indptr device int32 [B + 1]: see above
  * The copy is bit-exact. Rows whose position is negative or whose block-table
  * slot or page id is out of range are skipped. T == 0 or B == 0 returns TS_OK
- * with nothing enqueued. H_kv * D and new_stride are multiples of 16 bytes
- * (else TS_ERR_UNSUPPORTED), the pointers 16-byte aligned.
+ * with nothing enqueued. H_kv * D and new_stride are multiples of 16 bytes, a
+ * row at most 1 MiB (else TS_ERR_UNSUPPORTED), the pointers 16-byte aligned;
+ * page_size is any positive number.
  */
 TS_API ts_status ts_kv_append_chunk(const void* k_new, const void* v_new, void* k_pool, void* v_pool,
                                     const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
@@ -331,8 +336,8 @@ TS_API ts_status ts_kv_append_chunk_fp8(const void* k_new, const void* v_new, vo
  *   seq_lens        device int32 [B] tokens to read (from the first on)
  *   kv_indptr       device int32 [B + 1], not decreasing, within [0, rows]
  *   k_out, v_out    device [rows, H_kv, D] of dtype (bf16 or f32) (written)
- * Supported: D in {64, 128}. rows == 0 or B == 0 returns TS_OK with nothing
- * enqueued. Pools and results are 16-byte aligned.
+ * Supported: D in {64, 128}, any page_size. rows == 0 or B == 0 returns TS_OK
+ * with nothing enqueued. Pools and results are 16-byte aligned.
  */
 TS_API ts_status ts_kv_read_fp8(const void* k_pool, const void* v_pool, const float* k_scale,
                                 const float* v_scale, const int32_t* block_table, int32_t bt_stride,
@@ -377,11 +382,13 @@ TS_API size_t ts_paged_prefill_workspace_size(int32_t T, int32_t B, int32_t H_q,
  *   workspace     >= ts_paged_prefill_workspace_size(T, B, H_q, H_kv, D)
  *                 bytes, 256-byte aligned, the error word in front
  *   other arguments and errors as in ts_paged_decode_attn.
- * Pages that no row of a call sees are never read, nor are rows of a seen
- * page that lie past the sequence's end or outside every row's window. The
- * tokens of a page whose id is out of range, or past the block table's row,
- * (or its first 2^30 tokens) count as absent and set TS_DEVERR_PAGE_RANGE. A V row that some rows of a
- * 128-key tile see and others do not must be finite (the others weigh it by 0).
+ * Pages that no row of a call sees are never read. A page with a seen row may
+ * be read whole; what its other rows hold (past the sequence's end, outside
+ * every row's window; NaN included) has no effect. The tokens of a page whose
+ * id is out of range, tokens past the block table's row and tokens from
+ * position 2^30 on count as absent and set TS_DEVERR_PAGE_RANGE. A V row that
+ * some rows of a 128-key tile see and others do not must be finite (the others
+ * weigh it by 0).
  * Supported: D in {64, 128}, H_q / H_kv up to 64, page_size in {8, 16, 32},
  * T up to 2^30, q_stride a multiple of 16 bytes.
  */

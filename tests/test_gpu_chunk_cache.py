@@ -435,3 +435,43 @@ def test_fp8_append_of_float32_values_beside_every_border():
     for got in _quantized(torch.from_numpy(x).to(DEV)):
         assert np.array_equal(got[1], scales)
         assert np.array_equal(got[0], codes), np.argwhere(got[0] != codes)[:5]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_padding_rows_may_hold_anything(dtype):
+    """NaN in the input rows in front of the first sequence and behind the last: the results are those of
+    the rows alone, and no padding row of a result is written."""
+    n, ctx, H_q, H_kv, D, ps, front, back = [70, 0, 20], [0, 9, 300], 8, 2, 64, 16, 9, 30
+    k, v, bt, L, ptr, P = _batch(11, n, ctx, H_kv, D, ps, dtype)
+    T, g = len(k), torch.Generator().manual_seed(12)
+    q = torch.randn(T, H_q, D, generator=g).to(dtype)
+    cached = [torch.randn(P, ps, H_kv, D, generator=g).to(dtype) for _ in range(2)]
+    runs = []
+    for pad in (False, True):
+        def rows(t):
+            t = t.to(DEV)
+            nan = lambda count: torch.full((count, *t.shape[1:]), float("nan"), dtype=dtype, device=DEV)  # noqa: E731
+            return torch.cat([nan(front), t, nan(back)]) if pad else t
+        meta = (_i32(bt), _i32(L), _i32(ptr + front if pad else ptr))
+        pools = [c.to(DEV) for c in cached]
+        cache = [torch.zeros(P, ps, H_kv, D, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        cache += [torch.zeros(P, ps, H_kv, device=DEV) for _ in range(2)]
+        ts.ts_kv_append_chunk(rows(k), rows(v), *pools, *meta)
+        ts.ts_kv_append_chunk_fp8(rows(k), rows(v), *cache, *meta)
+        total = T + (front + back if pad else 0)
+        out = torch.full((total, H_q, D), 7.0, dtype=dtype, device=DEV)
+        lse = torch.full((total, H_q), 7.0, device=DEV)
+        ts.ts_paged_prefill_attn(rows(q), *pools, *meta, D ** -0.5, out=out, lse=lse)
+        torch.cuda.synchronize()
+        if pad:
+            for t in (out, lse):
+                assert torch.all(t[:front] == 7.0) and torch.all(t[front + T:] == 7.0)
+            out, lse = out[front:front + T], lse[front:front + T]
+        runs.append(pools + cache)
+        kk, vv, qd = (t.double().cpu().numpy() for t in (*pools, q))
+        args = (bt, L, ptr, D ** -0.5)
+        ref = (*oracle.prefill_attention(qd, kk, vv, *args), oracle.prefill_attention(qd, kk, np.abs(vv), *args)[0],
+               D ** -0.5 * np.abs(kk).sum(-1).max() * np.abs(qd).max())
+        check_attention(out, lse, ref, D, int(L.max()), "bf16" if dtype == torch.bfloat16 else "f32", f"padding {pad}")
+    for alone, padded in zip(*runs):
+        assert torch.equal(alone, padded)

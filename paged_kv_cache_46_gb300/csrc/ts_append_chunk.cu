@@ -9,11 +9,12 @@
 //
 // A warp takes a row (K and V, or one of them where they are quantized) and
 // finds the row's sequence by a 32-way search over q_indptr: no plan is made on
-// the host and none has to be kept. Both are bound by HBM: each value is read
-// once and written once. 15,000 bf16 rows of 8 x 128 (a part of a fused
+// the host and none has to be kept. Each value is read once and written once, and
+// HBM bounds the copy. 15,000 bf16 rows of 8 x 128 (a part of a fused
 // projection's rows): the copy 20.7 us, 123 MB at 5.9 TB/s; the quantizing one
-// 21 us for 16,000 rows, 99 MB at 4.7 TB/s, where the conversions take as long as the memory.
-// 33 rows: 2.4 and 2.5 us, of which the launch and two dependent loads are most.
+// 21.4 us for 16,000 rows, 99 MB at 4.6 TB/s: its issue slots are active 63 % of
+// the time and HBM at 68 % of its rate, neither exhausted.
+// 33 rows: 2.4 and 2.6 us, of which the launch and two dependent loads are most.
 #include <cuda_fp8.h>
 
 #include "ts_ragged.cuh"

@@ -8,9 +8,9 @@
 //
 // What bounds it: HBM, as the plain window. The rows are those of the window
 // plus one or a few pages per sequence: 64 sequences, window 4096 and 64 first
-// tokens, 32 / 8 heads of 128, bf16: 162 us, 1,092 MB at 6.7 TB/s (99 % of the
-// device's copy rate). One float32 sequence, window 250: 8.4 us, the latency of
-// the launch, the prologue and one round of loads.
+// tokens, 32 / 8 heads of 128, bf16: 164.5 us, 1,092 MB at 6.6 TB/s (98 % of the
+// device's copy rate). One float32 sequence, window 250: 8.1 to 8.9 us, the
+// latency of the launch, the prologue and one round of loads.
 #include "ts_paged_decode_kernel.cuh"
 
 namespace ts {

@@ -34,10 +34,14 @@
 // sees it), loads from TMEM (470), weights (980; 710 for a warp that has the SM
 // to itself, 510 of them the exponentials), issue and run of P V (512 + 540),
 // since TMEM has room for one score tile per query tile there. 4096 tokens over
-// 32,768, 32 / 8 heads of 128: 1.39 ms, 1.48 PFLOP/s at 1.77 GHz under the power
-// limit; 16 ragged prompts of 7,900 tokens in all, over up to 4,096 each: 292 us,
-// 1.14 PFLOP/s. At head dim 64 a third score buffer takes S off the chain (window
-// 1024, 7,300 tokens: 132 us). Tried against this: products of 64 keys with four
+// 32,768, 32 / 8 heads of 128: 2.66 million clocks, which is 1.38 ms (1.49
+// PFLOP/s) for the first tens of calls and 1.49 ms (1.38) where calls go on for
+// seconds and the power limit takes the clock from 1.93 to 1.79 GHz; 16 ragged
+// prompts of 7,900 tokens in all, over up to 4,096 each: 294 us, 1.13 PFLOP/s,
+// and 303 us. At head dim 64 a third score buffer takes S off the chain (window
+// 1024, 7,300 tokens: 135 us); the tensor pipe and the exponential unit are
+// active 28 % of the time there and issue slots 47 %: latency, with two softmax
+// warps a scheduler to hide it. Tried against this: products of 64 keys with four
 // score buffers (1.73 ms: an N = 64 product costs 47 clocks, not 32), the second
 // half of P through shared memory (1.63 ms), a row's keys over two warps (1.45
 // ms), scores loaded 32 at a time between the weights (1.56 ms).
@@ -1226,17 +1230,22 @@ extern "C" ts_status ts_paged_prefill_attn(const void* q, int64_t q_stride, cons
   prm.window = window;
   prm.sinks = sinks;
   prm.tile_tokens = kBM / g;
-  // An item's queries, first scores and epilogue take about as long as three of
-  // its key tiles (4.3 us against 1.5 at head dim 128): with more items than
-  // CTAs that is what balances them (16 ragged prompts: 310 us with one unit,
-  // 290 with four; 8 of 300 tokens: 62.3 and 60.9). With fewer, every item is cut
-  // and each part has that cost anyway (33 tokens: 15.4 us with one, 15.7 with
-  // four; 512 tokens: 26.4 and 26.6).
+  // A whole item's queries, first scores and epilogue take about as long as
+  // three of its key tiles (4.3 us against 1.5 at head dim 128): with more of
+  // them than CTAs that is what balances the cut (16 ragged prompts: 310 us with
+  // one unit, 290 with four; 8 of 300 tokens: 62.3 and 60.9). With fewer, every
+  // item is cut and each part has that cost anyway (33 tokens: 15.4 us with one,
+  // 15.7 with four; 512 tokens: 26.4 and 26.6). Only whole items' rows count
+  // here: the items of short chunks, one tile and bound by their loads, cost
+  // little beside their keys (64 chunks of 16 tokens over up to 4,096: 126 us
+  // with one unit, 130 with four; 256 of one token over up to 8,192: 791 and 814;
+  // 128 of up to 64 over up to 2,048: 162 both).
   const int64_t items = static_cast<int64_t>(H_kv) * T / (2 * prm.tile_tokens);
   prm.item_units = items >= ctas ? 4 : 1;
-  // Fewer, larger parts where there are few units: a part costs a launch's and
-  // the merge's latency (33 tokens over 1,000: 19.0 us with one unit each, 16.9
-  // with two, 17.9 with three, 19.1 with four, 25.0 with ten).
+  // Fewer, larger parts where there are few units: each part costs the merge
+  // (one unit, two, four; 33 tokens over 200: 12.0, 14.1, 18.2 us; over 1,000:
+  // 16.7, 16.7, 20.0; over 4,000: 26.7, 21.8, 21.8; 64 tokens over 2,000 with two
+  // kv heads: 17.7, 16.1, 19.3).
   prm.min_units = 2;
   prm.slot_rows = slot_rows_of(T, g);
   prm.scale_log2 = scale * kLog2eC;

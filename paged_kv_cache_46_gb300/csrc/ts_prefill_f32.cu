@@ -1,5 +1,6 @@
-// ts_paged_prefill_attn, float32: the tensor pipe has no float32 product, so
-// this path runs on the CUDA cores and keeps float32 accuracy.
+// ts_paged_prefill_attn, float32: on the CUDA cores, with float32 products and
+// sums throughout. (The tensor pipe has no float32 product; products of bf16
+// terms that add up to float32 values are not built here.)
 //
 // A CTA takes 128 query rows (128 / g tokens times the g heads of one kv head)
 // and walks the keys that some of them sees in tiles of 64. Thread (y, x) of
@@ -9,13 +10,16 @@
 // 16-byte reads of different keys fall into different banks. Running maximum
 // and sum per row, in float32.
 //
-// What bounds it: the packed float32 FMA rate. 12 16-byte shared reads feed 64
-// packed multiply-adds of the scores (1024 tokens over 8192, 32 / 8 heads of
-// 128: 3.8 ms); a 4 x 4 patch (5.3 ms) was bound by the reads instead.
+// What bounds it: the issue of packed multiply-adds and of the shared reads that
+// feed them, 12 of 16 bytes for 64 packed multiply-adds of the scores (1024
+// tokens over 8192, 32 / 8 heads of 128: 3.8 ms, 38 TFLOP/s, about half of the
+// multiply-adds' own rate; with a 4 x 4 patch 5.3 ms).
 //
 // Few rows over a long context leave most SMs idle, so each CTA's keys are
 // split over as many CTAs as the device has room for twice over; the parts are
-// joined by LSE (16 tokens over 28,000: 0.43 ms, with one part 5.5 ms).
+// joined by LSE (16 tokens over 28,000: 0.43 ms, with one part 5.5 ms). The
+// number of parts is one for the whole batch, from its counts of rows and
+// sequences: a long context among many short chunks is not split further.
 #include <algorithm>
 #include <cmath>
 

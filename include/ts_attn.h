@@ -26,9 +26,7 @@
  *   - GQA: query head h reads kv head h / (H_q / H_kv).
  *   - LSE outputs are natural-log log-sum-exp of the scaled scores, float32.
  *     A sequence of length 0 yields O = 0 and LSE = -inf. A query that sees a
- *     score of NaN or +inf has O = NaN and LSE = NaN in ts_paged_decode_attn,
- *     its window and first-token forms and ts_paged_prefill_attn, and
- *     ts_merge_states keeps it.
+ *     score of NaN or +inf has O = NaN and LSE = NaN, and merges keep it.
  *   - Device-side safety: a page id outside [0, num_pages) is never
  *     dereferenced. Attention treats the tokens of such a page as absent and
  *     sets bit TS_DEVERR_PAGE_RANGE in the workspace's error word; the append

@@ -387,20 +387,21 @@ __global__ void __launch_bounds__(kThreadsPfx, 2) cascade_prefix_kernel(
         const bool valid = mi < mcount;
         const int b = valid ? p.member_ids[mbeg + mi] : 0;
         const int64_t row = static_cast<int64_t>(b) * p.H_q + h * p.g + r % p.g;
-        float lse_new = l > 0.f ? (m + log2f(l)) * kLn2C : -INFINITY;
+        // (no key: -inf; a NaN or +inf score makes l NaN, and the state with it)
+        float lse_new = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2C;
         // weights of the state already there (accumulate) and of this one,
         // by LSE (TokenSpeed deep dive, section 7.1)
-        float w_old = 0.f, w_new = l > 0.f ? 1.0f / l : 0.f;
+        float w_old = 0.f, w_new = l == 0.f ? 0.f : 1.0f / l;
         if (p.accumulate && valid) {
           const float lse_old = p.prefix_lse[row];
           const float mx = fmaxf(lse_old, lse_new);
           const float ea = lse_old == -INFINITY ? 0.f : __expf(lse_old - mx);
           const float eb = lse_new == -INFINITY ? 0.f : __expf(lse_new - mx);
           const float den = ea + eb;
-          const float iden = den > 0.f ? 1.0f / den : 0.f;
+          const float iden = den == 0.f ? 0.f : 1.0f / den;
           w_old = ea * iden;
           w_new *= eb * iden;
-          lse_new = den > 0.f ? mx + logf(den) : -INFINITY;
+          lse_new = den == 0.f ? -INFINITY : mx + logf(den);
         }
 #pragma unroll
         for (int c0 = 0; c0 < kHD; c0 += 16) {

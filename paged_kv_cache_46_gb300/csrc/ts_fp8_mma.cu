@@ -641,8 +641,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mma_kernel(const MmaParams p,
       const float* st = stats + ((seg & 1) * kHq + h) * 3;
       const float m = st[0], l = st[1];
       const int gexp = __float_as_int(st[2]);
-      const float inv = l > 0.f ? 1.0f / (l * pow2i(gexp)) : 0.f;
-      const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+      // (no key: O = 0, LSE = -inf; a sum that is NaN stays NaN in both)
+      const float inv = l == 0.f ? 0.f : 1.0f / (l * pow2i(gexp));
+      const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
       // reduce-scatter of the four lanes' O rows: term t keeps dims [32 t, 32 t + 32)
       const bool b1 = (term >> 1) != 0, b0 = (term & 1) != 0;
       const uint32_t to = trow + kTO;
@@ -740,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mma_kernel(const MmaParams p,
               acc[x + 3] += wk * v.w;
             }
           }
-          const float idn = den > 0.f ? 1.0f / den : 0.f;
+          const float idn = den == 0.f ? 0.f : 1.0f / den;
           uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kD + term * 32);
 #pragma unroll
           for (int x = 0; x < 32; x += 8)
@@ -748,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mma_kernel(const MmaParams p,
                                     float2_to_bf16x2(acc[x + 2] * idn, acc[x + 3] * idn),
                                     float2_to_bf16x2(acc[x + 4] * idn, acc[x + 5] * idn),
                                     float2_to_bf16x2(acc[x + 6] * idn, acc[x + 7] * idn));
-          if (term == 0 && p.lse) p.lse[orow] = den > 0.f ? (mx + log2f(den)) * kLn2C : -INFINITY;
+          if (term == 0 && p.lse) p.lse[orow] = den == 0.f ? -INFINITY : (mx + log2f(den)) * kLn2C;
         }
       }
       // the Q terms of the segment after next go into this segment's Q buffer

@@ -521,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tc_kernel(
       __syncwarp();
       if (lane == 0) mbar_arrive(b_pfull(j & 1));
     }
-    // epilogue: O row / l in bf16 and the LSE (no key: O = 0, LSE = -inf)
+    // epilogue: O row / l in bf16 and the LSE (no key: O = 0, LSE = -inf; a sum
+    // that is NaN stays NaN in both)
     if (ok && n_kt > 0) {
       ok = mbar_wait(b_pvdone((n_kt - 1) & 1), ((n_kt - 1) >> 1) & 1);
       if (!__all_sync(0xffffffffu, ok)) ok = false;
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tc_kernel(
     }
     if (ok && warp_real) {
       const int64_t row = static_cast<int64_t>(b) * p.H_q + (h0 + hs) * p.g + r;
-      const float inv = l > 0.f ? 1.0f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll
       for (int c0 = 0; c0 < kHD; c0 += 16) {
         uint32_t u[16];
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_tc_kernel(
                                     float2_to_bf16x2(__uint_as_float(u[x + 6]) * inv, __uint_as_float(u[x + 7]) * inv));
         }
       }
-      if (real && p.lse) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2C : -INFINITY;
+      if (real && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2C;
     }
     if (!ok) set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
   }

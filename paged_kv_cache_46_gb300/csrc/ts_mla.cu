@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreadsMla, 1) mla_decode_kernel(const MlaPar
       float l_other = 0.f;
       if (!pair_exchange(l_half, l_other)) return false;
       const float l = l_half + l_other;
-      const float inv = l > 0.f ? ginv / l : 0.f;
+      const float inv = l == 0.f ? 0.f : ginv / l;  // no key: O = 0, LSE = -inf; a NaN sum stays NaN
       for (int c0 = 0; c0 < 128; c0 += 16) {
         uint32_t u[16];
         tmem_ld16(trow + kTO + hf * 128 + c0, u);
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreadsMla, 1) mla_decode_kernel(const MlaPar
                                  __uint_as_float(u[4 * x + 2]) * inv, __uint_as_float(u[4 * x + 3]) * inv);
         }
       }
-      const float lse = l > 0.f ? (m + log2f(l)) * kLn2M : -INFINITY;
+      const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2M;
       if (rank == 0 && hf == 0) {
         if (t.out_slot < 0) {
           if (p.lse) p.lse[static_cast<int64_t>(t.b) * kH + h] = lse;
@@ -914,7 +914,7 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(const MlaParams p) {
       acc[4 * x + 3] += w * o.w;
     }
   }
-  const float inv = wsum > 0.f ? 1.0f / wsum : 0.f;
+  const float inv = wsum == 0.f ? 0.f : 1.0f / wsum;
   __nv_bfloat16* out = p.out + (static_cast<int64_t>(b) * kH + h) * kDv;
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
@@ -923,7 +923,7 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(const MlaParams p) {
     pk.y = float2_to_bf16x2(acc[4 * x + 2] * inv, acc[4 * x + 3] * inv);
     *reinterpret_cast<uint2*>(out + (lane + 32 * x) * 4) = pk;
   }
-  if (lane == 0 && p.lse) p.lse[static_cast<int64_t>(b) * kH + h] = wsum > 0.f ? ms + logf(wsum) : -INFINITY;
+  if (lane == 0 && p.lse) p.lse[static_cast<int64_t>(b) * kH + h] = wsum == 0.f ? -INFINITY : ms + logf(wsum);
 }
 
 struct MlaWs {

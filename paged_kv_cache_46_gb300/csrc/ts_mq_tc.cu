@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, Layout<kHD>::kMinBlocks) mq_tc_kerne
       __syncwarp();
       if (lane == 0) mbar_arrive(b_pfull(j & 1));
     }
-    // epilogue: O row / l in bf16 and the LSE (no key: O = 0, LSE = -inf)
+    // epilogue: O row / l in bf16 and the LSE (no key: O = 0, LSE = -inf; a sum
+    // that is NaN stays NaN in both)
     if (ok && n_kt > 0) {
       ok = mbar_wait(b_pvdone((n_kt - 1) & 1), ((n_kt - 1) >> 1) & 1);
       if (!__all_sync(0xffffffffu, ok)) ok = false;
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, Layout<kHD>::kMinBlocks) mq_tc_kerne
     if (ok && warp_real) {
       const bool real = r < R;
       const int64_t row = (static_cast<int64_t>(b) * p.q_len + jt) * p.H_q + (h0 + hs) * p.g + r % p.g;
-      const float inv = lr > 0.f ? 1.0f / lr : 0.f;
+      const float inv = lr == 0.f ? 0.f : 1.0f / lr;
 #pragma unroll
       for (int c0 = 0; c0 < kHD; c0 += 16) {
         uint32_t u[16];
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, Layout<kHD>::kMinBlocks) mq_tc_kerne
                                     float2_to_bf16x2(__uint_as_float(u[x + 6]) * inv, __uint_as_float(u[x + 7]) * inv));
         }
       }
-      if (real && p.lse) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2C : -INFINITY;
+      if (real && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2C;
     }
     if (!ok) set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
   }

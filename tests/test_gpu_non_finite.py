@@ -174,3 +174,102 @@ def test_quantized_groups_that_are_not_finite_read_back_as_nan(dtype, D):
     torch.cuda.synchronize()
     for o in out:
         assert np.array_equal(torch.isnan(o).cpu().numpy(), np.repeat(~np.isfinite(scale)[..., None], D, -1))
+
+
+def _cache(B, lens, H_kv, D, ps=16, shared=0, seed=7):
+    """(K pool, V pool, block table [B, slots]) with the first `shared` pages of all sequences the same,
+    and one more of two of them."""
+    g = torch.Generator().manual_seed(seed)
+    slots = (max(lens) + ps - 1) // ps
+    bt = torch.arange(B * slots, dtype=torch.int32).view(B, slots)
+    bt[:, :shared] = bt[0, :shared]
+    if shared:
+        bt[3, shared] = bt[2, shared]  # a deeper node of the last two
+    pools = [torch.randn(B * slots, ps, H_kv, D, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2)]
+    return *pools, bt.to(DEV)
+
+
+def _q(*shape):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).to(DEV)
+
+
+def _codes(t):
+    """e4m3 codes and per-row scales of t."""
+    code, scale = oracle.quantize_token_groups(t.float().cpu().numpy())
+    return torch.from_numpy(code).to(DEV), torch.from_numpy(scale).to(DEV)
+
+
+LENS = [1500, 33, 700, 64]
+
+
+def _runs(which):
+    """A query [..., heads, D] (last but one dimension: heads) and the call over it."""
+    lens = torch.tensor(LENS, dtype=torch.int32, device=DEV)
+    args = dict(seq_lens=lens, scale=0.1, return_lse=True)
+    if which.startswith("mla"):
+        pool, _, bt = _cache(4, LENS, 1, 576, ps=64)
+        pool = pool.view(-1, 64, 576)
+        q = _q(4, *((2,) if which.endswith("multi") else ()), 128, 576)
+        if which == "mla_fp8":
+            kv, scale = _codes(pool)
+            q_code, q_scale = _codes(q)
+            # NaN of the query's row reaches the kernel as its scale
+            return q, lambda x: ts.ts_mla_paged_decode_fp8(
+                q_code, torch.where(torch.isnan(x).any(-1), torch.full_like(q_scale, float("nan")), q_scale), kv,
+                scale, bt, **args)
+        fn = ts.ts_mla_paged_decode_multi if which.endswith("multi") else ts.ts_mla_paged_decode
+        return q, lambda x: fn(x, pool, bt, **args)
+    D, shared = (64, 2) if which.startswith("cascade") else (128, 0)
+    k, v, bt = _cache(4, LENS, 8, D, shared=shared)
+    if which.startswith("multi"):
+        return _q(4, 4, 32, 128), lambda x: ts.ts_paged_decode_multi_attn(x, k, v, bt, **args)
+    q = _q(4, 32, D)
+    if which.startswith("fp8"):
+        kc, vc, ks, vs = (c for pair in zip(*(_codes(t) for t in (k, v))) for c in pair)
+        return q, lambda x: ts.ts_paged_decode_fp8_attn(x, kc, vc, ks, vs, bt, **args)
+    host = (bt.cpu().numpy(), np.array(LENS, dtype=np.int32), 16)
+    if which == "cascade":
+        groups = ts.groups_to_device(ts.ts_group_prefixes(*host), DEV)
+        return q, lambda x, key=k: ts.ts_cascade_decode_attn(x, key, v, groups, bt, **args)
+    forest = ts.forest_to_device(ts.ts_group_prefixes_nested(*host), DEV)
+    return q, lambda x, key=k: ts.ts_cascade_nested_decode_attn(x, key, v, forest, bt, **args)
+
+
+PATHS = {"multi_cuda": ("TS_MULTI_QUERY_PATH", "cuda"), "multi_tensor": ("TS_MULTI_QUERY_PATH", "tensor"),
+         "fp8_cuda": ("TS_FP8_DECODE_PATH", "cuda"), "fp8_tensor": ("TS_FP8_DECODE_PATH", "tensor"),
+         "fp8_mma": ("TS_FP8_DECODE_PATH", "mma")}
+
+
+@pytest.mark.parametrize("which", [*PATHS, "cascade", "cascade_nested", "mla", "mla_multi", "mla_fp8"])
+def test_other_decode_calls_give_nan_for_a_query_that_is_not_finite(which, monkeypatch):
+    """That row's O and LSE are NaN; the others are those of the clean query. Both runs round the weights
+    (bf16, 2^-8 of each at most, the sum of weighted |V| below the largest |V|) and the output (2^-8)."""
+    if which in PATHS:
+        monkeypatch.setenv(*PATHS[which])
+    q, call = _runs(which)
+    clean, clean_lse = call(q)
+    spoiled = q.clone()
+    rows = [(0, 5), (1, 0), (2, 31)]
+    for b, h in rows:
+        spoiled[b, ..., h, 3] = float("nan")
+    out, lse = call(spoiled)
+    torch.cuda.synchronize()
+    bad = torch.isnan(spoiled).any(-1)
+    assert torch.isnan(lse[bad]).all(), lse[bad]
+    assert torch.isnan(out[bad]).all()
+    top = 5.5  # |V| of 10^6 standard normal values
+    assert ((out[~bad].float() - clean[~bad].float()).abs() <= 2.0 ** -7 * (top + clean[~bad].float().abs())).all()
+    assert ((lse[~bad] - clean_lse[~bad]).abs() <= 2.0 ** -20 * clean_lse[~bad].abs().clamp(min=16)).all()
+
+
+@pytest.mark.parametrize("which", ["cascade", "cascade_nested"])
+def test_a_shared_prefix_that_is_not_finite_is_not_dropped(which):
+    """A NaN key of a shared page reaches every member of the group, at the heads of its kv head."""
+    q, call = _runs(which)
+    k, _, bt = _cache(4, LENS, 8, 64, shared=2)
+    k[bt[0, 1].item(), 7, 2, 0] = float("nan")
+    out, lse = call(q, k)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[:, 8:12]).all() and torch.isnan(lse[:, 8:12]).all()
+    for heads in (slice(0, 8), slice(12, 32)):
+        assert torch.isfinite(out[:, heads]).all() and torch.isfinite(lse[:, heads]).all()

@@ -19,7 +19,8 @@
 // split over as many CTAs as the device has room for twice over; the parts are
 // joined by LSE (16 tokens over 28,000: 0.43 ms, with one part 5.5 ms). The
 // number of parts is one for the whole batch, from its counts of rows and
-// sequences: a long context among many short chunks is not split further.
+// sequences: a long context among many short chunks is not split further (16
+// tokens over 28,000 beside 63 chunks of one token: 7.0 ms).
 #include <algorithm>
 #include <cmath>
 

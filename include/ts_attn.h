@@ -267,8 +267,8 @@ TS_API ts_status ts_paged_decode_sink_attn(const void* q, const void* k_pool, co
  * seq_lens serve ts_kv_append_chunk (or ts_kv_append_chunk_fp8) and then
  * ts_paged_prefill_attn. q_indptr is device int32 [B + 1], not decreasing,
  * within [0, T]. Rows outside [q_indptr[0], q_indptr[B]) (padding of a captured
- * graph) are memory like the others, of the inputs too: inputs there may be
- * read, whatever they hold has no effect, and no result is written there.
+ * graph) belong to no sequence: all T rows of the inputs must be readable
+ * memory, what the padding holds has no effect, and no result is written there.
  * Entries out of order never cause an access out of range; which rows are then
  * taken is not defined. n == 0 is a sequence without new tokens. Two sequences
  * of one call that write the same page row leave either's values there.

@@ -398,6 +398,224 @@ TS_API ts_status ts_paged_prefill_attn(const void* q, int64_t q_stride, const vo
                                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * A long-context step. ts_kv_append_chunk_rope takes a step's rows from the
+ * projection to the cache; ts_kv_page_bounds keeps, beside each page, bounds of
+ * its keys; ts_select_pages picks the pages of each sequence whose bounds promise
+ * most for a query; ts_paged_decode_sparse_attn attends those alone. ts_kv_fork
+ * and ts_kv_compact share, copy and move the pages, their scales and bounds with
+ * them. They go beyond the pages' text (SwiftLLM page, section 3.1: blocks on
+ * demand through a table; tokenspeed 딥다이브, section 6-4: scales per token
+ * group), with the same pools, tables and lengths as the calls above.
+ */
+
+/*
+ * ts_kv_append_chunk_rope - normalise and rotate the queries and keys of prompt
+ * chunks, and write K and V into the pools.
+ *
+ * Of every head row x of q and k_new, in float32, rounded once:
+ *   y = w x / sqrt(mean(x^2) + eps) where weights w are given, else y = x;
+ *   the pair j < rot_dim / 2 of its first rot_dim columns, (j, j + rot_dim / 2),
+ *   or (2 j, 2 j + 1) if interleaved, turns by a = position * inv_freq[j]:
+ *   (y1 cos a - y2 sin a, y2 cos a + y1 sin a). Other columns stay.
+ * Angles hold to float32 at any position. Rows, positions and placement as
+ * ts_kv_append_chunk; V is copied bit for bit, and so are K columns that neither
+ * a weight nor a rotation touches. A decode step is n = 1 for every sequence.
+ *
+ *   q             device [T, H_q, D] of dtype, rows q_stride elements apart
+ *   k_new, v_new  device [T, H_kv, D] of dtype, rows new_stride elements apart
+ *   q_weight,
+ *   k_weight      device [D] of dtype, or NULL: that tensor is not normalised
+ *   eps           >= 0, finite
+ *   inv_freq      device float32 [rot_dim / 2], finite; radians per position
+ *                 (NULL if rot_dim == 0)
+ *   k_pool,v_pool device [num_pages, page_size, H_kv, D] of dtype (written)
+ *   q_out         device [T, H_q, D] of dtype, rows q_out_stride elements apart
+ *                 (written). It may be q itself with the same row step.
+ * Rows of no sequence and rows at a negative position are left as they were in
+ * q_out; K and V rows whose slot or page is out of range are skipped.
+ * Supported: D in {64, 128}, rot_dim a multiple of 8 up to D, up to 4096 heads,
+ * row steps multiples of 16 bytes, any page_size. T == 0 or B == 0 returns TS_OK
+ * with nothing enqueued. Tensors are 16-byte aligned.
+ */
+TS_API ts_status ts_kv_append_chunk_rope(const void* q, int64_t q_stride, const void* k_new, const void* v_new,
+                                         int64_t new_stride, const void* q_weight, const void* k_weight,
+                                         float eps, const float* inv_freq, int32_t rot_dim, int32_t interleaved,
+                                         void* k_pool, void* v_pool, const int32_t* block_table,
+                                         int32_t bt_stride, const int32_t* seq_lens, const int32_t* q_indptr,
+                                         int32_t T, int32_t B, int32_t H_q, int32_t H_kv, int32_t D,
+                                         int32_t page_size, int32_t num_pages, ts_dtype dtype, void* q_out,
+                                         int64_t q_out_stride, void* stream);
+
+/*
+ * ts_kv_page_bounds - bounds of the keys of every page that holds a new token.
+ *
+ * For each page that holds one of the rows of seq_lens and q_indptr (as in
+ * ts_kv_append_chunk, whose K rows are in the pool already), and each kv head,
+ * over the page's tokens that the sequence holds: M[d] = max K[t, d], m[d] = min
+ * K[t, d], s = max(max |M|, max |m|, 1e-10) * (1 / 127), as codes
+ *   bounds[page, h, 0, d] = min(ceil(M[d] / s), 127),
+ *   bounds[page, h, 1, d] = max(floor(m[d] / s), -127),
+ * in float32, and bound_scale[page, h] = s. A page with a key that is infinite or
+ * NaN gets s = infinity and codes 0, which ts_select_pages ranks first. Other
+ * pages are left as they were. Pages are computed anew from their keys: a call
+ * may be repeated, and q_indptr over whole sequences (n = L) covers them whole.
+ *
+ *   k_pool       device [num_pages, page_size, H_kv, D] of dtype
+ *   bounds       device int8 [num_pages, H_kv, 2, D] (written), 16-byte aligned
+ *   bound_scale  device float32 [num_pages, H_kv] (written)
+ *   T            rows of q_indptr's ranges; rows from T on are not looked at
+ * Supported: D in {64, 128}, up to 4096 heads, any page_size.
+ */
+TS_API ts_status ts_kv_page_bounds(const void* k_pool, int8_t* bounds, float* bound_scale,
+                                   const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                   const int32_t* q_indptr, int32_t T, int32_t B, int32_t H_kv, int32_t D,
+                                   int32_t page_size, int32_t num_pages, ts_dtype dtype, void* stream);
+
+/*
+ * ts_select_pages_workspace_size - workspace bytes for ts_select_pages. Returns
+ * 0 on invalid or unsupported arguments.
+ */
+TS_API size_t ts_select_pages_workspace_size(int32_t B, int32_t q_len, int32_t H_kv, int32_t bt_stride);
+
+/*
+ * ts_select_pages - choose, for every query row and kv head, the pages that
+ * ts_paged_decode_sparse_attn attends.
+ *
+ * Query token j of sequence b sits at position p = seq_lens[b] - q_len + j and
+ * has n = p / page_size + 1 pages. n <= pages: all of them. Otherwise the first
+ * `first`, the last `last`, and of the rest the pages - first - last of highest
+ * score. The score of a page is the largest over the g query heads of
+ *   (dot * qs) * bound_scale[page, h],  dot = sum_d max(c[d] M'[d], c[d] m'[d]),
+ * where M', m' are the page's codes (ts_kv_page_bounds), qs = max(max |q|, 1e-10)
+ * * (1 / 127) and c[d] = round(q[d] / qs) to nearest even: a bound of the
+ * quantized query's product with any key of the page. dot is a whole number, the
+ * products float32: equal inputs choose equal pages on every device. Of equal
+ * scores the lowest page counts first. A score of NaN (a query or page that is
+ * not finite) counts as the highest; a page whose id is out of range as the
+ * lowest, and sets TS_DEVERR_PAGE_RANGE.
+ *
+ *   q          device [B, q_len, H_q, D] of dtype
+ *   seq_lens   device int32 [B], the q_len new tokens counted
+ *   page_idx   device int32 [B, q_len, H_kv, pages] (written): slots of the
+ *              sequence's block-table row, ascending; -1 behind the last
+ *   first >= 0, last >= 1, first + last <= pages
+ *   workspace  >= ts_select_pages_workspace_size(B, q_len, H_kv, bt_stride)
+ *              bytes, 256-byte aligned, the error word in front
+ * Pages past the block table's row do not take part (TS_DEVERR_PAGE_RANGE).
+ * Supported: D in {64, 128}, H_q / H_kv and H_kv in {1, 2, 4, 8}, any page_size,
+ * up to 65,535 query rows. B == 0 returns TS_OK with nothing enqueued.
+ */
+TS_API ts_status ts_select_pages(const void* q, const int8_t* bounds, const float* bound_scale,
+                                 const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                 int32_t B, int32_t q_len, int32_t H_q, int32_t H_kv, int32_t D,
+                                 int32_t page_size, int32_t num_pages, int32_t pages, int32_t first,
+                                 int32_t last, ts_dtype dtype, int32_t* page_idx, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * ts_paged_decode_sparse_workspace_size - workspace bytes for
+ * ts_paged_decode_sparse_attn. Depends on the device's SM count. Returns 0 on
+ * invalid or unsupported arguments.
+ */
+TS_API size_t ts_paged_decode_sparse_workspace_size(int32_t B, int32_t q_len, int32_t H_q, int32_t H_kv,
+                                                    int32_t D, int32_t page_size, int32_t pages);
+
+/*
+ * ts_paged_decode_sparse_attn - decode attention over listed pages.
+ *
+ * ts_paged_decode_multi_attn's operation where each query row and kv head has a
+ * list of block-table slots of its own: token j of sequence b, at position p =
+ * seq_lens[b] - q_len + j, attends the tokens t <= p whose slot t / page_size is
+ * listed. Entries may come in any order; -1 (any negative) and slots behind p are
+ * skipped; a slot that is listed twice counts twice. A row that sees no token
+ * gets O = 0, LSE = -inf. With all slots listed it is
+ * ts_paged_decode_multi_attn's result.
+ *
+ *   q         device [B, q_len, H_q, D] of dtype
+ *   page_idx  device int32 [B, q_len, H_kv, pages]
+ *   out       device [B, q_len, H_q, D] of dtype (written)
+ *   lse       device float32 [B, q_len, H_q] (written) or NULL
+ *   workspace >= ts_paged_decode_sparse_workspace_size(...) bytes, 256-byte
+ *             aligned, the error word in front
+ *   other arguments and errors as in ts_paged_decode_attn.
+ * A listed page whose id is out of range, or whose slot lies past the block
+ * table's row, counts as absent and sets TS_DEVERR_PAGE_RANGE. What rows behind
+ * a query's position hold (NaN included) has no effect on it. The lists are cut
+ * over the SMs by sizes and the device alone: equal calls give equal bits.
+ * Supported: D in {64, 128}, H_q / H_kv and H_kv in {1, 2, 4, 8}, page_size in
+ * {8, 16, 32}, up to 2^24 query rows.
+ */
+TS_API ts_status ts_paged_decode_sparse_attn(const void* q, const void* k_pool, const void* v_pool,
+                                             const int32_t* block_table, int32_t bt_stride,
+                                             const int32_t* seq_lens, const int32_t* page_idx, int32_t pages,
+                                             int32_t B, int32_t q_len, int32_t H_q, int32_t H_kv, int32_t D,
+                                             int32_t page_size, int32_t num_pages, float scale, ts_dtype dtype,
+                                             void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                             void* stream);
+
+/*
+ * ts_kv_fork - let sequences continue in several ways: each child shares its
+ * parent's whole pages and gets a copy of the last, partly filled one.
+ *
+ * For each i < n, with L = seq_lens[parents[i]]: row children[i] of the block
+ * table takes the parent's first ceil(L / page_size) slots and the length L. If
+ * L is no multiple of page_size, the last of them becomes page fresh[i] instead,
+ * and the parent's page is copied there in every buffer; else fresh[i] is not
+ * used. Slots behind keep their values.
+ *
+ *   buffers      HOST array [n_buffers] of device pointers, each [num_pages] of
+ *                page_bytes[i] bytes: K, V, scales, bounds, of any layers
+ *   page_bytes   HOST array [n_buffers], each in [1, 2^30] (fastest where the
+ *                page and the pointer are multiples of 16 bytes)
+ *   block_table  device int32 [B, bt_stride], seq_lens device int32 [B] (both
+ *                written at the children's rows)
+ *   parents, children, fresh  device int32 [n]
+ * A child must not be listed twice nor be a parent in the same call, and fresh
+ * pages must be distinct and held by no sequence (else the results are not
+ * defined). An entry is skipped whole if a row is out of range, child and parent
+ * are one row, L is negative or longer than the table's row, or its last page or
+ * fresh page is needed and out of range. n == 0 or B == 0: nothing is enqueued.
+ */
+TS_API ts_status ts_kv_fork(void* const* buffers, const int64_t* page_bytes, int32_t n_buffers,
+                            int32_t* block_table, int32_t bt_stride, int32_t* seq_lens, int32_t B,
+                            const int32_t* parents, const int32_t* children, const int32_t* fresh, int32_t n,
+                            int32_t page_size, int32_t num_pages, void* stream);
+
+/*
+ * ts_kv_compact_workspace_size - workspace bytes for ts_kv_compact. 0 on invalid
+ * arguments.
+ */
+TS_API size_t ts_kv_compact_workspace_size(int32_t num_pages);
+
+/*
+ * ts_kv_compact - move the pages in use to the front of the pool; the rest is
+ * free.
+ *
+ * A page is held if one of the first ceil(seq_lens[b] / page_size) slots of some
+ * row b of the block table names it (several may). With U held pages: those below
+ * U stay, the i-th held page from U on moves to the i-th free page below U, both
+ * in ascending order, in every buffer. Afterwards pages U .. num_pages - 1 are
+ * free: a sequence is freed by leaving it out of the table (or by length 0).
+ *
+ *   buffers, page_bytes  as ts_kv_fork
+ *   block_table  device int32 [B, bt_stride]
+ *   table_out    device int32 [B, bt_stride] (written): block_table with the held
+ *                slots' new pages; all other slots as they are. It may be
+ *                block_table itself.
+ *   page_map     device int32 [num_pages] (written): each held page's new id, -1
+ *                for a free one
+ *   used         device int32 [1] (written): U
+ *   workspace    >= ts_kv_compact_workspace_size(num_pages) bytes, 256-byte aligned
+ * Page ids out of range are left as they are. A page that only others know of
+ * (a cache of prefixes) must be listed in a row of the table to be kept.
+ */
+TS_API ts_status ts_kv_compact(void* const* buffers, const int64_t* page_bytes, int32_t n_buffers,
+                               const int32_t* block_table, int32_t* table_out, int32_t bt_stride,
+                               const int32_t* seq_lens, int32_t B, int32_t page_size, int32_t num_pages,
+                               int32_t* page_map, int32_t* used, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
  * ts_paged_decode_multi_workspace_size - workspace bytes for
  * ts_paged_decode_multi_attn (B sequences of q_len query tokens). Returns 0 on
  * invalid arguments.

@@ -103,6 +103,21 @@ _SIGNATURES = {
     "ts_paged_prefill_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
     "ts_paged_prefill_attn": (ctypes.c_int, [_VP, _I64, _VP, _VP, _VP, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I32,
                                              _I32, _I32, _I32, _I32, _F32, ctypes.c_int, _VP, _VP, _VP, _SZ, _VP]),
+    "ts_kv_append_chunk_rope": (ctypes.c_int, [_VP, _I64, _VP, _VP, _I64, _VP, _VP, _F32, _VP, _I32, _I32, _VP, _VP,
+                                               _VP, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                               ctypes.c_int, _VP, _I64, _VP]),
+    "ts_kv_page_bounds": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _I32,
+                                         ctypes.c_int, _VP]),
+    "ts_select_pages_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
+    "ts_select_pages": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I32, _VP, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                       _I32, _I32, ctypes.c_int, _VP, _VP, _SZ, _VP]),
+    "ts_paged_decode_sparse_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32]),
+    "ts_paged_decode_sparse_attn": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I32,
+                                                   _I32, _I32, _I32, _F32, ctypes.c_int, _VP, _VP, _VP, _SZ, _VP]),
+    "ts_kv_fork": (ctypes.c_int, [_VP, _VP, _I32, _VP, _I32, _VP, _I32, _VP, _VP, _VP, _I32, _I32, _I32, _VP]),
+    "ts_kv_compact_workspace_size": (_SZ, [_I32]),
+    "ts_kv_compact": (ctypes.c_int, [_VP, _VP, _I32, _VP, _VP, _I32, _VP, _I32, _I32, _I32, _VP, _VP, _VP, _SZ,
+                                     _VP]),
     "ts_paged_decode_multi_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
     "ts_paged_decode_multi_attn": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I32, _VP, _I32, _I32, _I32, _I32, _I32,
                                                   _I32, _I32, _F32, ctypes.c_int, _VP, _VP, _VP, _SZ, _VP]),
@@ -458,6 +473,230 @@ def ts_paged_prefill_attn(q, k_pool, v_pool, block_table, seq_lens, q_indptr, sc
                                        P, int(window), int(sinks), float(scale), _dt(q), op, lp, wp,
                                        workspace.nbytes, _stream(stream)))
     return (out, lse) if return_lse else out
+
+
+def ts_kv_append_chunk_rope(q, k_new, v_new, k_pool, v_pool, block_table, seq_lens, q_indptr, inv_freq=None,
+                            q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_out=None,
+                            stream=None):
+    """Normalise (where weights are given) and rotate the queries [T, H_q, D] and keys [T, H_kv, D]
+    of a ragged batch of chunks by their positions, and write K and V into the pools (see
+    ts_attn.h). ``inv_freq`` (float32, radians per position) has one entry per rotated pair.
+    Rows may be a part of wider rows. Returns the queries, in ``q_out`` (which may be ``q``)."""
+    B = _require_chunks(seq_lens, q_indptr, block_table)
+    T, H_q, D = q.shape
+    if not q.dtype == k_new.dtype == k_pool.dtype == v_pool.dtype:
+        raise TypeError("queries, new rows and pools must have one dtype")
+    k, v, step = _chunk_rows(k_new, v_new, k_pool, v_pool)
+    P, ps, H_kv, D_pool = k_pool.shape
+    if D != D_pool or T != k_new.shape[0]:
+        raise ValueError("q must be [T, H_q, D] with the new rows' T and D")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != q.dtype or w.shape != (D,)):
+            raise ValueError("weights must be [D] of the queries' dtype")
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
+            raise TypeError("inv_freq must be float32 [rot_dim / 2]")
+        rot = 2 * inv_freq.shape[0]
+    qp, q_step = _rows(q)
+    if q_out is None:
+        with _made_for(stream):
+            q_out = torch.empty(T, H_q, D, dtype=q.dtype, device=q.device)
+    if q_out.dtype != q.dtype or q_out.shape != q.shape:
+        raise ValueError("q_out must have the queries' shape and dtype")
+    op, out_step = _rows(q_out)
+    at = k_pool.get_device()
+    if q.get_device() != at or q_out.get_device() != at:
+        raise ValueError("queries and pools must be on one device")
+    kp, vp, bt, lens, ptr, freq, qw, kw = _pointers(k_pool, v_pool, block_table, seq_lens, q_indptr, inv_freq, q_weight,
+                                                    k_weight)
+    _check(lib().ts_kv_append_chunk_rope(qp, q_step, k, v, step, qw, kw, eps, freq, rot, bool(interleaved), kp, vp, bt,
+                                         block_table.shape[1], lens, ptr, T, B, H_q, H_kv, D, ps, P, _dt(q), op,
+                                         out_step, _stream(stream)))
+    return q_out
+
+
+def _require_bounds(bounds, bound_scale, D):
+    """Page bounds int8 [num_pages, H_kv, 2, D] and their scales float32 [num_pages, H_kv]."""
+    if bounds.dtype != torch.int8 or bound_scale.dtype != torch.float32:
+        raise TypeError("page bounds are int8, their scales float32")
+    if bounds.dim() != 4 or bounds.shape[2] != 2 or bounds.shape[3] != D or bound_scale.shape != bounds.shape[:2]:
+        raise ValueError("page bounds must be [num_pages, H_kv, 2, D], their scales [num_pages, H_kv]")
+
+
+def ts_kv_page_bounds(k_pool, bounds, bound_scale, block_table, seq_lens, q_indptr, rows: int, stream=None) -> None:
+    """Bounds of the keys of every page that holds one of the newest tokens (those of ``q_indptr``,
+    ``rows`` in all), into ``bounds`` int8 [num_pages, H_kv, 2, D] and ``bound_scale`` float32
+    [num_pages, H_kv] (see ts_attn.h). Other pages' bounds stay."""
+    B = _require_chunks(seq_lens, q_indptr, block_table)
+    P, ps, H_kv, D = k_pool.shape
+    _require_bounds(bounds, bound_scale, D)
+    if bounds.shape[:2] != (P, H_kv):
+        raise ValueError("page bounds must have the pool's pages and kv heads")
+    kp, bp, sp, bt, lens, ptr = _pointers(k_pool, bounds, bound_scale, block_table, seq_lens, q_indptr)
+    _check(lib().ts_kv_page_bounds(kp, bp, sp, bt, block_table.shape[1], lens, ptr, rows, B, H_kv, D, ps, P,
+                                   _dt(k_pool), _stream(stream)))
+
+
+def ts_select_pages_workspace_size(B: int, q_len: int, H_kv: int, bt_stride: int) -> int:
+    return int(lib().ts_select_pages_workspace_size(B, q_len, H_kv, bt_stride))
+
+
+def ts_select_pages(q, bounds, bound_scale, block_table, seq_lens, page_size: int, pages: int, first: int = 1,
+                    last: int = 1, page_idx=None, workspace=None, stream=None):
+    """The ``pages`` slots of each sequence whose page bounds promise most, for every query row and
+    kv head: q [B, H_q, D] or [B, q_len, H_q, D] -> int32 [B, (q_len,) H_kv, pages], ascending,
+    -1 behind the last; the first ``first`` and last ``last`` pages are always among them
+    (see ts_attn.h)."""
+    B = _require_chunks(seq_lens, None, block_table)
+    shape = q.shape
+    q_len = 1 if len(shape) == 3 else shape[1]
+    H_q, D = shape[-2:]
+    _require_bounds(bounds, bound_scale, D)
+    P, H_kv = bound_scale.shape
+    if shape[0] != B or len(shape) not in (3, 4):
+        raise ValueError("q must be [B, H_q, D] or [B, q_len, H_q, D]")
+    want = (*shape[:-2], H_kv, pages)
+    if page_idx is None:
+        with _made_for(stream):
+            page_idx = torch.empty(want, dtype=_INT32, device=q.device)
+    elif page_idx.dtype != _INT32 or page_idx.shape != want:
+        raise ValueError("page_idx must be int32 [B, (q_len,) H_kv, pages]")
+    qp, bp, sp, bt, lens, ip, wp = _pointers(q, bounds, bound_scale, block_table, seq_lens, page_idx, workspace)
+    if workspace is None:
+        with _made_for(stream):
+            workspace = new_workspace(ts_select_pages_workspace_size(B, q_len, H_kv, block_table.shape[1]), q.device)
+        wp = workspace.data_ptr()
+    _check(lib().ts_select_pages(qp, bp, sp, bt, block_table.shape[1], lens, B, q_len, H_q, H_kv, D, page_size, P, pages,
+                                 first, last, _dt(q), ip, wp, workspace.nbytes, _stream(stream)))
+    return page_idx
+
+
+def ts_paged_decode_sparse_workspace_size(B: int, q_len: int, H_q: int, H_kv: int, D: int, page_size: int,
+                                          pages: int) -> int:
+    return int(lib().ts_paged_decode_sparse_workspace_size(B, q_len, H_q, H_kv, D, page_size, pages))
+
+
+def ts_paged_decode_sparse_attn(q, k_pool, v_pool, block_table, seq_lens, page_idx, scale: float, out=None, lse=None,
+                                workspace=None, stream=None, return_lse: bool = False):
+    """Decode attention over listed pages: q [B, H_q, D] or [B, q_len, H_q, D], ``page_idx`` int32
+    [B, (q_len,) H_kv, pages] of block-table slots (negative: none; see ts_select_pages). Token j of
+    a sequence, at position ``seq_lens[b] - q_len + j``, attends the listed pages' tokens up to
+    itself. Returns ``out`` (and ``lse``)."""
+    B = _require_chunks(seq_lens, None, block_table)
+    shape = q.shape
+    q_len = 1 if len(shape) == 3 else shape[1]
+    H_q, D = shape[-2:]
+    P, ps, H_kv, D_pool = k_pool.shape
+    if k_pool.dtype != q.dtype or v_pool.dtype != q.dtype:
+        raise TypeError("queries and pools must have one dtype")
+    if k_pool.shape != v_pool.shape or D_pool != D:
+        raise ValueError("pools must be [num_pages, page_size, H_kv, D] with the queries' D")
+    if shape[0] != B or len(shape) not in (3, 4):
+        raise ValueError("q must be [B, H_q, D] or [B, q_len, H_q, D]")
+    pages = page_idx.shape[-1]
+    if page_idx.dtype != _INT32 or page_idx.shape != (*shape[:-2], H_kv, pages):
+        raise ValueError("page_idx must be int32 [B, (q_len,) H_kv, pages]")
+    if out is None:
+        with _made_for(stream):
+            out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        with _made_for(stream):
+            lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+    if out.dtype != q.dtype or out.shape != shape:
+        raise ValueError("out must have the queries' shape and dtype")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:-1]):
+        raise ValueError("lse must be float32 of the queries' rows and heads")
+    qp, kp, vp, bt, lens, ip, op, lp, wp = _pointers(q, k_pool, v_pool, block_table, seq_lens, page_idx, out, lse,
+                                                     workspace)
+    if workspace is None:
+        with _made_for(stream):
+            workspace = new_workspace(ts_paged_decode_sparse_workspace_size(B, q_len, H_q, H_kv, D, ps, pages), q.device)
+        wp = workspace.data_ptr()
+    _check(lib().ts_paged_decode_sparse_attn(qp, kp, vp, bt, block_table.shape[1], lens, ip, pages, B, q_len, H_q, H_kv,
+                                             D, ps, P, scale, _dt(q), op, lp, wp, workspace.nbytes, _stream(stream)))
+    return (out, lse) if return_lse else out
+
+
+class KVBuffers:
+    """The buffers of a cache that one block table serves, for ts_kv_fork and ts_kv_compact: tensors
+    [num_pages, ...], kept alive by this object."""
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        self.num_pages = self.tensors[0].shape[0] if self.tensors else 0
+        for t in self.tensors:
+            if t.dim() < 1 or t.shape[0] != self.num_pages:
+                raise ValueError("buffers must have one number of pages")
+        pointers = _pointers(*self.tensors)
+        n = len(pointers)
+        self.count = n
+        self.device = self.tensors[0].get_device() if n else -1
+        self._data = (ctypes.c_void_p * n)(*pointers)
+        self._bytes = (ctypes.c_int64 * n)(*(t.nbytes // max(1, self.num_pages) for t in self.tensors))
+        self.data, self.page_bytes = ctypes.addressof(self._data), ctypes.addressof(self._bytes)
+
+
+def kv_buffers(tensors) -> KVBuffers:
+    """A cache's tensors [num_pages, ...] (K, V, scales, bounds, of any layers) as one handle."""
+    return KVBuffers(tensors)
+
+
+def _require_buffers(buffers, block_table):
+    if not isinstance(buffers, KVBuffers):
+        buffers = KVBuffers(buffers)
+    if buffers.count == 0:
+        raise ValueError("a cache has one buffer at least")
+    if buffers.device != block_table.get_device():
+        raise ValueError("buffers and block table must be on one device")
+    return buffers
+
+
+def ts_kv_fork(buffers, block_table, seq_lens, parents, children, fresh, page_size: int, stream=None) -> None:
+    """Row ``children[i]`` of ``block_table`` and ``seq_lens`` becomes a continuation of row
+    ``parents[i]``: whole pages are shared, a partly filled last page is copied to page ``fresh[i]``
+    in all ``buffers`` (a list of tensors [num_pages, ...], or kv_buffers of one). See ts_attn.h."""
+    B = _require_chunks(seq_lens, None, block_table)
+    buffers = _require_buffers(buffers, block_table)
+    n = parents.numel()
+    for t in (parents, children, fresh):
+        if t.dtype != _INT32 or t.numel() != n:
+            raise TypeError("parents, children and fresh must be int32 of one length")
+    bt, lens, pp, cp, fp = _pointers(block_table, seq_lens, parents, children, fresh)
+    _check(lib().ts_kv_fork(buffers.data, buffers.page_bytes, buffers.count, bt, block_table.shape[1], lens, B, pp, cp,
+                            fp, n, page_size, buffers.num_pages, _stream(stream)))
+
+
+def ts_kv_compact_workspace_size(num_pages: int) -> int:
+    return int(lib().ts_kv_compact_workspace_size(num_pages))
+
+
+def ts_kv_compact(buffers, block_table, seq_lens, page_size: int, table_out=None, page_map=None, used=None,
+                  workspace=None, stream=None):
+    """Move the pages that the rows of ``block_table`` hold to the front of all ``buffers`` (a list of
+    tensors [num_pages, ...], or kv_buffers of one). Returns the new block table (``table_out``, which
+    may be ``block_table``), each page's new id (-1: free) and the number of pages in use (int32 [1]):
+    the pages from there on are free. See ts_attn.h."""
+    B = _require_chunks(seq_lens, None, block_table)
+    buffers = _require_buffers(buffers, block_table)
+    P, device = buffers.num_pages, block_table.device
+    with _made_for(stream):
+        if table_out is None:
+            table_out = torch.empty_like(block_table)
+        if page_map is None:
+            page_map = torch.empty(P, dtype=_INT32, device=device)
+        if used is None:
+            used = torch.empty(1, dtype=_INT32, device=device)
+        if workspace is None:
+            workspace = new_workspace(ts_kv_compact_workspace_size(P), device)
+    if table_out.dtype != _INT32 or page_map.dtype != _INT32 or used.dtype != _INT32:
+        raise TypeError("tables and page ids must be int32")
+    if table_out.shape != block_table.shape or page_map.numel() != P or used.numel() != 1:
+        raise ValueError("table_out must be the block table's shape, page_map [num_pages], used [1]")
+    bt, to, lens, mp, up, wp = _pointers(block_table, table_out, seq_lens, page_map, used, workspace)
+    _check(lib().ts_kv_compact(buffers.data, buffers.page_bytes, buffers.count, bt, to, block_table.shape[1], lens, B,
+                               page_size, P, mp, up, wp, workspace.nbytes, _stream(stream)))
+    return table_out, page_map, used
 
 
 def ts_paged_decode_attn_noalloc(q, k_pool, v_pool, block_table, seq_lens, scale: float, out, lse=None,

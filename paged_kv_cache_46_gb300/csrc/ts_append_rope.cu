@@ -1,0 +1,296 @@
+// ts_kv_append_chunk_rope: the rows of a ragged batch of prompt chunks (or one
+// new token per sequence) on their way from the projection to the attention:
+// queries and keys normalised per head and rotated by their positions, K and V
+// written into their pages, the queries into rows.
+//
+// Of a head's row x of D values, with weights w:
+//   y = w x / sqrt(mean(x^2) + eps)           (no weights: y = x)
+//   (y1, y2) -> (y1 cos a - y2 sin a, y2 cos a + y1 sin a),  a = position *
+//   inv_freq[j], for the pairs j < rot / 2 of its first rot columns: (j, j +
+//   rot / 2), or (2 j, 2 j + 1) where they are interleaved.
+// All in float32, rounded once to the stored type.
+//
+// Each value is read once and written once, and HBM bounds it.
+//
+// A warp takes a row, or one of `parts` shares of its heads where there are few
+// rows. D / 8 lanes hold a head, as two groups of four columns a lane, chosen so
+// that both columns of a pair are in one lane: nothing is exchanged but the sum
+// of squares. The heads of a step are taken kBatch steps at a time, loaded before
+// the row's place is known.
+//
+// Angles: a float32 product of position and frequency is off by 2^-24 of the
+// angle, a hundredth of a turn at position 131,072. Turns are counted in 64-bit
+// fixed point instead: inv_freq / (2 pi) mod 1 as a 64-bit fraction (one product
+// in float64), times the position modulo 2^64, is the angle in turns. Its nearest
+// quarter turn is taken off exactly and the rest, at most an eighth of a turn,
+// is rounded to float32 once: 2^-24 of pi / 4 at most.
+#include "ts_ragged.cuh"
+
+#include <cmath>
+
+namespace ts {
+namespace {
+
+constexpr int kWarps = 8;   // per CTA
+constexpr int kBatch = 4;   // steps in flight
+
+template <typename T>
+struct RopeParams {
+  const T* q;
+  const T* k_new;
+  const T* v_new;
+  const T* q_weight;
+  const T* k_weight;
+  const float* inv_freq;
+  T* k_pool;
+  T* v_pool;
+  T* q_out;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* q_indptr;
+  int64_t q_stride, new_stride, q_out_stride;
+  int32_t bt_stride, T_rows, B, H_q, H_kv, num_pages, rot, interleaved, parts;
+  float eps;
+  PageSize page_size;
+};
+
+// Four consecutive values as they are stored.
+template <typename T>
+struct Quad;
+template <>
+struct Quad<__nv_bfloat16> {
+  uint2 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = w; }
+  __device__ __forceinline__ void get(float (&x)[4]) const {
+    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+  }
+  __device__ __forceinline__ void set(const float (&x)[4]) {
+    w.x = float2_to_bf16x2(x[0], x[1]);
+    w.y = float2_to_bf16x2(x[2], x[3]);
+  }
+};
+template <>
+struct Quad<float> {
+  float4 w;
+  __device__ __forceinline__ void load(const float* p) { w = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = w; }
+  __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w; }
+  __device__ __forceinline__ void set(const float (&x)[4]) { w = make_float4(x[0], x[1], x[2], x[3]); }
+};
+
+// Cosine and sine of pos * inv_freq (see the head of this file).
+__device__ __forceinline__ float2 turn(int pos, float inv_freq) {
+  double f = static_cast<double>(inv_freq) * 0.15915494309189533577;  // 1 / (2 pi)
+  f -= floor(f);
+  const unsigned long long step = static_cast<unsigned long long>(f * 18446744073709551616.0);
+  const uint32_t t = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * step) >> 32);
+  const uint32_t quarter = (t + 0x20000000u) >> 30;
+  const int32_t rest = static_cast<int32_t>(t - (quarter << 30));  // within an eighth of a turn
+  float s, c;
+  sincospif(static_cast<float>(rest) * 4.656612873077392578125e-10f, &s, &c);  // 2^-31: in half turns
+  const float x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;
+  return make_float2((quarter + 1u) & 2u ? -x : x, quarter & 2u ? -y : y);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeParams<T> p) {
+  // Programmatic dependent launch as in ts_kv_append.
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  constexpr int kLanes = D / 8, kVecs = 32 / kLanes;
+  const int lane = threadIdx.x & 31;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t r = w / p.parts;
+  const int part = static_cast<int>(w - r * p.parts);
+  if (r >= p.T_rows) return;
+  const int l = lane % kLanes, vec = lane / kLanes;
+  const bool turns = l < p.rot / 8;
+  const bool split = turns && !p.interleaved;
+  const int oa = split ? 4 * l : 8 * l, ob = split ? p.rot / 2 + 4 * l : 8 * l + 4;
+  const int heads = p.H_q + 2 * p.H_kv;
+
+  Quad<T> xa[kBatch], xb[kBatch];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int hv = (s0 + u * p.parts) * kVecs + vec;
+      if (hv < heads) {
+        const T* src = hv < p.H_q            ? p.q + r * p.q_stride + hv * D
+                       : hv < p.H_q + p.H_kv ? p.k_new + r * p.new_stride + (hv - p.H_q) * D
+                                             : p.v_new + r * p.new_stride + (hv - p.H_q - p.H_kv) * D;
+        xa[u].load(src + oa);
+        xb[u].load(src + ob);
+      } else {
+        xa[u] = {};
+        xb[u] = {};
+      }
+    }
+  };
+  load(part);
+  const int b = ragged_sequence(p.q_indptr, p.B, static_cast<int>(r), lane);
+  if (b < 0) return;
+  const int pos = p.seq_lens[b] - (p.q_indptr[b + 1] - static_cast<int>(r));
+  if (pos < 0) return;
+  const int64_t row = pool_row(p.block_table, p.bt_stride, b, pos, p.page_size, p.num_pages);
+
+  // pair 4 l + i of the lane, i < 4: each of the kVecs lanes that share them computes 4 / kVecs
+  float2 cs[4];
+  {
+    constexpr int kOwn = 4 / kVecs;
+    float2 own[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      own[i] = turns ? turn(pos, p.inv_freq[4 * l + vec * kOwn + i]) : make_float2(1.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int from = i / kOwn * kLanes + l;
+      cs[i].x = __shfl_sync(0xffffffffu, own[i % kOwn].x, from);
+      cs[i].y = __shfl_sync(0xffffffffu, own[i % kOwn].y, from);
+    }
+  }
+
+  for (int s0 = part;;) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int hv = (s0 + u * p.parts) * kVecs + vec;
+      const bool is_q = hv < p.H_q, is_v = hv >= p.H_q + p.H_kv;
+      const T* weight = is_q ? p.q_weight : is_v ? nullptr : p.k_weight;
+      float a[4], c[4];
+      xa[u].get(a);
+      xb[u].get(c);
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ss = fmaf(a[i], a[i], fmaf(c[i], c[i], ss));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (weight != nullptr) {
+        const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+        Quad<T> wq;
+        float wt[4];
+        wq.load(weight + oa);
+        wq.get(wt);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = a[i] * inv * wt[i];
+        wq.load(weight + ob);
+        wq.get(wt);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = c[i] * inv * wt[i];
+      }
+      if (turns) {
+        if (p.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float a0 = a[2 * i], c0 = c[2 * i];
+            a[2 * i] = a0 * cs[i].x - a[2 * i + 1] * cs[i].y;
+            a[2 * i + 1] = a[2 * i + 1] * cs[i].x + a0 * cs[i].y;
+            c[2 * i] = c0 * cs[i + 2].x - c[2 * i + 1] * cs[i + 2].y;
+            c[2 * i + 1] = c[2 * i + 1] * cs[i + 2].x + c0 * cs[i + 2].y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a0 = a[i];
+            a[i] = a0 * cs[i].x - c[i] * cs[i].y;
+            c[i] = c[i] * cs[i].x + a0 * cs[i].y;
+          }
+        }
+      }
+      if (!is_v && (turns || weight != nullptr)) {  // V and untouched columns stay as they are, bit for bit
+        xa[u].set(a);
+        xb[u].set(c);
+      }
+      if (hv < heads && (is_q || row >= 0)) {
+        T* dst = is_q    ? p.q_out + r * p.q_out_stride + hv * D
+                 : is_v ? p.v_pool + (row * p.H_kv + (hv - p.H_q - p.H_kv)) * D
+                        : p.k_pool + (row * p.H_kv + (hv - p.H_q)) * D;
+        xa[u].store(dst + oa);
+        xb[u].store(dst + ob);
+      }
+    }
+    s0 += kBatch * p.parts;
+    if (s0 * kVecs >= heads) return;
+    load(s0);
+  }
+}
+
+template <typename T>
+ts_status launch(int D, const void* q, const void* k_new, const void* v_new, const void* q_weight,
+                 const void* k_weight, void* k_pool, void* v_pool, void* q_out, RopeParams<T>& p,
+                 cudaStream_t stream) {
+  p.q = static_cast<const T*>(q), p.k_new = static_cast<const T*>(k_new), p.v_new = static_cast<const T*>(v_new);
+  p.q_weight = static_cast<const T*>(q_weight), p.k_weight = static_cast<const T*>(k_weight);
+  p.k_pool = static_cast<T*>(k_pool), p.v_pool = static_cast<T*>(v_pool), p.q_out = static_cast<T*>(q_out);
+  const int steps = (p.H_q + 2 * p.H_kv + 256 / D - 1) / (256 / D);
+  // shares of a row: enough warps to fill the device twice over, each with a step at least
+  const int64_t want = static_cast<int64_t>(device_sm_count()) * 64;
+  p.parts = static_cast<int32_t>(want / p.T_rows);
+  if (p.parts < 1) p.parts = 1;
+  if (p.parts > steps) p.parts = steps;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(p.T_rows) * p.parts - 1) / kWarps + 1));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto kern = D == 64 ? rope_append_kernel<T, 64> : rope_append_kernel<T, 128>;
+  LaunchTrace trace("rope_append_kernel", stream);
+  return cuda_check(cudaLaunchKernelEx(&cfg, kern, p), "ts_kv_append_chunk_rope: launch");
+}
+
+}  // namespace
+}  // namespace ts
+
+extern "C" ts_status ts_kv_append_chunk_rope(const void* q, int64_t q_stride, const void* k_new, const void* v_new,
+                                             int64_t new_stride, const void* q_weight, const void* k_weight,
+                                             float eps, const float* inv_freq, int32_t rot_dim, int32_t interleaved,
+                                             void* k_pool, void* v_pool, const int32_t* block_table,
+                                             int32_t bt_stride, const int32_t* seq_lens, const int32_t* q_indptr,
+                                             int32_t T, int32_t B, int32_t H_q, int32_t H_kv, int32_t D,
+                                             int32_t page_size, int32_t num_pages, ts_dtype dtype, void* q_out,
+                                             int64_t q_out_stride, void* stream) {
+  using namespace ts;
+  const char* who = "ts_kv_append_chunk_rope";
+  if (T < 0 || B < 0 || H_q <= 0 || H_kv <= 0 || D <= 0 || page_size <= 0 || num_pages <= 0 || bt_stride <= 0)
+    return fail(TS_ERR_INVALID_ARG, "%s: bad sizes (T=%d B=%d H_q=%d H_kv=%d D=%d ps=%d P=%d bt=%d)", who, T, B, H_q,
+                H_kv, D, page_size, num_pages, bt_stride);
+  if (dtype != TS_F32 && dtype != TS_BF16)
+    return fail(TS_ERR_INVALID_ARG, "%s: bad dtype %d", who, static_cast<int>(dtype));
+  if (rot_dim < 0 || rot_dim > D)
+    return fail(TS_ERR_INVALID_ARG, "%s: rot_dim=%d outside [0, D=%d]", who, rot_dim, D);
+  if (!std::isfinite(eps) || eps < 0.f) return fail(TS_ERR_INVALID_ARG, "%s: bad eps", who);
+  if (D != 64 && D != 128) return fail(TS_ERR_UNSUPPORTED, "%s: D=%d (supported 64, 128)", who, D);
+  if (rot_dim % 8 != 0) return fail(TS_ERR_UNSUPPORTED, "%s: rot_dim=%d is not a multiple of 8", who, rot_dim);
+  const int64_t es = dtype == TS_F32 ? 4 : 2;
+  if (H_q > 4096 || H_kv > 4096) return fail(TS_ERR_UNSUPPORTED, "%s: more than 4096 heads", who);
+  const int64_t q_width = static_cast<int64_t>(H_q) * D, width = static_cast<int64_t>(H_kv) * D;
+  if (q_stride < q_width || q_out_stride < q_width || new_stride < width)
+    return fail(TS_ERR_INVALID_ARG, "%s: rows closer together than they are wide", who);
+  if (T == 0 || B == 0) return TS_OK;
+  if (!q || !k_new || !v_new || !k_pool || !v_pool || !block_table || !seq_lens || !q_indptr || !q_out ||
+      (rot_dim > 0 && !inv_freq))
+    return fail(TS_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (q_stride * es % 16 != 0 || q_out_stride * es % 16 != 0 || new_stride * es % 16 != 0)
+    return fail(TS_ERR_UNSUPPORTED, "%s: row steps must be multiples of 16 B", who);
+  for (const void* x : {q, k_new, v_new, q_weight, k_weight, static_cast<const void*>(k_pool),
+                        static_cast<const void*>(v_pool), static_cast<const void*>(q_out)})
+    if (reinterpret_cast<uintptr_t>(x) % 16 != 0)
+      return fail(TS_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", who);
+  if (reinterpret_cast<uintptr_t>(inv_freq) % 4 != 0)
+    return fail(TS_ERR_INVALID_ARG, "%s: inv_freq must be 4-byte aligned", who);
+  auto fill = [&](auto p) {
+    p.inv_freq = inv_freq;
+    p.block_table = block_table, p.seq_lens = seq_lens, p.q_indptr = q_indptr;
+    p.q_stride = q_stride, p.new_stride = new_stride, p.q_out_stride = q_out_stride;
+    p.bt_stride = bt_stride, p.T_rows = T, p.B = B, p.H_q = H_q, p.H_kv = H_kv, p.num_pages = num_pages;
+    p.rot = rot_dim, p.interleaved = interleaved != 0, p.eps = eps;
+    return launch(D, q, k_new, v_new, q_weight, k_weight, k_pool, v_pool, q_out, p,
+                  static_cast<cudaStream_t>(stream));
+  };
+  if (dtype == TS_BF16) return fill(RopeParams<__nv_bfloat16>{.page_size = PageSize(page_size)});
+  return fill(RopeParams<float>{.page_size = PageSize(page_size)});
+}

@@ -1,0 +1,191 @@
+// ts_kv_page_bounds: the bounds of each page's keys, kept beside the pages for
+// ts_select_pages.
+//
+// Of a page and kv head, over the page's tokens that the sequence holds:
+//   M[d] = max_t K[t, d],  m[d] = min_t K[t, d],  s = max(max |M|, max |m|, 1e-10) / 127,
+// kept as 8-bit codes ceil(M / s) and floor(m / s) and the float32 scale s.
+// Rounding outward keeps them bounds of the keys.
+//
+// A new token changes its own page alone, so a call takes the pages that hold a
+// row of the batch: row r is a page's first of the batch if it is its sequence's
+// first, or the first of the page. Pages are computed anew from their K rows, so
+// a call may be repeated, and a page given to another sequence needs no reset.
+#include "ts_ragged.cuh"
+
+namespace ts {
+namespace {
+
+constexpr int kWarps = 8;  // per CTA, one kv head each
+
+struct BoundsParams {
+  int8_t* bounds;
+  float* scale;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* q_indptr;
+  int32_t bt_stride, T, B, H_kv, num_pages, span;
+  PageSize page_size;
+};
+
+// 16 bytes of K as floats.
+template <typename T>
+__device__ __forceinline__ void widen(const uint4& w, float (&x)[16 / sizeof(T)]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      const float2 f = bf16x2_to_float2(u[i]);
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    } else {
+      x[i] = __uint_as_float(u[i]);
+    }
+  }
+}
+
+// Codes of n values, outward: ceil (up) or floor, within +-127; 0 where the page's scale is not finite.
+template <int N>
+__device__ __forceinline__ void store_codes(int8_t* to, const float (&x)[N], float scale, bool up) {
+  uint32_t w[N / 4];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float y = __fdiv_rn(x[i], scale);
+    const int c = scale < INFINITY ? static_cast<int>(fminf(fmaxf(up ? ceilf(y) : floorf(y), -127.f), 127.f)) : 0;
+    const uint32_t byte = static_cast<uint32_t>(c) & 0xffu;
+    w[i / 4] = i % 4 ? w[i / 4] | byte << (8 * (i % 4)) : byte;
+  }
+  if constexpr (N == 8)
+    *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(to) = w[0];
+}
+
+// A warp takes `span` rows of the batch and one kv head; a row of D values is
+// held by kLanes lanes of 16 bytes, kRows rows at a time.
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) page_bounds_kernel(const T* __restrict__ k_pool, const BoundsParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  constexpr int kLanes = D * static_cast<int>(sizeof(T)) / 16, kRows = 32 / kLanes, kEach = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
+  const int h = blockIdx.y * kWarps + (threadIdx.x >> 5);
+  if (h >= p.H_kv) return;
+  const int ps = p.page_size.rows;
+  // lane i looks at row i of the span: is it the first of its page in this batch?
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * p.span + lane;
+  int page = -1, count = 0;
+  if (lane < p.span && r < p.T) {
+    int lo = 0, hi = p.B;  // the last b with q_indptr[b] <= r
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.q_indptr[mid] <= r)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int r0 = p.q_indptr[lo], r1 = p.q_indptr[lo + 1];
+    if (r0 <= r && r < r1) {
+      const int L = p.seq_lens[lo], pos = L - (r1 - static_cast<int>(r));
+      const int slot = p.page_size.shift >= 0 ? pos >> p.page_size.shift : pos / ps;
+      const int at = pos - slot * ps;
+      if (pos >= 0 && (r == r0 || at == 0) && slot < p.bt_stride) {
+        page = p.block_table[static_cast<int64_t>(lo) * p.bt_stride + slot];
+        if (page >= p.num_pages) page = -1;
+        count = min(ps, L - slot * ps);
+      }
+    }
+  }
+  unsigned todo = __ballot_sync(0xffffffffu, page >= 0);
+  const int l = lane % kLanes, sub = lane / kLanes;
+  while (todo) {
+    const int from = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int64_t pg = __shfl_sync(0xffffffffu, page, from);
+    const int n = __shfl_sync(0xffffffffu, count, from);
+    const uint4* k = reinterpret_cast<const uint4*>(k_pool + (pg * ps * p.H_kv + h) * D) + l;
+    const int64_t step = static_cast<int64_t>(p.H_kv) * D * sizeof(T) / 16;
+    float top[kEach], low[kEach];
+    uint32_t largest = 0u;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) top[i] = -INFINITY, low[i] = INFINITY;
+    for (int t0 = sub; t0 < n; t0 += 4 * kRows) {
+      uint4 w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u] = k[min(t0 + u * kRows, n - 1) * step];  // (a row again changes nothing)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float x[kEach];
+        widen<T>(w[u], x);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          top[i] = fmaxf(top[i], x[i]);
+          low[i] = fminf(low[i], x[i]);
+          largest = max(largest, __float_as_uint(x[i]) & 0x7fffffffu);  // orders as magnitudes, NaN above all
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+#pragma unroll
+    for (int o = 16; o >= kLanes; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+        low[i] = fminf(low[i], __shfl_xor_sync(0xffffffffu, low[i], o));
+      }
+    const float scale = largest >= 0x7f800000u ? INFINITY : fmaxf(__uint_as_float(largest), 1e-10f) * (1.f / 127.f);
+    if (sub == 0) {
+      int8_t* to = p.bounds + (pg * p.H_kv + h) * 2 * D + l * kEach;
+      store_codes(to, top, scale, true);
+      store_codes(to + D, low, scale, false);
+      if (l == 0) p.scale[pg * p.H_kv + h] = scale;
+    }
+  }
+}
+
+template <typename T>
+ts_status launch(int D, const void* k_pool, const BoundsParams& p, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.T - 1) / p.span + 1), static_cast<unsigned>((p.H_kv - 1) / kWarps + 1));
+  cfg.blockDim = dim3(32 * (p.H_kv < kWarps ? p.H_kv : kWarps));
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto kern = D == 64 ? page_bounds_kernel<T, 64> : page_bounds_kernel<T, 128>;
+  LaunchTrace trace("page_bounds_kernel", stream);
+  return cuda_check(cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(k_pool), p), "ts_kv_page_bounds: launch");
+}
+
+}  // namespace
+}  // namespace ts
+
+extern "C" ts_status ts_kv_page_bounds(const void* k_pool, int8_t* bounds, float* bound_scale,
+                                       const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                       const int32_t* q_indptr, int32_t T, int32_t B, int32_t H_kv, int32_t D,
+                                       int32_t page_size, int32_t num_pages, ts_dtype dtype, void* stream) {
+  using namespace ts;
+  const char* who = "ts_kv_page_bounds";
+  if (T < 0 || B < 0 || H_kv <= 0 || D <= 0 || page_size <= 0 || num_pages <= 0 || bt_stride <= 0)
+    return fail(TS_ERR_INVALID_ARG, "%s: bad sizes (T=%d B=%d H_kv=%d D=%d ps=%d P=%d bt=%d)", who, T, B, H_kv, D,
+                page_size, num_pages, bt_stride);
+  if (dtype != TS_F32 && dtype != TS_BF16)
+    return fail(TS_ERR_INVALID_ARG, "%s: bad dtype %d", who, static_cast<int>(dtype));
+  if (D != 64 && D != 128) return fail(TS_ERR_UNSUPPORTED, "%s: D=%d (supported 64, 128)", who, D);
+  if (H_kv > 4096) return fail(TS_ERR_UNSUPPORTED, "%s: more than 4096 heads", who);
+  if (T == 0 || B == 0) return TS_OK;
+  if (!k_pool || !bounds || !bound_scale || !block_table || !seq_lens || !q_indptr)
+    return fail(TS_ERR_INVALID_ARG, "%s: null pointer", who);
+  for (const void* x : {k_pool, static_cast<const void*>(bounds)})
+    if (reinterpret_cast<uintptr_t>(x) % 16 != 0)
+      return fail(TS_ERR_INVALID_ARG, "%s: pool and bounds must be 16-byte aligned", who);
+  if (reinterpret_cast<uintptr_t>(bound_scale) % 4 != 0)
+    return fail(TS_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", who);
+  // Few rows: a warp each, so that the pages of a decode step are taken at once.
+  const int span = T <= 2048 ? 1 : 32;
+  const BoundsParams p{bounds, bound_scale, block_table, seq_lens, q_indptr, bt_stride, T,
+                       B,      H_kv,        num_pages,   span,     PageSize(page_size)};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return dtype == TS_BF16 ? launch<__nv_bfloat16>(D, k_pool, p, s) : launch<float>(D, k_pool, p, s);
+}

@@ -59,6 +59,17 @@ from .chunks import (
     kv_append_chunk_fp8,
     kv_read_fp8,
 )
+from .long_context import (
+    rotate,
+    kv_append_chunk_rope,
+    page_bounds,
+    update_page_bounds,
+    page_scores,
+    select_pages,
+    sparse_decode_attention,
+    kv_fork,
+    kv_compact,
+)
 
 __all__ = [
     "gather_sequence",
@@ -87,5 +98,14 @@ __all__ = [
     "kv_append_chunk",
     "kv_append_chunk_fp8",
     "kv_read_fp8",
+    "rotate",
+    "kv_append_chunk_rope",
+    "page_bounds",
+    "update_page_bounds",
+    "page_scores",
+    "select_pages",
+    "sparse_decode_attention",
+    "kv_fork",
+    "kv_compact",
     "PrefixGroups",
 ]

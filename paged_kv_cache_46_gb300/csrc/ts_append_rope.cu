@@ -20,8 +20,8 @@
 //
 // Angles: a float32 product of position and frequency is off by 2^-24 of the
 // angle, a hundredth of a turn at position 131,072. Turns are counted in 64-bit
-// fixed point instead: inv_freq / (2 pi) mod 1 as a 64-bit fraction (one product
-// in float64), times the position modulo 2^64, is the angle in turns. Its nearest
+// fixed point instead: inv_freq / (2 pi) mod 1 as a 64-bit fraction (a float64
+// product and its remainder), times the position modulo 2^64, is the angle in turns. Its nearest
 // quarter turn is taken off exactly and the rest, at most an eighth of a turn,
 // is rounded to float32 once: 2^-24 of pi / 4 at most.
 #include "ts_ragged.cuh"
@@ -82,16 +82,17 @@ struct Quad<float> {
 
 // Cosine and sine of pos * inv_freq (see the head of this file).
 __device__ __forceinline__ float2 turn(int pos, float inv_freq) {
-  double f = static_cast<double>(inv_freq) * 0.15915494309189533577;  // 1 / (2 pi)
-  f -= floor(f);
-  const unsigned long long step = static_cast<unsigned long long>(f * 18446744073709551616.0);
+  const double x = inv_freq, f = x * 0.15915494309189534;  // 1 / (2 pi), and what this product and constant leave
+  const double low = fma(x, 0.15915494309189534, -f) + x * -9.839338337591243e-18;
+  const unsigned long long step = static_cast<unsigned long long>((f - floor(f)) * 18446744073709551616.0) +
+                                  static_cast<unsigned long long>(static_cast<long long>(low * 18446744073709551616.0));
   const uint32_t t = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * step) >> 32);
   const uint32_t quarter = (t + 0x20000000u) >> 30;
   const int32_t rest = static_cast<int32_t>(t - (quarter << 30));  // within an eighth of a turn
   float s, c;
   sincospif(static_cast<float>(rest) * 4.656612873077392578125e-10f, &s, &c);  // 2^-31: in half turns
-  const float x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;
-  return make_float2((quarter + 1u) & 2u ? -x : x, quarter & 2u ? -y : y);
+  const float u = quarter & 1u ? s : c, v = quarter & 1u ? c : s;
+  return make_float2((quarter + 1u) & 2u ? -u : u, quarter & 2u ? -v : v);
 }
 
 template <typename T, int D>

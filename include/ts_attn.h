@@ -526,9 +526,10 @@ TS_API size_t ts_paged_decode_sparse_workspace_size(int32_t B, int32_t q_len, in
  * ts_paged_decode_multi_attn's operation where each query row and kv head has a
  * list of block-table slots of its own: token j of sequence b, at position p =
  * seq_lens[b] - q_len + j, attends the tokens t <= p whose slot t / page_size is
- * listed. Entries may come in any order; -1 (any negative) and slots behind p are
- * skipped; a slot that is listed twice counts twice. A row that sees no token
- * gets O = 0, LSE = -inf. With all slots listed it is
+ * listed. Of a list the first min(pages, n) entries are taken, n = p / page_size +
+ * 1 (distinct slots are no more), in any order; among them negative ones and
+ * slots behind p are skipped, and a slot that is listed twice counts twice. A row
+ * that sees no token gets O = 0, LSE = -inf. With all slots listed it is
  * ts_paged_decode_multi_attn's result.
  *
  *   q         device [B, q_len, H_q, D] of dtype

@@ -136,7 +136,7 @@ def sparse_decode_attention(q, k_pool, v_pool, block_table, seq_lens, page_idx, 
             pos = int(seq_lens[b]) - q_len + j
             for h in range(H_kv):
                 k, v = [], []
-                for slot in map(int, page_idx[b, j, h]):
+                for slot in map(int, page_idx[b, j, h][:max(0, pos // ps + 1)]):
                     if slot < 0 or slot * ps > pos or slot >= block_table.shape[1]:
                         continue
                     page = block_table[b, slot]

@@ -4,20 +4,37 @@
 // Of a query row at position p, over the tokens t <= p of the listed pages:
 //   s_t = scale * <q, K_t>,  O = sum_t softmax(s)_t V_t,  LSE = log sum_t exp(s_t).
 //
-// A work item is a query row and kv head; its list is cut into `parts` equal
-// ranges, one CTA each, so that few rows fill the device. The warps of a CTA take
-// the listed pages in turn, a page's rows kRows at a time: 16 bytes of a row per
-// lane, the g query heads in registers, a running maximum and sum per group of
-// lanes. States are joined over lanes, then warps, then (parts > 1) by a second
-// kernel from float32 states in the workspace.
-#include "ts_common.cuh"
+// A list entry read is page_size x D values of K and of V, and HBM bounds the
+// call: a row of one kv head is 128 to 512 bytes, its neighbours belong to the
+// other heads.
+//
+// Split: the entries of all items (a query row and kv head) in order are cut into
+// equal contiguous ranges, one per warp of a grid that fills the device; a row
+// counts min(pages, its pages) entries, found on the device, so that short
+// sequences cost what they hold. Warps are workers of their own: nothing in a
+// CTA is shared but the prefix sums of that plan. A range that ends inside an
+// item leaves a float32 state, at most two per warp, which sparse_merge_kernel
+// joins; an item within one range is written at once.
+//
+// bf16 (sparse_mma_kernel): tiles of 16 tokens, two (D = 64: four) per warp in
+// flight, brought by the TMA as boxes of one kv head's 8 or 16 rows and 64 columns,
+// with the 128-byte swizzle so that ldmatrix meets every bank once. The g query heads are the rows of an m16n8k16 product, padded to 16: a 128-row
+// tcgen05 tile would be 4 / 128 full, and these products take a tenth of the
+// time that their 8 KB take to arrive. The weights are rounded to bf16 for P V
+// (both operands share a type) and O is divided by the sum of the unrounded ones.
+// float32 (sparse_f32_kernel): on the CUDA cores, 16 bytes of a row per lane,
+// four rows of K and V in flight.
+#include "ts_tcgen05.cuh"
 
 #include <cmath>
 
 namespace ts {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kChunks = kThreads;  // row chunks of the plan, one per thread
+constexpr int kParts = 32;         // ranges that an item is cut into at most, and one more at its end
+constexpr int kMergeThreads = 512;
 constexpr float kLog2eS = 1.4426950408889634f;
 constexpr float kLn2S = 0.6931471805599453f;
 
@@ -30,272 +47,693 @@ struct SparseParams {
   const int32_t* page_idx;
   void* out;
   float* lse;
-  float* part_o;    // [parts, rows, H_q, D]
-  float* part_lse;  // [parts, rows, H_q], base 2
+  int64_t* plan;    // [kChunks + 1] entries in front of each chunk of rows, kept for the merge
+  float* part_o;    // [2 * warps, g, D]
+  float* part_lse;  // [2 * warps, g], base 2
   uint32_t* err_word;
-  int32_t bt_stride, rows, q_len, H_kv, page_size, num_pages, pages, parts;
+  int32_t bt_stride, rows, q_len, H_kv, page_size, num_pages, pages, warps;
   float scale_log2;
 };
 
-template <typename T>
-__device__ __forceinline__ void widen(const uint4& w, float (&x)[16 / sizeof(T)]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// Position of a query row, and the entries of its lists that are taken.
+__device__ __forceinline__ int row_position(const SparseParams& p, int row) {
+  const int b = row / p.q_len;
+  return p.seq_lens[b] - p.q_len + (row - b * p.q_len);
+}
+__device__ __forceinline__ int row_entries(const SparseParams& p, int row) {
+  const int pos = row_position(p, row);
+  return pos < 0 ? 0 : min(p.pages, pos / p.page_size + 1);
+}
+__device__ __forceinline__ int chunk_rows(const SparseParams& p) { return (p.rows + kChunks - 1) / kChunks; }
+
+// Entries in front of each chunk of rows (the whole CTA calls it), for one kv head.
+__device__ __forceinline__ void make_plan(const SparseParams& p, int64_t (&before)[kChunks + 1]) {
+  __shared__ int64_t warp_sum[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, each = chunk_rows(p);
+  int64_t sum = 0;
+  for (int r = tid * each; r < min(p.rows, (tid + 1) * each); ++r) sum += row_entries(p, r);
+  int64_t incl = sum;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 2) {
-      const float2 f = bf16x2_to_float2(u[i]);
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    } else {
-      x[i] = __uint_as_float(u[i]);
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
   }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) incl += warp_sum[w];
+  before[tid + 1] = incl;
+  if (tid == 0) before[0] = 0;
+  __syncthreads();
 }
 
-template <typename T>
-__device__ __forceinline__ void store4(T* to, float4 v) {
-  if constexpr (sizeof(T) == 2)
-    *reinterpret_cast<uint2*>(to) = make_uint2(float2_to_bf16x2(v.x, v.y), float2_to_bf16x2(v.z, v.w));
-  else
-    *reinterpret_cast<float4*>(to) = v;
+// Entries of a warp's range, of `total` in all.
+__device__ __forceinline__ int64_t range_entries(const SparseParams& p, int64_t total) {
+  return max((total + p.warps - 1) / p.warps, static_cast<int64_t>((p.pages + kParts - 1) / kParts));
 }
+
+// Walks the items of entries [at, end): row, head and the part [i0, i1) of its list.
+struct Walk {
+  int64_t at, end, item0;  // item0: first entry of the item
+  int32_t row, h, count, i0, i1, pos;
+
+  // Finds the item of entry `at` (warp-wide).
+  __device__ __forceinline__ bool start(const SparseParams& p, const int64_t (&before)[kChunks + 1], int64_t from,
+                                        int64_t to, int lane) {
+    const int64_t total = before[kChunks] * p.H_kv;
+    at = from;
+    end = min(to, total);
+    if (at >= end) return false;
+    int chunk = 0;  // the last one with before * H_kv <= at
+#pragma unroll
+    for (int c0 = 0; c0 < kChunks; c0 += 32)
+      chunk += __popc(__ballot_sync(0xffffffffu, before[c0 + lane + 1] * p.H_kv <= at));
+    const int each = chunk_rows(p);
+    int64_t sum = before[chunk] * p.H_kv;
+    for (int r0 = chunk * each;; r0 += 32) {
+      const int r = r0 + lane;
+      const int n = r < p.rows ? row_entries(p, r) : 0;
+      int64_t incl = static_cast<int64_t>(n) * p.H_kv;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, sum + incl > at);
+      if (hit) {
+        const int from_lane = __ffs(hit) - 1;
+        row = r0 + from_lane;
+        count = __shfl_sync(0xffffffffu, n, from_lane);
+        sum += __shfl_sync(0xffffffffu, incl, from_lane) - static_cast<int64_t>(count) * p.H_kv;
+        break;
+      }
+      sum += __shfl_sync(0xffffffffu, incl, 31);
+      if (r0 + 32 >= p.rows) return false;  // (lengths changed under the call)
+    }
+    h = static_cast<int>((at - sum) / count);
+    item0 = sum + static_cast<int64_t>(h) * count;
+    settle(p);
+    return true;
+  }
+  __device__ __forceinline__ void settle(const SparseParams& p) {
+    pos = row_position(p, row);
+    i0 = static_cast<int>(at - item0);
+    i1 = static_cast<int>(min(static_cast<int64_t>(count), end - item0));
+  }
+  __device__ __forceinline__ bool next(const SparseParams& p) {
+    at = item0 + i1;
+    if (at >= end) return false;
+    item0 += count;
+    if (++h == p.H_kv) {
+      h = 0;
+      do {
+        if (++row >= p.rows) return false;
+        count = row_entries(p, row);
+      } while (count == 0);
+    }
+    settle(p);
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == count; }
+};
 
 // A listed page: its pool page and how many of its tokens the row sees (0: none).
 struct Listed {
   int32_t page, tokens;
 };
-__device__ __forceinline__ Listed listed_page(const SparseParams& p, int idx, int b, int pos) {
+__device__ __forceinline__ Listed listed_page(const SparseParams& p, const Walk& w, int i) {
   Listed e{0, 0};
-  if (idx < 0 || static_cast<int64_t>(idx) * p.page_size > pos) return e;
-  const int page = idx < p.bt_stride ? p.block_table[static_cast<int64_t>(b) * p.bt_stride + idx] : -1;
+  if (i >= w.i1) return e;
+  const int idx = p.page_idx[(static_cast<int64_t>(w.row) * p.H_kv + w.h) * p.pages + i];
+  if (idx < 0 || static_cast<int64_t>(idx) * p.page_size > w.pos) return e;
+  const int page =
+      idx < p.bt_stride ? p.block_table[static_cast<int64_t>(w.row / p.q_len) * p.bt_stride + idx] : -1;
   if (page < 0 || page >= p.num_pages) {
     set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
     return e;
   }
   e.page = page;
-  e.tokens = min(p.page_size, pos - idx * p.page_size + 1);
+  e.tokens = min(p.page_size, w.pos - idx * p.page_size + 1);
   return e;
 }
 
-template <typename T, int D, int G>
-__global__ void __launch_bounds__(kWarps * 32) sparse_decode_kernel(const SparseParams p) {
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  constexpr int kEach = 16 / static_cast<int>(sizeof(T)), kLanes = D / kEach, kRows = 32 / kLanes, kAhead = 4;
-  __shared__ float sh_m[kWarps][G], sh_l[kWarps][G];
-  __shared__ __align__(16) float sh_o[kWarps][G][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % kLanes, sub = lane / kLanes;
-  const int64_t item = blockIdx.x / static_cast<unsigned>(p.parts);
-  const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.parts));
-  const int row = static_cast<int>(item / p.H_kv), h = static_cast<int>(item % p.H_kv);
-  const int b = row / p.q_len, pos = p.seq_lens[b] - p.q_len + (row - b * p.q_len);
-  const int H_q = p.H_kv * G;
+template <typename T>
+__device__ __forceinline__ void store2(T* to, float x, float y) {
+  if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<uint32_t*>(to) = float2_to_bf16x2(x, y);
+  else
+    *reinterpret_cast<float2*>(to) = make_float2(x, y);
+}
 
-  float q[G][kEach], acc[G][kEach], m[G], sum[G];
-  const T* qsrc = static_cast<const T*>(p.q) + (static_cast<int64_t>(row) * H_q + h * G) * D + l * kEach;
-#pragma unroll
-  for (int i = 0; i < G; ++i) {
-    widen<T>(*reinterpret_cast<const uint4*>(qsrc + i * D), q[i]);
-    m[i] = -INFINITY;
-    sum[i] = 0.f;
-#pragma unroll
-    for (int d = 0; d < kEach; ++d) acc[i][d] = 0.f, q[i][d] *= p.scale_log2;
+// Where a segment's state of query head i goes: its result, or one of the warp's
+// two places in the workspace (0 where the item began before the range).
+template <typename T, int D>
+struct Target {
+  T* out;
+  float* lse;
+  float* part_o;
+  float* part_lse;
+  __device__ __forceinline__ Target(const SparseParams& p, const Walk& w, int64_t warp, int g, int i) {
+    out = nullptr, lse = nullptr, part_o = nullptr, part_lse = nullptr;
+    if (w.whole()) {
+      const int64_t at = static_cast<int64_t>(w.row) * p.H_kv * g + w.h * g + i;
+      out = static_cast<T*>(p.out) + at * D;
+      if (p.lse != nullptr) lse = p.lse + at;
+    } else {
+      const int64_t at = (2 * warp + (w.i0 == 0)) * g + i;
+      part_o = p.part_o + at * D;
+      part_lse = p.part_lse + at;
+    }
   }
-  const int32_t* list = p.page_idx + item * p.pages;
-  const int i0 = static_cast<int>(static_cast<int64_t>(p.pages) * part / p.parts);
-  const int i1 = static_cast<int>(static_cast<int64_t>(p.pages) * (part + 1) / p.parts);
-  const int64_t step = static_cast<int64_t>(p.H_kv) * D;  // elements between rows
-  for (int c0 = i0 + warp; c0 < i1; c0 += 32 * kWarps) {
-    // lane i looks up the i-th of this warp's next 32 entries
-    const int mine = c0 + lane * kWarps;
-    const Listed e = mine < i1 ? listed_page(p, list[mine], b, pos) : Listed{0, 0};
-    for (unsigned todo = __ballot_sync(0xffffffffu, e.tokens > 0); todo; todo &= todo - 1) {
-      const int from = __ffs(todo) - 1;
-      const int64_t page = __shfl_sync(0xffffffffu, e.page, from);
-      const int n = __shfl_sync(0xffffffffu, e.tokens, from);
-      const int64_t base = (page * p.page_size * p.H_kv + h) * D + l * kEach;
-      const T* kp = static_cast<const T*>(p.k_pool) + base;
-      const T* vp = static_cast<const T*>(p.v_pool) + base;
-      for (int t0 = sub; t0 - sub < n; t0 += kAhead * kRows) {
-        uint4 kw[kAhead], vw[kAhead];
+  __device__ __forceinline__ void put(int d, float x, float y) const {
+    if (out != nullptr)
+      store2(out + d, x, y);
+    else
+      store2(part_o + d, x, y);
+  }
+  __device__ __forceinline__ void put_lse(float lse2) const {
+    if (part_lse != nullptr)
+      *part_lse = lse2;
+    else if (lse != nullptr)
+      *lse = lse2 * kLn2S;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// bf16
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// (x, y) += the first eight rows of A (16 x 16, its last eight rows zero) x B (16 x 8).
+__device__ __forceinline__ void mma_rows8(float& x, float& y, uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+  [[maybe_unused]] float u, v;  // rows 8 .. 15
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %5}, {%7, %8}, "
+      "{%0, %1, %9, %9};"
+      : "+f"(x), "+f"(y), "=f"(u), "=f"(v)
+      : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// A stage: 16 rows of K, then of V, in boxes of 64 columns (rows of 128 bytes, 128-byte swizzle).
+template <int D>
+struct MmaSmem {
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kOperand = 16 * D * 2, kStage = 2 * kOperand;
+  static constexpr int kBytes = kWarps * kStages * kStage;
+};
+
+// The bits of the first n of eight rows.
+__device__ __forceinline__ unsigned first_rows(int n) { return n >= 8 ? 0xffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
+    const __grid_constant__ SparseParams p, const __grid_constant__ CUtensorMap kmap,
+    const __grid_constant__ CUtensorMap vmap) {
+  pdl_launch_dependents();
+  using S = MmaSmem<D>;
+  constexpr int kStages = S::kStages;
+  extern __shared__ __align__(1024) unsigned char ring[];
+  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+  __shared__ int64_t before[kChunks + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t worker = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  if ((smem_u32(ring) & 1023u) != 0u) {
+    if (threadIdx.x == 0) set_device_error(p.err_word, TS_DEVERR_SMEM_ALIGN);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(&bars[0][0] + i), 1);
+    fence_mbar_init();
+  }
+  make_plan(p, before);
+  const int64_t range = range_entries(p, before[kChunks] * p.H_kv);
+  Walk w;
+  const bool any = w.start(p, before, worker * range, (worker + 1) * range, lane);
+  pdl_wait_primary();  // so far the lengths alone were read
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= kChunks; i += kThreads) p.plan[i] = before[i];
+  if (!any) return;
+
+  const uint32_t stage0 = smem_u32(ring) + warp * kStages * S::kStage;
+  const uint32_t bar0 = smem_u32(&bars[warp][0]);
+  const int quarter = lane & 3, head = lane >> 2;
+  const int groups = p.page_size >> 3;  // of eight rows, in a page: 1, 2 or 4
+  const int gshift = groups >> 1;       // its logarithm
+  // ldmatrix rows and 16-byte chunks of a lane: keys 0 .. 7 and 8 .. 15, columns 0 .. 7 and 8 .. 15 of a step
+  const int krow = (lane & 7) + ((lane >> 4) << 3), vrow = (lane & 7) + (lane & 8);
+  const uint32_t kat = krow * 128 + ((((lane >> 3) & 1) ^ (krow & 7)) << 4);
+  const uint32_t vat = vrow * 128 + (((lane >> 4) ^ (vrow & 7)) << 4);
+  uint32_t stage = 0, parity = 0;       // of the next tile to be waited for
+  bool ok = true;
+
+  do {
+    // the item's queries, as rows of A
+    uint32_t qa[D / 16][2];
+    {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                 (static_cast<int64_t>(w.row) * p.H_kv * G + w.h * G + head) * D + 2 * quarter;
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int64_t at = min(t0 + u * kRows, n - 1) * step;
-          kw[u] = *reinterpret_cast<const uint4*>(kp + at);
-          vw[u] = *reinterpret_cast<const uint4*>(vp + at);
-        }
-        float s[kAhead][G];
+      for (int k = 0; k < D / 16; ++k) {
+        qa[k][0] = head < G ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
+        qa[k][1] = head < G ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
+      }
+    }
+    float m = -INFINITY, sum = 0.f;
+    float o[D / 8][2];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          float x[kEach];
-          widen<T>(kw[u], x);
+    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = 0.f;
+
+    for (int c0 = w.i0; c0 < w.i1 && ok; c0 += 32) {
+      const Listed e = listed_page(p, w, c0 + lane);
+      const int entries = min(32, w.i1 - c0);
+      const int tiles = (entries * groups + 1) >> 1;
+      // pool row and seen rows of the eight-row group i of these entries
+      auto group = [&](int i, int& row, unsigned& rows) {
+        const int from = i >> gshift, at = (i & (groups - 1)) * 8;
+        const int page = __shfl_sync(0xffffffffu, e.page, from & 31), n = __shfl_sync(0xffffffffu, e.tokens, from & 31);
+        row = page * p.page_size + at;
+        rows = from < 32 ? first_rows(n - at) : 0u;
+      };
+      auto issue = [&](int t, uint32_t st) {
+        int row0, row1;
+        unsigned rows0, rows1;
+        group(2 * t, row0, rows0);
+        group(2 * t + 1, row1, rows1);
+        if (lane == 0) {
+          const uint32_t bar = bar0 + 8 * st, to = stage0 + st * S::kStage;
+          if (groups > 1) {  // the tile is a part of one page
+            mbar_arrive_expect_tx(bar, rows0 ? S::kStage : 0);
+            if (rows0) {
 #pragma unroll
-          for (int i = 0; i < G; ++i) {
-            float d = q[i][0] * x[0];
+              for (int x = 0; x < D / 64; ++x) {
+                tma_load_3d(to + x * 2048, &kmap, 64 * x, w.h, row0, bar);
+                tma_load_3d(to + S::kOperand + x * 2048, &vmap, 64 * x, w.h, row0, bar);
+              }
+            }
+          } else {  // of two
+            mbar_arrive_expect_tx(bar, (rows0 ? S::kStage / 2 : 0) + (rows1 ? S::kStage / 2 : 0));
 #pragma unroll
-            for (int j = 1; j < kEach; ++j) d = fmaf(q[i][j], x[j], d);
-            s[u][i] = d;
+            for (int x = 0; x < D / 64; ++x) {
+              if (rows0) {
+                tma_load_3d(to + x * 2048, &kmap, 64 * x, w.h, row0, bar);
+                tma_load_3d(to + S::kOperand + x * 2048, &vmap, 64 * x, w.h, row0, bar);
+              }
+              if (rows1) {
+                tma_load_3d(to + x * 2048 + 1024, &kmap, 64 * x, w.h, row1, bar);
+                tma_load_3d(to + S::kOperand + x * 2048 + 1024, &vmap, 64 * x, w.h, row1, bar);
+              }
+            }
           }
+        }
+        __syncwarp();
+      };
+      uint32_t put = stage;
+      for (int t = 0; t < kStages && t < tiles; ++t) {
+        issue(t, put);
+        put = put + 1 == kStages ? 0 : put + 1;
+      }
+      for (int t = 0; t < tiles; ++t) {
+        int row0, row1;
+        unsigned rows, rows1;
+        group(2 * t, row0, rows);
+        group(2 * t + 1, row1, rows1);
+        rows |= rows1 << 8;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8 * stage, parity));
+        if (!ok) {  // leave, but not with copies in flight
+          for (int i = t; i < tiles && i < t + kStages; ++i) {
+            mbar_wait(bar0 + 8 * stage, parity);
+            if (++stage == kStages) stage = 0, parity ^= 1u;
+          }
+          break;
+        }
+        if (rows != 0u) {
+          const uint32_t ks = stage0 + stage * S::kStage, vs = ks + S::kOperand;
+          if (rows != 0xffffu) {  // values of rows that are not seen must not count, not even NaN
+            if (!(rows >> (lane & 15) & 1u)) {
+              for (int i = lane >> 4; i < D / 8; i += 2)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vs + (i >> 3) * 2048 + (lane & 15) * 128 +
+                                                                             (i & 7) * 16),
+                             "r"(0u)
+                             : "memory");
+            }
+            fence_async_smem();
+            __syncwarp();
+          }
+          // scores: lane holds keys 2 quarter + {0, 1} and 8 more of query head `head`
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1)
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t b[4];
+            ldmatrix4(b, ks + (k >> 2) * 2048 + (kat ^ ((k & 3) << 5)));
+            mma_rows8(s[0], s[1], qa[k][0], qa[k][1], b[0], b[1]);
+            mma_rows8(s[2], s[3], qa[k][0], qa[k][1], b[2], b[3]);
+          }
+          const unsigned seen = rows >> (2 * quarter);
+          s[0] = seen & 1u ? s[0] * p.scale_log2 : -INFINITY;
+          s[1] = seen & 2u ? s[1] * p.scale_log2 : -INFINITY;
+          s[2] = seen & 0x100u ? s[2] * p.scale_log2 : -INFINITY;
+          s[3] = seen & 0x200u ? s[3] * p.scale_log2 : -INFINITY;
+          float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          top = fmaxf(top, m);
+          if (__any_sync(0xffffffffu, top > m)) {
+            const float scale = fast_exp2(m - (top == -INFINITY ? 0.f : top));
+            m = top;
+            sum *= scale;
 #pragma unroll
-            for (int i = 0; i < G; ++i) s[u][i] += __shfl_xor_sync(0xffffffffu, s[u][i], o);
-          if (t0 + u * kRows >= n) {
+            for (int j = 0; j < D / 8; ++j) o[j][0] *= scale, o[j][1] *= scale;
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int i = 0; i < G; ++i) s[u][i] = -INFINITY;
+          for (int i = 0; i < 4; ++i) {
+            s[i] = fast_exp2(s[i] - ref);
+            sum += s[i];
+          }
+          const uint32_t p0 = float2_to_bf16x2(s[0], s[1]), p1 = float2_to_bf16x2(s[2], s[3]);
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            uint32_t b[4];
+            ldmatrix4_trans(b, vs + (j >> 2) * 2048 + (vat ^ ((j & 3) << 5)));
+            mma_rows8(o[2 * j][0], o[2 * j][1], p0, p1, b[0], b[1]);
+            mma_rows8(o[2 * j + 1][0], o[2 * j + 1][1], p0, p1, b[2], b[3]);
           }
         }
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-          float top = m[i];
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u) top = fmaxf(top, s[u][i]);
-          const float ref = top == -INFINITY ? 0.f : top;
-          const float scale = fast_exp2(m[i] - ref);
-          m[i] = top;
-          sum[i] *= scale;
-#pragma unroll
-          for (int j = 0; j < kEach; ++j) acc[i][j] *= scale;
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u) {
-            s[u][i] = fast_exp2(s[u][i] - ref);
-            sum[i] += s[u][i];
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          if (t0 + u * kRows >= n) continue;  // (what such rows hold must not count, not even NaN)
-          float x[kEach];
-          widen<T>(vw[u], x);
-#pragma unroll
-          for (int i = 0; i < G; ++i)
-#pragma unroll
-            for (int j = 0; j < kEach; ++j) acc[i][j] = fmaf(s[u][i], x[j], acc[i][j]);
+        __syncwarp();
+        if (t + kStages < tiles) issue(t + kStages, stage);
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1u;
         }
       }
     }
-  }
-  // joined over the groups of lanes
+    if (!ok) break;
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if (head < G) {
+      const Target<__nv_bfloat16, D> to(p, w, worker, G, head);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays NaN)
 #pragma unroll
-  for (int o = 16; o >= kLanes; o >>= 1) {
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, m[i], o), top = fmaxf(m[i], m2);
-      const float ref = top == -INFINITY ? 0.f : top;
-      const float a = fast_exp2(m[i] - ref), c = fast_exp2(m2 - ref);
-      m[i] = top;
-      sum[i] = a * sum[i] + c * __shfl_xor_sync(0xffffffffu, sum[i], o);
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) acc[i][j] = a * acc[i][j] + c * __shfl_xor_sync(0xffffffffu, acc[i][j], o);
+      for (int j = 0; j < D / 8; ++j) to.put(8 * j + 2 * quarter, o[j][0] * inv, o[j][1] * inv);
+      if (quarter == 0) to.put_lse(sum == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + log2f(sum));
     }
-  }
-  if (sub == 0) {
+  } while (w.next(p));
+  if (!ok && lane == 0) set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
+}
+
+// ---------------------------------------------------------------------------
+// float32
+// ---------------------------------------------------------------------------
+
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads) sparse_f32_kernel(const SparseParams p) {
+  pdl_launch_dependents();
+  constexpr int kEach = 4, kLanes = D / kEach, kRows = 32 / kLanes, kAhead = 4;
+  __shared__ int64_t before[kChunks + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % kLanes, sub = lane / kLanes;
+  const int64_t worker = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  make_plan(p, before);
+  const int64_t range = range_entries(p, before[kChunks] * p.H_kv);
+  Walk w;
+  const bool any = w.start(p, before, worker * range, (worker + 1) * range, lane);
+  pdl_wait_primary();  // so far the lengths alone were read
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= kChunks; i += kThreads) p.plan[i] = before[i];
+  if (!any) return;
+  const int64_t step = static_cast<int64_t>(p.H_kv) * D;  // elements between rows
+  do {
+    float q[G][kEach], acc[G][kEach], m[G], sum[G];
+    const float* qsrc =
+        static_cast<const float*>(p.q) + (static_cast<int64_t>(w.row) * p.H_kv * G + w.h * G) * D + l * kEach;
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-      if (l == 0) sh_m[warp][i] = m[i], sh_l[warp][i] = sum[i];
+      const float4 x = *reinterpret_cast<const float4*>(qsrc + i * D);
+      q[i][0] = x.x * p.scale_log2, q[i][1] = x.y * p.scale_log2;
+      q[i][2] = x.z * p.scale_log2, q[i][3] = x.w * p.scale_log2;
+      m[i] = -INFINITY;
+      sum[i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) sh_o[warp][i][l * kEach + j] = acc[i][j];
+      for (int d = 0; d < kEach; ++d) acc[i][d] = 0.f;
+    }
+    for (int c0 = w.i0; c0 < w.i1; c0 += 32) {
+      const Listed e = listed_page(p, w, c0 + lane);
+      for (unsigned todo = __ballot_sync(0xffffffffu, e.tokens > 0); todo; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1;
+        const int64_t page = __shfl_sync(0xffffffffu, e.page, from);
+        const int n = __shfl_sync(0xffffffffu, e.tokens, from);
+        const int64_t base = (page * p.page_size * p.H_kv + w.h) * D + l * kEach;
+        const float* kp = static_cast<const float*>(p.k_pool) + base;
+        const float* vp = static_cast<const float*>(p.v_pool) + base;
+        for (int t0 = sub; t0 - sub < n; t0 += kAhead * kRows) {
+          float4 k[kAhead], v[kAhead];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const int64_t at = min(t0 + u * kRows, n - 1) * step;
+            k[u] = *reinterpret_cast<const float4*>(kp + at);
+            v[u] = *reinterpret_cast<const float4*>(vp + at);
+          }
+          float s[kAhead][G];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+              s[u][i] = fmaf(q[i][3], k[u].w, fmaf(q[i][2], k[u].z, fmaf(q[i][1], k[u].y, q[i][0] * k[u].x)));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+              for (int i = 0; i < G; ++i) s[u][i] += __shfl_xor_sync(0xffffffffu, s[u][i], o);
+            if (t0 + u * kRows >= n) {
+#pragma unroll
+              for (int i = 0; i < G; ++i) s[u][i] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < G; ++i) {
+            float top = m[i];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) top = fmaxf(top, s[u][i]);
+            const float ref = top == -INFINITY ? 0.f : top;
+            const float scale = fast_exp2(m[i] - ref);
+            m[i] = top;
+            sum[i] *= scale;
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) acc[i][j] *= scale;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+              s[u][i] = fast_exp2(s[u][i] - ref);
+              sum[i] += s[u][i];
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            if (t0 + u * kRows >= n) continue;  // (what such rows hold must not count, not even NaN)
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+              acc[i][0] = fmaf(s[u][i], v[u].x, acc[i][0]);
+              acc[i][1] = fmaf(s[u][i], v[u].y, acc[i][1]);
+              acc[i][2] = fmaf(s[u][i], v[u].z, acc[i][2]);
+              acc[i][3] = fmaf(s[u][i], v[u].w, acc[i][3]);
+            }
+          }
+        }
+      }
+    }
+    // joined over the groups of lanes
+#pragma unroll
+    for (int o = 16; o >= kLanes; o >>= 1) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m[i], o), top = fmaxf(m[i], m2);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float a = fast_exp2(m[i] - ref), c = fast_exp2(m2 - ref);
+        m[i] = top;
+        sum[i] = a * sum[i] + c * __shfl_xor_sync(0xffffffffu, sum[i], o);
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) acc[i][j] = a * acc[i][j] + c * __shfl_xor_sync(0xffffffffu, acc[i][j], o);
+      }
+    }
+    if (sub == 0) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const Target<float, D> to(p, w, worker, G, i);
+        const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];  // (NaN stays NaN)
+        to.put(l * kEach, acc[i][0] * inv, acc[i][1] * inv);
+        to.put(l * kEach + 2, acc[i][2] * inv, acc[i][3] * inv);
+        if (l == 0) to.put_lse(sum[i] == 0.f ? -INFINITY : (m[i] == -INFINITY ? 0.f : m[i]) + log2f(sum[i]));
+      }
+    }
+  } while (w.next(p));
+}
+
+// ---------------------------------------------------------------------------
+
+// Joins the states of items that were cut, and writes the rows that see nothing. A
+// CTA per query row and kv head; g D / 4 threads hold four columns each, as often
+// as they fit, and share the states.
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kMergeThreads) sparse_merge_kernel(const SparseParams p) {
+  constexpr int kCols = G * D / 4, kShares = kMergeThreads / kCols;
+  __shared__ int32_t warp_sum[kMergeThreads / 32];
+  __shared__ float weight[kParts + 2][G];
+  __shared__ float4 part[kShares][kCols];
+  __shared__ float sh_total[G], sh_top[G];
+  pdl_launch_dependents();
+  const int row = blockIdx.x / p.H_kv, h = blockIdx.x % p.H_kv, tid = threadIdx.x;
+  const int count = row_entries(p, row), each = chunk_rows(p), chunk = row / each;
+  // entries in front of the row, in its chunk
+  int64_t in_front = 0;
+  if (row > chunk * each) {
+    int mine = 0;
+    for (int r = chunk * each + tid; r < row; r += kMergeThreads) mine += row_entries(p, r);
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if ((tid & 31) == 0) warp_sum[tid >> 5] = mine;
+    __syncthreads();
+    for (int w = 0; w < kMergeThreads / 32; ++w) in_front += warp_sum[w];
+  }
+  pdl_wait_primary();  // so far the lengths alone were read
+  in_front += p.plan[chunk];
+  const int64_t range = range_entries(p, p.plan[kChunks] * p.H_kv);
+  const int64_t first = in_front * p.H_kv + static_cast<int64_t>(h) * count;
+  const int64_t w0 = first / range, w1 = (first + count - 1) / range;
+  if (count > 0 && w0 == w1) return;  // written already
+  const int n = count > 0 ? static_cast<int>(w1 - w0) + 1 : 0;  // at most kParts + 1
+  if (tid < 32) {
+    for (int i = 0; i < G; ++i) {
+      const float a = tid < n ? p.part_lse[(2 * (w0 + tid) + (tid == 0)) * G + i] : -INFINITY;
+      const float c = tid + 32 < n ? p.part_lse[2 * (w0 + tid + 32) * G + i] : -INFINITY;
+      float top = fmaxf(a, c);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float ref = top == -INFINITY ? 0.f : top, wa = fast_exp2(a - ref), wc = fast_exp2(c - ref);
+      float total = wa + wc;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      weight[tid][i] = wa;
+      if (tid + 32 < kParts + 2) weight[tid + 32][i] = wc;
+      if (tid == 0) sh_total[i] = total, sh_top[i] = ref;
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < G * D / 4; e += kWarps * 32) {
-    const int i = e / (D / 4), d = e % (D / 4) * 4;
-    float top = sh_m[0][i];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sh_m[w][i]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float total = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float a = fast_exp2(sh_m[w][i] - ref);
-      const float4 x = *reinterpret_cast<const float4*>(&sh_o[w][i][d]);
-      total = fmaf(a, sh_l[w][i], total);
-      o = make_float4(fmaf(a, x.x, o.x), fmaf(a, x.y, o.y), fmaf(a, x.z, o.z), fmaf(a, x.w, o.w));
-    }
-    const float inv = total == 0.f ? 0.f : 1.f / total;  // (NaN stays NaN)
-    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    const float lse2 = total == 0.f ? -INFINITY : ref + log2f(total);
-    const int64_t at = static_cast<int64_t>(row) * H_q + h * G + i;
-    if (p.parts == 1) {
-      store4(static_cast<T*>(p.out) + at * D + d, o);
-      if (d == 0 && p.lse != nullptr) p.lse[at] = lse2 * kLn2S;
-    } else {
-      const int64_t to = static_cast<int64_t>(part) * p.rows * H_q + at;
-      *reinterpret_cast<float4*>(p.part_o + to * D + d) = o;
-      if (d == 0) p.part_lse[to] = lse2;
-    }
-  }
-}
-
-// Joins the parts of a query head: D / 4 threads each.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) sparse_merge_kernel(const SparseParams p, int32_t heads) {
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-  const int64_t at = e / (D / 4), total_heads = static_cast<int64_t>(p.rows) * heads;
-  const int d = static_cast<int>(e % (D / 4)) * 4;
-  if (at >= total_heads) return;
-  float top = -INFINITY;
-  for (int i = 0; i < p.parts; ++i) top = fmaxf(top, p.part_lse[i * total_heads + at]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float total = 0.f;
+  const int share = tid / kCols, e = tid % kCols, i = e / (D / 4), d = e % (D / 4) * 4;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < p.parts; ++i) {
-    const float a = fast_exp2(p.part_lse[i * total_heads + at] - ref);
-    const float4 x = *reinterpret_cast<const float4*>(p.part_o + (i * total_heads + at) * D + d);
-    total += a;
+#pragma unroll 4
+  for (int k = share; k < n; k += kShares) {
+    const float a = weight[k][i];
+    const float4 x = *reinterpret_cast<const float4*>(p.part_o + ((2 * (w0 + k) + (k == 0)) * G + i) * D + d);
     o = make_float4(fmaf(a, x.x, o.x), fmaf(a, x.y, o.y), fmaf(a, x.z, o.z), fmaf(a, x.w, o.w));
   }
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-  store4(static_cast<T*>(p.out) + at * D + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-  if (d == 0 && p.lse != nullptr) p.lse[at] = total == 0.f ? -INFINITY : (ref + log2f(total)) * kLn2S;
+  part[share][e] = o;
+  __syncthreads();
+  if (share != 0) return;
+#pragma unroll
+  for (int k = 1; k < kShares; ++k) {
+    const float4 x = part[k][e];
+    o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+  }
+  const float total = sh_total[i], inv = total == 0.f ? 0.f : 1.f / total;  // (NaN stays NaN)
+  const int64_t at = (static_cast<int64_t>(row) * p.H_kv + h) * G + i;
+  T* out = static_cast<T*>(p.out) + at * D + d;
+  store2(out, o.x * inv, o.y * inv);
+  store2(out + 2, o.z * inv, o.w * inv);
+  if (d == 0 && p.lse != nullptr) p.lse[at] = total == 0.f ? -INFINITY : (sh_top[i] + log2f(total)) * kLn2S;
 }
 
-// Parts of each list: so many CTAs that the device is filled, each with a page
-// per warp at least.
-int sparse_parts(int64_t items, int pages) {
-  const int64_t want = (static_cast<int64_t>(paged_decode_ctas()) * 4 + items - 1) / (items > 0 ? items : 1);
-  const int64_t most = (pages + kWarps - 1) / kWarps;
-  return static_cast<int>(want < 1 ? 1 : want > most ? most : want);
+// Warps of the grid: two CTAs on each SM, or as many as lists of full length keep busy.
+int sparse_warps(int64_t items, int pages) {
+  const int64_t least = (pages + kParts - 1) / kParts, most = (items * pages + least - 1) / least, full = static_cast<int64_t>(paged_decode_ctas()) * 2 * kWarps;
+  const int64_t n = most < full ? most : full;
+  return static_cast<int>((n < 1 ? 1 : n) + kWarps - 1) / kWarps * kWarps;
 }
 
-size_t sparse_bytes(int64_t rows, int H_q, int D, int parts) {
-  const size_t states = parts > 1 ? static_cast<size_t>(parts) * rows * H_q * (D + 1) * sizeof(float) : 0;
-  return align_up(kWorkspaceAlign + states, kWorkspaceAlign);
-}
+struct SparseWs {
+  size_t plan, part_o, part_lse, total;
+  SparseWs(int warps, int g, int D) {
+    plan = kWorkspaceAlign;
+    part_o = align_up(plan + (kChunks + 1) * sizeof(int64_t), kWorkspaceAlign);
+    part_lse = part_o + static_cast<size_t>(2) * warps * g * D * sizeof(float);
+    total = align_up(part_lse + static_cast<size_t>(2) * warps * g * sizeof(float), kWorkspaceAlign);
+  }
+};
 
 template <typename K, typename... A>
-cudaError_t launch_pdl(K kern, unsigned grid, int threads, cudaStream_t stream, A... args) {
+cudaError_t launch_pdl(K kern, unsigned grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// 3-D map over a pool [rows][H_kv][D] bf16 with a box of 64 columns of one kv head's
+// `rows` rows, 128-byte swizzle.
+ts_status make_pool_map(CUtensorMap* map, const void* pool, int64_t pool_rows, int H_kv, int D, int rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return fail(TS_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H_kv),
+                              static_cast<cuuint64_t>(pool_rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(H_kv) * D * 2};
+  const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(rows)}, ones[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, ones,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(TS_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return TS_OK;
+}
+
+template <int D>
+ts_status prepare_mma(const void* kernel) {
+  return cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MmaSmem<D>::kBytes),
+                    "ts_paged_decode_sparse_attn: shared memory");
+}
+
+template <typename T, int D, int G>
+ts_status launch(const SparseParams& p, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(p.warps / kWarps);
+  const char* what = "ts_paged_decode_sparse_attn: launch";
+  ts_status st;
+  if constexpr (sizeof(T) == 2) {
+    const auto kern = sparse_mma_kernel<D, G>;
+    st = prepare_once(reinterpret_cast<const void*>(kern), prepare_mma<D>);
+    if (st != TS_OK) return st;
+    CUtensorMap kmap, vmap;
+    const int64_t pool_rows = static_cast<int64_t>(p.num_pages) * p.page_size;
+    const int box = p.page_size < 16 ? p.page_size : 16;
+    st = make_pool_map(&kmap, p.k_pool, pool_rows, p.H_kv, D, box);
+    if (st == TS_OK) st = make_pool_map(&vmap, p.v_pool, pool_rows, p.H_kv, D, box);
+    if (st != TS_OK) return st;
+    LaunchTrace trace("sparse_mma_kernel", s);
+    st = cuda_check(launch_pdl(kern, grid, kThreads, MmaSmem<D>::kBytes, s, p, kmap, vmap), what);
+  } else {
+    LaunchTrace trace("sparse_f32_kernel", s);
+    st = cuda_check(launch_pdl(sparse_f32_kernel<D, G>, grid, kThreads, 0, s, p), what);
+  }
+  if (st != TS_OK) return st;
+  LaunchTrace trace("sparse_merge_kernel", s);
+  return cuda_check(launch_pdl(sparse_merge_kernel<T, D, G>, static_cast<unsigned>(p.rows * p.H_kv), kMergeThreads, 0,
+                               s, p),
+                    "ts_paged_decode_sparse_attn: merge launch");
+}
+
 template <typename T, int D>
 ts_status launch(int g, const SparseParams& p, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.rows) * p.H_kv * p.parts);
-  {
-    LaunchTrace trace("sparse_decode_kernel", s);
-    const auto kern = g == 1   ? sparse_decode_kernel<T, D, 1>
-                      : g == 2 ? sparse_decode_kernel<T, D, 2>
-                      : g == 4 ? sparse_decode_kernel<T, D, 4>
-                               : sparse_decode_kernel<T, D, 8>;
-    const ts_status st = cuda_check(launch_pdl(kern, grid, kWarps * 32, s, p), "ts_paged_decode_sparse_attn: launch");
-    if (st != TS_OK || p.parts == 1) return st;
-  }
-  const int64_t threads = static_cast<int64_t>(p.rows) * p.H_kv * g * (D / 4);
-  LaunchTrace trace("sparse_merge_kernel", s);
-  return cuda_check(launch_pdl(sparse_merge_kernel<T, D>, static_cast<unsigned>((threads - 1) / 128 + 1), 128, s, p,
-                               p.H_kv * g),
-                    "ts_paged_decode_sparse_attn: merge launch");
+  return g == 1 ? launch<T, D, 1>(p, s) : g == 2 ? launch<T, D, 2>(p, s) : g == 4 ? launch<T, D, 4>(p, s)
+                                                                                  : launch<T, D, 8>(p, s);
 }
 
 bool supported(int H_q, int H_kv, int D, int page_size) {
@@ -313,7 +751,7 @@ extern "C" size_t ts_paged_decode_sparse_workspace_size(int32_t B, int32_t q_len
   using namespace ts;
   const int64_t rows = static_cast<int64_t>(B) * q_len;
   if (B < 0 || q_len <= 0 || pages <= 0 || rows > (1 << 24) || !supported(H_q, H_kv, D, page_size)) return 0;
-  return sparse_bytes(rows, H_q, D, sparse_parts(rows * H_kv, pages));
+  return SparseWs(sparse_warps(rows * H_kv, pages), H_q / H_kv, D).total;
 }
 
 extern "C" ts_status ts_paged_decode_sparse_attn(const void* q, const void* k_pool, const void* v_pool,
@@ -347,17 +785,16 @@ extern "C" ts_status ts_paged_decode_sparse_attn(const void* q, const void* k_po
   for (const void* x : {q, k_pool, v_pool, static_cast<const void*>(out)})
     if (reinterpret_cast<uintptr_t>(x) % 16 != 0)
       return fail(TS_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", who);
-  const int parts = sparse_parts(rows * H_kv, pages);
-  const size_t bytes = sparse_bytes(rows, H_q, D, parts);
-  if (!workspace || workspace_bytes < bytes || reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign != 0)
-    return fail(TS_ERR_WORKSPACE, "%s: workspace %zu B < %zu B needed or misaligned", who, workspace_bytes, bytes);
-  float* part_o = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kWorkspaceAlign);
-  const SparseParams p{q, k_pool, v_pool, block_table, seq_lens, page_idx, out, lse, part_o,
-                       part_o + static_cast<size_t>(parts) * rows * H_q * D, static_cast<uint32_t*>(workspace),
-                       bt_stride, static_cast<int32_t>(rows), q_len, H_kv, page_size, num_pages, pages, parts,
-                       scale * kLog2eS};
+  const int g = H_q / H_kv, warps = sparse_warps(rows * H_kv, pages);
+  const SparseWs ws(warps, g, D);
+  if (!workspace || workspace_bytes < ws.total || reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign != 0)
+    return fail(TS_ERR_WORKSPACE, "%s: workspace %zu B < %zu B needed or misaligned", who, workspace_bytes, ws.total);
+  unsigned char* w = static_cast<unsigned char*>(workspace);
+  const SparseParams p{q, k_pool, v_pool, block_table, seq_lens, page_idx, out, lse,
+                       reinterpret_cast<int64_t*>(w + ws.plan), reinterpret_cast<float*>(w + ws.part_o),
+                       reinterpret_cast<float*>(w + ws.part_lse), static_cast<uint32_t*>(workspace), bt_stride,
+                       static_cast<int32_t>(rows), q_len, H_kv, page_size, num_pages, pages, warps, scale * kLog2eS};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int g = H_q / H_kv;
   if (dtype == TS_BF16)
     return D == 64 ? launch<__nv_bfloat16, 64>(g, p, s) : launch<__nv_bfloat16, 128>(g, p, s);
   return D == 64 ? launch<float, 64>(g, p, s) : launch<float, 128>(g, p, s);

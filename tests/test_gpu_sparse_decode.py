@@ -35,7 +35,7 @@ def _lists(c, q_len, pages, order="ascending"):
                     pick[0] = have - 1
                 out[b, j, h, :n] = np.sort(pick)
                 if order == "any":
-                    out[b, j, h] = c.rng.permutation(out[b, j, h])
+                    out[b, j, h, :n] = c.rng.permutation(out[b, j, h, :n])
     return out
 
 
@@ -121,7 +121,7 @@ def test_entries_that_are_not_pages():
     idx[0, 0, 0] = [-1, -5, 12, -(2 ** 31), -1, 3]
     idx[0, 1, 1] = -1                                   # sees nothing
     idx[1, 0, 0] = [2 ** 31 - 1, 1000000, 6, 7, 5, -1]  # behind the position: skipped, not absent pages
-    idx[2, 1, 0] = [2, 2, 1, 1, 1, -1]                  # twice and three times
+    idx[2, 1, 0] = [2, 2, 1, 1, 0, -1]                  # a slot twice; three pages: three entries are taken
     out, lse, err = _run(c, q, idx)
     assert err == 0
     _check(c, q, idx, out, lse)

@@ -84,7 +84,7 @@ def test_sparse_decode_refuses_on_the_host(lib, monkeypatch):
     assert call(B=0, q=None, ws=None, wsb=0) == OK
     size = lib.ts_paged_decode_sparse_workspace_size
     need = size(1, 1, 8, 2, 64, 16, 32)
-    assert need > 256 and size(4096, 1, 8, 2, 64, 16, 32) == 256  # many rows are not cut
+    assert 256 < need <= size(4096, 1, 8, 2, 64, 16, 32) < 1 << 20  # two states for each warp of the grid at most
     assert size(-1, 1, 8, 2, 64, 16, 32) == size(1, 1, 8, 2, 96, 16, 32) == size(1, 1, 8, 2, 64, 16, 0) == 0
     assert call(wsb=need - 1) == call(ws=None) == call(ws=ctypes.c_void_p(128)) == WORKSPACE
 

@@ -20,8 +20,9 @@
 // flight, brought by the TMA as boxes of one kv head's 8 or 16 rows and 64 columns,
 // with the 128-byte swizzle so that ldmatrix meets every bank once. The g query heads are the rows of an m16n8k16 product, padded to 16: a 128-row
 // tcgen05 tile would be 4 / 128 full, and these products take a tenth of the
-// time that their 8 KB take to arrive. The weights are rounded to bf16 for P V
-// (both operands share a type) and O is divided by the sum of the unrounded ones.
+// time that their 8 KB take to arrive. Both operands of P V are bf16: the weights
+// enter as two terms, rounded weights in the rows of the heads and what the
+// rounding left in the eight rows of padding, so that they count with 16 bits.
 // float32 (sparse_f32_kernel): on the CUDA cores, 16 bytes of a row per lane,
 // four rows of K and V in flight.
 #include "ts_tcgen05.cuh"
@@ -244,6 +245,24 @@ __device__ __forceinline__ void mma_rows8(float& x, float& y, uint32_t a0, uint3
       : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// c += A (16 x 16: rows 0 .. 7 in a0, a2; rows 8 .. 15 in a1, a3) x B (16 x 8).
+__device__ __forceinline__ void mma_rows16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                           uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// What the two rounded values of a pair leave, rounded in turn.
+__device__ __forceinline__ uint32_t rest_bf16x2(float lo, float hi, uint32_t rounded) {
+  const float2 f = bf16x2_to_float2(rounded);
+  return float2_to_bf16x2(lo - f.x, hi - f.y);
+}
+
+// The sum of both terms' products; an infinite value of V times a remainder (0 or negative) must not count.
+__device__ __forceinline__ float both_terms(float x, float rest) { return fabsf(x) == INFINITY ? x : x + rest; }
+
 // A stage: 16 rows of K, then of V, in boxes of 64 columns (rows of 128 bytes, 128-byte swizzle).
 template <int D>
 struct MmaSmem {
@@ -309,9 +328,9 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
       }
     }
     float m = -INFINITY, sum = 0.f;
-    float o[D / 8][2];
+    float o[D / 8][4];  // of rounded weights, and of what the rounding left
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = 0.f;
+    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
     for (int c0 = w.i0; c0 < w.i1 && ok; c0 += 32) {
       const Listed e = listed_page(p, w, c0 + lane);
@@ -412,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
             m = top;
             sum *= scale;
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) o[j][0] *= scale, o[j][1] *= scale;
+            for (int j = 0; j < D / 8; ++j) o[j][0] *= scale, o[j][1] *= scale, o[j][2] *= scale, o[j][3] *= scale;
           }
           const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
@@ -421,12 +440,13 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
             sum += s[i];
           }
           const uint32_t p0 = float2_to_bf16x2(s[0], s[1]), p1 = float2_to_bf16x2(s[2], s[3]);
+          const uint32_t r0 = rest_bf16x2(s[0], s[1], p0), r1 = rest_bf16x2(s[2], s[3], p1);
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             uint32_t b[4];
             ldmatrix4_trans(b, vs + (j >> 2) * 2048 + (vat ^ ((j & 3) << 5)));
-            mma_rows8(o[2 * j][0], o[2 * j][1], p0, p1, b[0], b[1]);
-            mma_rows8(o[2 * j + 1][0], o[2 * j + 1][1], p0, p1, b[2], b[3]);
+            mma_rows16(o[2 * j], p0, r0, p1, r1, b[0], b[1]);
+            mma_rows16(o[2 * j + 1], p0, r0, p1, r1, b[2], b[3]);
           }
         }
         __syncwarp();
@@ -444,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
       const Target<__nv_bfloat16, D> to(p, w, worker, G, head);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays NaN)
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) to.put(8 * j + 2 * quarter, o[j][0] * inv, o[j][1] * inv);
+      for (int j = 0; j < D / 8; ++j) to.put(8 * j + 2 * quarter, both_terms(o[j][0], o[j][2]) * inv, both_terms(o[j][1], o[j][3]) * inv);
       if (quarter == 0) to.put_lse(sum == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + log2f(sum));
     }
   } while (w.next(p));

@@ -173,6 +173,19 @@ def test_scores_that_are_not_finite(dtype):
     assert not out.any() and torch.isneginf(lse).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_values_make_their_columns_infinite(dtype):
+    c, q, idx = _case(64, [640, 640], 1, 4, 2, 64, 40, dtype=dtype)
+    want = _run(c, q, idx)[0]
+    c.v_pool[c.table[0, 7], 3, 1, 9] = float("inf")
+    c.v_pool[c.table[1, 30], 15, 0, 0] = -float("inf")
+    for ctas in (1, 50):
+        out, lse, _ = _run(c, q, idx, ctas)
+        assert (out[0, 0, 4:, 9] == float("inf")).all() and (out[1, 0, :4, 0] == -float("inf")).all()
+        out[0, 0, 4:, 9], out[1, 0, :4, 0] = want[0, 0, 4:, 9], want[1, 0, :4, 0]
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
 def test_rising_scores():
     """Each page's scores far above those before: every step moves the reference."""
     c, q, _ = _case(60, [1600], 1, 4, 1, 64, 1, dtype="f32")

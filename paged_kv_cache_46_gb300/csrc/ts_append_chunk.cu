@@ -136,34 +136,6 @@ __device__ __forceinline__ uint2 codes_by_definition(const Eight<T>& x, float sc
   return make_uint2(code[0], code[1]);
 }
 
-// Quotients rounded to nearest even by Markstein's theorems ("Computation of
-// elementary functions on the IBM RISC System/6000 processor", 1990), each
-// operation rounded once:
-//   - from a y within one unit in the last place of 1 / s, y + (1 - y s) y is
-//     the rounded reciprocal, unless s's significand is all ones;
-//   - from a q within one unit of x / s and the rounded reciprocal, q + (x - q s)
-//     times it is the rounded quotient.
-// x times the reciprocal may be off by one and a half units; a first step
-// brings it within one. The residuals have to be exact, which they are for s
-// >= 1e-10 / 448 and quotients of 2^-11 or more; smaller ones are off by units
-// of their last place and far below half of the smallest code.
-__device__ __forceinline__ float quotient(float x, float s, float inv) {
-  float q = x * inv;
-  q = fmaf(fmaf(-q, s, x), inv, q);
-  return fmaf(fmaf(-q, s, x), inv, q);
-}
-__device__ __forceinline__ float2 quotients(float2 x, float2 neg_s, float2 inv) {
-  float2 q = __fmul2_rn(x, inv);
-  q = __ffma2_rn(__ffma2_rn(q, neg_s, x), inv, q);
-  return __ffma2_rn(__ffma2_rn(q, neg_s, x), inv, q);
-}
-__device__ __forceinline__ float reciprocal(float s) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));  // within one unit
-  return fmaf(fmaf(-s, y, 1.f), y, y);
-}
-__device__ __forceinline__ bool all_ones(float s) { return (~__float_as_uint(s) & 0x007fffffu) == 0u; }
-
 // Quantization as ts_kv_append_fp8, bit for bit: a group is the D values of
 // one (token, kv head); scale = max(max |x|, 1e-10) / 448, code =
 // e4m3(clamp(x / scale, -448, 448)), in float32 rounded to nearest even. A NaN

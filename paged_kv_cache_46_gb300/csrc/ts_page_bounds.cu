@@ -62,7 +62,7 @@ __device__ __forceinline__ void store_codes(int8_t* to, const float (&x)[N], flo
 // A warp takes `span` rows of the batch and one kv head; a row of D values is
 // held by kLanes lanes of 16 bytes, kRows rows at a time.
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) page_bounds_kernel(const T* __restrict__ k_pool, const BoundsParams p) {
+__global__ void __launch_bounds__(kWarps * 32) page_bounds_kernel(const T* k_pool, const BoundsParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   constexpr int kLanes = D * static_cast<int>(sizeof(T)) / 16, kRows = 32 / kLanes, kEach = 16 / sizeof(T);

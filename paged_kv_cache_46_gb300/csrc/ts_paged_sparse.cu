@@ -25,6 +25,7 @@
 // rounding left in the eight rows of padding, so that they count with 16 bits.
 // float32 (sparse_f32_kernel): on the CUDA cores, 16 bytes of a row per lane,
 // four rows of K and V in flight.
+#include "ts_ranges.cuh"
 #include "ts_tcgen05.cuh"
 
 #include <cmath>
@@ -33,7 +34,6 @@ namespace ts {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kChunks = kThreads;  // row chunks of the plan, one per thread
 constexpr int kParts = 32;         // ranges that an item is cut into at most, and one more at its end
 constexpr int kMergeThreads = 512;
 constexpr float kLog2eS = 1.4426950408889634f;
@@ -48,7 +48,7 @@ struct SparseParams {
   const int32_t* page_idx;
   void* out;
   float* lse;
-  int64_t* plan;    // [kChunks + 1] entries in front of each chunk of rows, kept for the merge
+  int64_t* plan;    // [kThreads + 1] entries in front of each chunk of rows, kept for the merge
   float* part_o;    // [2 * warps, g, D]
   float* part_lse;  // [2 * warps, g], base 2
   uint32_t* err_word;
@@ -56,116 +56,25 @@ struct SparseParams {
   float scale_log2;
 };
 
-// Position of a query row, and the entries of its lists that are taken.
-__device__ __forceinline__ int row_position(const SparseParams& p, int row) {
-  const int b = row / p.q_len;
-  return p.seq_lens[b] - p.q_len + (row - b * p.q_len);
-}
+// Entries of a row's lists that are taken.
 __device__ __forceinline__ int row_entries(const SparseParams& p, int row) {
   const int pos = row_position(p, row);
   return pos < 0 ? 0 : min(p.pages, pos / p.page_size + 1);
 }
-__device__ __forceinline__ int chunk_rows(const SparseParams& p) { return (p.rows + kChunks - 1) / kChunks; }
-
-// Entries in front of each chunk of rows (the whole CTA calls it), for one kv head.
-__device__ __forceinline__ void make_plan(const SparseParams& p, int64_t (&before)[kChunks + 1]) {
-  __shared__ int64_t warp_sum[kWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, each = chunk_rows(p);
-  int64_t sum = 0;
-  for (int r = tid * each; r < min(p.rows, (tid + 1) * each); ++r) sum += row_entries(p, r);
-  int64_t incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) incl += warp_sum[w];
-  before[tid + 1] = incl;
-  if (tid == 0) before[0] = 0;
-  __syncthreads();
-}
-
 // Entries of a warp's range, of `total` in all.
-__device__ __forceinline__ int64_t range_entries(const SparseParams& p, int64_t total) {
-  return max((total + p.warps - 1) / p.warps, static_cast<int64_t>((p.pages + kParts - 1) / kParts));
+__device__ __forceinline__ int64_t range_of(const SparseParams& p, int64_t total) {
+  return max(even_range(total, p.warps), static_cast<int64_t>((p.pages + kParts - 1) / kParts));
 }
-
-// Walks the items of entries [at, end): row, head and the part [i0, i1) of its list.
-struct Walk {
-  int64_t at, end, item0;  // item0: first entry of the item
-  int32_t row, h, count, i0, i1, pos;
-
-  // Finds the item of entry `at` (warp-wide).
-  __device__ __forceinline__ bool start(const SparseParams& p, const int64_t (&before)[kChunks + 1], int64_t from,
-                                        int64_t to, int lane) {
-    const int64_t total = before[kChunks] * p.H_kv;
-    at = from;
-    end = min(to, total);
-    if (at >= end) return false;
-    int chunk = 0;  // the last one with before * H_kv <= at
-#pragma unroll
-    for (int c0 = 0; c0 < kChunks; c0 += 32)
-      chunk += __popc(__ballot_sync(0xffffffffu, before[c0 + lane + 1] * p.H_kv <= at));
-    const int each = chunk_rows(p);
-    int64_t sum = before[chunk] * p.H_kv;
-    for (int r0 = chunk * each;; r0 += 32) {
-      const int r = r0 + lane;
-      const int n = r < p.rows ? row_entries(p, r) : 0;
-      int64_t incl = static_cast<int64_t>(n) * p.H_kv;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, sum + incl > at);
-      if (hit) {
-        const int from_lane = __ffs(hit) - 1;
-        row = r0 + from_lane;
-        count = __shfl_sync(0xffffffffu, n, from_lane);
-        sum += __shfl_sync(0xffffffffu, incl, from_lane) - static_cast<int64_t>(count) * p.H_kv;
-        break;
-      }
-      sum += __shfl_sync(0xffffffffu, incl, 31);
-      if (r0 + 32 >= p.rows) return false;  // (lengths changed under the call)
-    }
-    h = static_cast<int>((at - sum) / count);
-    item0 = sum + static_cast<int64_t>(h) * count;
-    settle(p);
-    return true;
-  }
-  __device__ __forceinline__ void settle(const SparseParams& p) {
-    pos = row_position(p, row);
-    i0 = static_cast<int>(at - item0);
-    i1 = static_cast<int>(min(static_cast<int64_t>(count), end - item0));
-  }
-  __device__ __forceinline__ bool next(const SparseParams& p) {
-    at = item0 + i1;
-    if (at >= end) return false;
-    item0 += count;
-    if (++h == p.H_kv) {
-      h = 0;
-      do {
-        if (++row >= p.rows) return false;
-        count = row_entries(p, row);
-      } while (count == 0);
-    }
-    settle(p);
-    return true;
-  }
-  __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == count; }
-};
 
 // A listed page: its pool page and how many of its tokens the row sees (0: none).
 struct Listed {
   int32_t page, tokens;
 };
-__device__ __forceinline__ Listed listed_page(const SparseParams& p, const Walk& w, int i) {
+__device__ __forceinline__ Listed listed_page(const SparseParams& p, const Walk& w, int pos, int i) {
   Listed e{0, 0};
   if (i >= w.i1) return e;
   const int idx = p.page_idx[(static_cast<int64_t>(w.row) * p.H_kv + w.h) * p.pages + i];
-  if (idx < 0 || static_cast<int64_t>(idx) * p.page_size > w.pos) return e;
+  if (idx < 0 || static_cast<int64_t>(idx) * p.page_size > pos) return e;
   const int page =
       idx < p.bt_stride ? p.block_table[static_cast<int64_t>(w.row / p.q_len) * p.bt_stride + idx] : -1;
   if (page < 0 || page >= p.num_pages) {
@@ -173,7 +82,7 @@ __device__ __forceinline__ Listed listed_page(const SparseParams& p, const Walk&
     return e;
   }
   e.page = page;
-  e.tokens = min(p.page_size, w.pos - idx * p.page_size + 1);
+  e.tokens = min(p.page_size, pos - idx * p.page_size + 1);
   return e;
 }
 
@@ -283,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
   constexpr int kStages = S::kStages;
   extern __shared__ __align__(1024) unsigned char ring[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
-  __shared__ int64_t before[kChunks + 1];
+  __shared__ int64_t before[kThreads + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t worker = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   if ((smem_u32(ring) & 1023u) != 0u) {
@@ -294,13 +203,13 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
     for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(&bars[0][0] + i), 1);
     fence_mbar_init();
   }
-  make_plan(p, before);
-  const int64_t range = range_entries(p, before[kChunks] * p.H_kv);
+  make_plan<kThreads>(p, before);
+  const int64_t range = range_of(p, before[kThreads] * p.H_kv);
   Walk w;
-  const bool any = w.start(p, before, worker * range, (worker + 1) * range, lane);
+  const bool any = w.start<kThreads>(p, before, worker * range, (worker + 1) * range, lane);
   pdl_wait_primary();  // so far the lengths alone were read
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= kChunks; i += kThreads) p.plan[i] = before[i];
+    for (int i = threadIdx.x; i <= kThreads; i += kThreads) p.plan[i] = before[i];
   if (!any) return;
 
   const uint32_t stage0 = smem_u32(ring) + warp * kStages * S::kStage;
@@ -316,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
   bool ok = true;
 
   do {
+    const int pos = row_position(p, w.row);
     // the item's queries, as rows of A
     uint32_t qa[D / 16][2];
     {
@@ -333,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
     for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
     for (int c0 = w.i0; c0 < w.i1 && ok; c0 += 32) {
-      const Listed e = listed_page(p, w, c0 + lane);
+      const Listed e = listed_page(p, w, pos, c0 + lane);
       const int entries = min(32, w.i1 - c0);
       const int tiles = (entries * groups + 1) >> 1;
       // pool row and seen rows of the eight-row group i of these entries
@@ -479,19 +389,20 @@ template <int D, int G>
 __global__ void __launch_bounds__(kThreads) sparse_f32_kernel(const SparseParams p) {
   pdl_launch_dependents();
   constexpr int kEach = 4, kLanes = D / kEach, kRows = 32 / kLanes, kAhead = 4;
-  __shared__ int64_t before[kChunks + 1];
+  __shared__ int64_t before[kThreads + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % kLanes, sub = lane / kLanes;
   const int64_t worker = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  make_plan(p, before);
-  const int64_t range = range_entries(p, before[kChunks] * p.H_kv);
+  make_plan<kThreads>(p, before);
+  const int64_t range = range_of(p, before[kThreads] * p.H_kv);
   Walk w;
-  const bool any = w.start(p, before, worker * range, (worker + 1) * range, lane);
+  const bool any = w.start<kThreads>(p, before, worker * range, (worker + 1) * range, lane);
   pdl_wait_primary();  // so far the lengths alone were read
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= kChunks; i += kThreads) p.plan[i] = before[i];
+    for (int i = threadIdx.x; i <= kThreads; i += kThreads) p.plan[i] = before[i];
   if (!any) return;
   const int64_t step = static_cast<int64_t>(p.H_kv) * D;  // elements between rows
   do {
+    const int pos = row_position(p, w.row);
     float q[G][kEach], acc[G][kEach], m[G], sum[G];
     const float* qsrc =
         static_cast<const float*>(p.q) + (static_cast<int64_t>(w.row) * p.H_kv * G + w.h * G) * D + l * kEach;
@@ -506,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) sparse_f32_kernel(const SparseParams
       for (int d = 0; d < kEach; ++d) acc[i][d] = 0.f;
     }
     for (int c0 = w.i0; c0 < w.i1; c0 += 32) {
-      const Listed e = listed_page(p, w, c0 + lane);
+      const Listed e = listed_page(p, w, pos, c0 + lane);
       for (unsigned todo = __ballot_sync(0xffffffffu, e.tokens > 0); todo; todo &= todo - 1) {
         const int from = __ffs(todo) - 1;
         const int64_t page = __shfl_sync(0xffffffffu, e.page, from);
@@ -609,7 +520,7 @@ __global__ void __launch_bounds__(kMergeThreads) sparse_merge_kernel(const Spars
   __shared__ float sh_total[G], sh_top[G];
   pdl_launch_dependents();
   const int row = blockIdx.x / p.H_kv, h = blockIdx.x % p.H_kv, tid = threadIdx.x;
-  const int count = row_entries(p, row), each = chunk_rows(p), chunk = row / each;
+  const int count = row_entries(p, row), each = chunk_rows<kThreads>(p), chunk = row / each;
   // entries in front of the row, in its chunk
   int64_t in_front = 0;
   if (row > chunk * each) {
@@ -622,7 +533,7 @@ __global__ void __launch_bounds__(kMergeThreads) sparse_merge_kernel(const Spars
   }
   pdl_wait_primary();  // so far the lengths alone were read
   in_front += p.plan[chunk];
-  const int64_t range = range_entries(p, p.plan[kChunks] * p.H_kv);
+  const int64_t range = range_of(p, p.plan[kThreads] * p.H_kv);
   const int64_t first = in_front * p.H_kv + static_cast<int64_t>(h) * count;
   const int64_t w0 = first / range, w1 = (first + count - 1) / range;
   if (count > 0 && w0 == w1) return;  // written already
@@ -679,7 +590,7 @@ struct SparseWs {
   size_t plan, part_o, part_lse, total;
   SparseWs(int warps, int g, int D) {
     plan = kWorkspaceAlign;
-    part_o = align_up(plan + (kChunks + 1) * sizeof(int64_t), kWorkspaceAlign);
+    part_o = align_up(plan + (kThreads + 1) * sizeof(int64_t), kWorkspaceAlign);
     part_lse = part_o + static_cast<size_t>(2) * warps * g * D * sizeof(float);
     total = align_up(part_lse + static_cast<size_t>(2) * warps * g * sizeof(float), kWorkspaceAlign);
   }

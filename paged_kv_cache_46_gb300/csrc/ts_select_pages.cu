@@ -10,21 +10,26 @@
 // device. A term is c M' where c > 0 and c m' where c < 0: the row [max(c, 0),
 // min(c, 0)] times the row [M', m'], four 8-bit products an instruction.
 //
-// page_score_kernel: HBM bounds it (2 D + 4 bytes a page and head). A warp keeps
-// the codes of the g query heads of one kv head in registers; 2 D / 16 lanes take
-// a page's bounds, 16 bytes each.
-// page_pick_kernel: a CTA per query row and kv head finds the threshold by
-// counting in bins that halve no range but cut the remaining one in 2048, then
-// lists the pages above it in order; equal scores go to the lowest pages.
-#include "ts_common.cuh"
+// page_score_kernel: HBM bounds it (2 D + 4 bytes a page and head). A warp takes
+// one kv head; sixteen pages are the rows of an m16n8k32 product of 8-bit whole
+// numbers, the g query heads (padded to eight) its columns. The order of the codes
+// along the sum is free, so that a lane's operands are 16 bytes of a page's codes as
+// they lie in memory, and 16 bytes of a query head's; nothing goes through shared
+// memory.
+// page_pick_kernel: a CTA per query row and kv head. One histogram of 2048 equal
+// bins between the smallest and the largest key finds the bin of the threshold;
+// the few keys in it are ranked against each other (key, then page); a bit per
+// chosen page and a sum over the words of bits give each its place in the list.
+// Where many keys share the bin, it is cut in 2048 again first.
+#include "ts_ranges.cuh"
 
 #include <cmath>
 
 namespace ts {
 namespace {
 
-constexpr int kWarps = 8, kPickThreads = 512, kPickBins = 2048, kPickSmemKeys = 8192;
-constexpr int kSlots = 64;  // pages per scoring CTA
+constexpr int kThreads = 128, kWarps = kThreads / 32, kResident = 5;  // CTAs on an SM
+constexpr int kBins = 2048, kKeys = 16, kRanked = 96;  // kKeys: in a thread's registers
 
 struct SelectParams {
   const int8_t* bounds;
@@ -34,246 +39,376 @@ struct SelectParams {
   uint32_t* keys;  // [rows, H_kv, bt_stride]
   int32_t* page_idx;
   uint32_t* err_word;
-  int32_t bt_stride, q_len, H_kv, page_size, num_pages, pages, first, last;
+  int32_t bt_stride, rows, q_len, H_kv, page_size, num_pages, pages, first, last, warps;
 };
 
-// Pages of the query at the row's position, as far as the table has slots; < 0 position: none.
+// Pages of the query at a row's position, as far as the table has slots; none in front of the first token.
 __device__ __forceinline__ int pages_of(const SelectParams& p, int row, bool* past) {
-  const int b = row / p.q_len;
-  const int pos = p.seq_lens[b] - p.q_len + (row - b * p.q_len);
+  const int pos = row_position(p, row);
   if (pos < 0) return 0;
   const int have = pos / p.page_size + 1;
   *past = have > p.bt_stride;
   return min(have, p.bt_stride);
 }
+// Tiles of sixteen pages to be scored, where the row has more pages than are listed.
+__device__ __forceinline__ int row_entries(const SelectParams& p, int row) {
+  bool past;
+  const int have = pages_of(p, row, &past);
+  return have > p.pages ? (have + 15) / 16 : 0;
+}
 
 // Scores as whole numbers of their order: NaN above all, 0 is no score's.
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);  // -0 becomes 0: they are equal
-  if ((u & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t key = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return x != x ? 0xffffffffu : key;
 }
+// The larger of two scores; NaN if one is.
+__device__ __forceinline__ float larger(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
+// d += A (16 x 32, 8 bits) x B (32 x 8, 8 bits).
+__device__ __forceinline__ void mma_s8(int32_t (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                       uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four consecutive values as floats.
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Bytes that hold four whole numbers below zero, and those that do not.
+__device__ __forceinline__ uint32_t negative_bytes(uint32_t w) { return ((w >> 7) & 0x01010101u) * 0xffu; }
 
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kWarps * 32) page_score_kernel(const T* __restrict__ q, const SelectParams p) {
-  pdl_wait_primary();
+__global__ void __launch_bounds__(kThreads, kResident) page_score_kernel(const T* q, const SelectParams p) {
   pdl_launch_dependents();
-  constexpr int kL = 2 * D / 16, kU = 32 / kL;  // lanes of a page's bounds, pages at a time
-  __shared__ __align__(16) int8_t code[8 * G][2 * D];
-  __shared__ float q_scale[8 * G];
-  __shared__ int32_t page[kSlots];
-  const int row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = row / p.q_len, i0 = blockIdx.x * kSlots;
-  bool past = false;
-  const int have = pages_of(p, row, &past);
-  if (have <= p.pages || i0 >= have) {
-    if (past && blockIdx.x == 0 && threadIdx.x == 0) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
+  constexpr int kChunks = 2 * D / 64;  // of 64 codes: a quad of lanes holds 16 each
+  constexpr int kTiles = D == 128 ? 1 : 2;  // in flight
+  __shared__ int64_t before[kThreads + 1];
+  const int lane = threadIdx.x & 31, quarter = lane & 3, at = lane >> 2;
+  const int64_t worker = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  make_plan<kThreads>(p, before);
+  const int64_t range = even_range(before[kThreads] * p.H_kv, p.warps);
+  Walk walk;
+  if (!walk.start<kThreads>(p, before, worker * range, (worker + 1) * range, lane)) {
+    pdl_wait_primary();
     return;
   }
-  if (past && threadIdx.x == 0) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
-  for (int i = threadIdx.x; i < kSlots; i += kWarps * 32) {
-    int pg = -1;
-    if (i0 + i < have) {
-      pg = p.block_table[static_cast<int64_t>(b) * p.bt_stride + i0 + i];
-      if (pg < 0 || pg >= p.num_pages) {
-        set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
-        pg = -1;
-      }
-    }
-    page[i] = pg;
-  }
-  const int H_q = p.H_kv * G;
-  for (int h = warp; h < H_q; h += kWarps) {
-    const T* src = q + (static_cast<int64_t>(row) * H_q + h) * D;
-    float x[D / 32];
-    uint32_t largest = 0u;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      x[i] = static_cast<float>(src[lane + 32 * i]);
-      largest = max(largest, __float_as_uint(x[i]) & 0x7fffffffu);
-    }
-    largest = __reduce_max_sync(0xffffffffu, largest);
-    const bool odd = largest >= 0x7f800000u;
-    const float top = __uint_as_float(largest);  // (a NaN stays one)
-    const float scale = odd ? top : fmaxf(top, 1e-10f) * (1.f / 127.f);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int c = odd ? 0 : static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(x[i], scale)), -127.f), 127.f));
-      code[h][lane + 32 * i] = static_cast<int8_t>(max(c, 0));
-      code[h][D + lane + 32 * i] = static_cast<int8_t>(min(c, 0));
-    }
-    if (lane == 0) q_scale[h] = scale;
-  }
-  __syncthreads();
 
-  const int h = warp % p.H_kv, share = warp / p.H_kv, shares = kWarps / p.H_kv;
-  const int l = lane % kL, sub = lane / kL;
-  uint4 c[G];
+  bool waited = false;
+  do {
+    const int row = walk.row, h = walk.h;
+    bool past;
+    const int have = pages_of(p, row, &past);
+    const int end = min(have, 16 * walk.i1);
+    const int32_t* table = p.block_table + static_cast<int64_t>(row / p.q_len) * p.bt_stride;
+    // rows `at` and `at` + 8 of the tiles in flight: pages, looked up a step ahead of their codes and scales
+    int32_t page[kTiles][2];
+    uint4 w[kTiles][2][kChunks];
+    float s[kTiles][2];
+    bool good[kTiles][2];
+    auto look_up = [&](int first) {
 #pragma unroll
-  for (int i = 0; i < G; ++i) c[i] = *reinterpret_cast<const uint4*>(&code[h * G + i][16 * l]);
-  // after the sums a lane holds those of one head: its index follows from the lane
-  int mine = 0;
+      for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-  for (int n = G / 2, o = kL / 2; n > 0; n >>= 1, o >>= 1) mine += (l & o) ? n : 0;
-  const float qs = q_scale[h * G + mine];
-  uint32_t* keys = p.keys + (static_cast<int64_t>(row) * p.H_kv + h) * p.bt_stride;
-
-  constexpr int kAhead = 4;
-  const int step = shares * kU;
-  for (int j0 = share * kU + sub; j0 - sub < kSlots; j0 += kAhead * step) {
-    uint4 w[kAhead];
-    float s[kAhead];
+        for (int r = 0; r < 2; ++r) {
+          const int slot = first + 16 * t + 8 * r + at;
+          page[t][r] = slot < end ? table[slot] : -1;
+        }
+    };
+    auto load = [&](int t) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int j = j0 + u * step;
-      const int pg = j < kSlots ? page[j] : -1;
-      const int64_t at = static_cast<int64_t>(max(pg, 0)) * p.H_kv + h;
-      w[u] = *reinterpret_cast<const uint4*>(p.bounds + at * 2 * D + 16 * l);
-      s[u] = p.bound_scale[at];
-    }
+      for (int r = 0; r < 2; ++r) {
+        good[t][r] = static_cast<uint32_t>(page[t][r]) < static_cast<uint32_t>(p.num_pages);
+        const int64_t place = static_cast<int64_t>(good[t][r] ? page[t][r] : 0) * p.H_kv + h;
+        const uint4* src = reinterpret_cast<const uint4*>(p.bounds + place * 2 * D) + quarter;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int j = j0 + u * step;
-      int v[G];
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        v[i] = __dp4a(static_cast<int>(c[i].x), static_cast<int>(w[u].x), 0);
-        v[i] = __dp4a(static_cast<int>(c[i].y), static_cast<int>(w[u].y), v[i]);
-        v[i] = __dp4a(static_cast<int>(c[i].z), static_cast<int>(w[u].z), v[i]);
-        v[i] = __dp4a(static_cast<int>(c[i].w), static_cast<int>(w[u].w), v[i]);
+        for (int c = 0; c < kChunks; ++c) w[t][r][c] = src[4 * c];
+        s[t][r] = p.bound_scale[place];
       }
-      int o = kL / 2;
+    };
+    int i = 16 * walk.i0;
+    look_up(i);
+    if (!waited) pdl_wait_primary();  // so far lengths and block table alone were read
+    waited = true;
 #pragma unroll
-      for (int n = G / 2; n > 0; n >>= 1, o >>= 1) {
-        const bool upper = (l & o) != 0;
+    for (int t = 0; t < kTiles; ++t)
+      if (i + 16 * t < end) load(t);
+    look_up(i + 16 * kTiles);
+
+    // the codes of query head `at`, as columns of B: above zero beside the upper bounds, below beside the lower
+    uint32_t code[kChunks][4];
+    float q_scale = 0.f;
+    {
+      const T* src = q + (static_cast<int64_t>(row) * p.H_kv * G + h * G + (G < 8 ? min(at, G - 1) : at)) * D + 16 * quarter;
+      uint32_t largest = 0u;
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-          const int send = upper ? v[i] : v[i + n];
-          v[i] = (upper ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, send, o);
+      for (int c = 0; c < kChunks / 2; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 x = load4(src + 64 * c + 4 * k);
+          largest = max(max(max(magnitude(x.x), magnitude(x.y)), max(magnitude(x.z), magnitude(x.w))), largest);
+        }
+      largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
+      largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
+      const bool odd = largest >= 0x7f800000u;  // (its scale stays infinite or NaN, and so do its scores)
+      q_scale = odd ? __uint_as_float(largest) : fmaxf(__uint_as_float(largest), 1e-10f) * (1.f / 127.f);
+      const float inv = reciprocal(q_scale);
+      auto quantize = [&](auto&& divide) {
+#pragma unroll
+        for (int c = 0; c < kChunks / 2; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 x = load4(src + 64 * c + 4 * k);
+            // 1.5 * 2^23 more: the rounded number is in the last bits
+            const uint32_t u0 = __float_as_uint(divide(x.x) + 12582912.f), u1 = __float_as_uint(divide(x.y) + 12582912.f);
+            const uint32_t u2 = __float_as_uint(divide(x.z) + 12582912.f), u3 = __float_as_uint(divide(x.w) + 12582912.f);
+            const uint32_t word = odd ? 0u : __byte_perm(__byte_perm(u0, u1, 0x0040), __byte_perm(u2, u3, 0x0040), 0x5410);
+            const uint32_t below = negative_bytes(word);
+            code[c][k] = word & ~below;
+            code[kChunks / 2 + c][k] = word & below;
+          }
+      };
+      if (__any_sync(0xffffffffu, all_ones(q_scale)))  // see quotient()
+        quantize([&](float x) { return __fdiv_rn(x, q_scale); });
+      else
+        quantize([&](float x) { return quotient(x, q_scale, inv); });
+    }
+    const float qs0 = __shfl_sync(0xffffffffu, q_scale, 8 * quarter);
+    const float qs1 = __shfl_sync(0xffffffffu, q_scale, 8 * quarter + 4);
+    uint32_t* keys = p.keys + (static_cast<int64_t>(row) * p.H_kv + h) * p.bt_stride;
+
+    for (; i < end; i += 16 * kTiles) {
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        const int first = i + 16 * t;
+        if (first >= end) break;
+        int32_t dot[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          mma_s8(dot, w[t][0][c].x, w[t][1][c].x, w[t][0][c].y, w[t][1][c].y, code[c][0], code[c][1]);
+          mma_s8(dot, w[t][0][c].z, w[t][1][c].z, w[t][0][c].w, w[t][1][c].w, code[c][2], code[c][3]);
+        }
+        const float scale[2] = {s[t][0], s[t][1]};
+        const bool ok[2] = {good[t][0], good[t][1]};
+        if (first + 16 * kTiles < end) load(t);
+        float score[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {  // heads 2 quarter and 2 quarter + 1
+          float k0 = static_cast<float>(dot[2 * r]) * qs0 * scale[r];
+          const float k1 = static_cast<float>(dot[2 * r + 1]) * qs1 * scale[r];
+          if (G > 1) k0 = larger(k0, k1);
+          if (G < 8) k0 = 2 * quarter < G ? k0 : -INFINITY;
+          if (G > 2) k0 = larger(k0, __shfl_xor_sync(0xffffffffu, k0, 1));
+          if (G > 4) k0 = larger(k0, __shfl_xor_sync(0xffffffffu, k0, 2));
+          if (G <= 2) k0 = __shfl_sync(0xffffffffu, k0, lane & 28);
+          score[r] = k0;  // complete in the quad's first two lanes
+        }
+        const int slot = first + 8 * quarter + at;  // which store rows `at` and `at` + 8
+        if (quarter < 2 && slot < end) {
+          const bool fine = quarter ? ok[1] : ok[0];
+          keys[slot] = fine ? order_key(quarter ? score[1] : score[0]) : 0u;
+          if (!fine) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
         }
       }
-#pragma unroll
-      for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-      uint32_t key = order_key(static_cast<float>(v[0]) * qs * s[u]);
-      o = kL / 2;
-#pragma unroll
-      for (int n = G / 2; n > 0; n >>= 1, o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
-      if (l == 0 && j < kSlots && i0 + j < have) keys[i0 + j] = page[j] >= 0 ? key : 0u;
+      look_up(i + 32 * kTiles);
     }
-  }
+  } while (walk.next(p));
 }
 
+// Sums of v over the threads in front, and over all (uniform); `sums` is scratch of a word per warp.
+template <int kWarpsOf>
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t (&sums)[kWarpsOf], uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();  // the sums of a scan before have been read
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  uint32_t mine = lane < kWarpsOf ? sums[lane] : 0u;
+  total = __reduce_add_sync(0xffffffffu, mine);
+  mine = lane < warp ? mine : 0u;
+  return incl - v + __reduce_add_sync(0xffffffffu, mine);
+}
+
+template <int kPickThreads>
 __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectParams p) {
-  pdl_wait_primary();
+  __shared__ uint32_t bins[kBins];
+  __shared__ uint32_t ranked_key[kRanked], ranked_at[kRanked];
+  __shared__ uint32_t words[kPickThreads];  // bits of the chosen, a stretch of pages at a time
+  __shared__ uint32_t sums[kPickThreads / 32], low[kPickThreads / 32], high[kPickThreads / 32];
+  __shared__ uint32_t sh_need, sh_bin, sh_count, sh_ranked;
+  static_assert(kPickThreads / 32 <= 32 && kBins % kPickThreads == 0, "one warp adds up the warps' sums");
   pdl_launch_dependents();
-  __shared__ uint32_t bins[kPickBins];
-  __shared__ uint32_t kept[kPickSmemKeys];
-  __shared__ uint32_t warp_a[kPickThreads / 32], warp_b[kPickThreads / 32];
-  __shared__ uint32_t shared_lo, shared_hi, shared_need, shared_bin;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t item = blockIdx.x;  // (row, kv head)
   const int row = static_cast<int>(item / p.H_kv);
   bool past = false;
   const int have = pages_of(p, row, &past);
+  pdl_wait_primary();  // so far the lengths alone were read
+  if (past && tid == 0) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
   int32_t* out = p.page_idx + item * p.pages;
   if (have <= p.pages) {
-    if (past && tid == 0) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
     for (int i = tid; i < p.pages; i += kPickThreads) out[i] = i < have ? i : -1;
     return;
   }
-  const int n = have - p.first - p.last, need0 = p.pages - p.first - p.last;  // n > need0
+  const int n = have - p.first - p.last;
+  uint32_t need = static_cast<uint32_t>(p.pages - p.first - p.last);  // of n, which are more
   for (int i = tid; i < p.first; i += kPickThreads) out[i] = i;
   for (int i = tid; i < p.last; i += kPickThreads) out[p.pages - p.last + i] = have - p.last + i;
-  if (need0 == 0) return;
+  if (need == 0u) return;
   const uint32_t* keys = p.keys + item * p.bt_stride + p.first;
-  if (n <= kPickSmemKeys) {
-    for (int i = tid; i < n; i += kPickThreads) kept[i] = keys[i];
-    keys = kept;
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  const bool fits = n <= kKeys * kPickThreads;
+  uint32_t kept[kKeys];
+  if (fits) {
+#pragma unroll
+    for (int u = 0; u < kKeys; ++u) kept[u] = tid + u * kPickThreads < n ? keys[tid + u * kPickThreads] : 0u;
   }
-  if (tid == 0) shared_lo = 0xffffffffu, shared_hi = 0u, shared_need = static_cast<uint32_t>(need0);
+  // f(i, key) for this thread's keys
+  auto each_key = [&](auto&& f) {
+    if (fits) {
+#pragma unroll
+      for (int u = 0; u < kKeys; ++u) {
+        if (u * kPickThreads >= n) break;
+        if (tid + u * kPickThreads < n) f(tid + u * kPickThreads, kept[u]);
+      }
+    } else {
+#pragma unroll 8
+      for (int i = tid; i < n; i += kPickThreads) f(i, keys[i]);
+    }
+  };
+  each_key([&](int, uint32_t k) { lo = min(lo, k), hi = max(hi, k); });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) low[warp] = lo, high[warp] = hi;
+  for (int i = tid; i < kBins; i += kPickThreads) bins[i] = 0u;
+  if (tid == 0) sh_ranked = 0u;
   __syncthreads();
-  {
-    uint32_t lo = 0xffffffffu, hi = 0u;
-    for (int i = tid; i < n; i += kPickThreads) lo = min(lo, keys[i]), hi = max(hi, keys[i]);
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) atomicMin(&shared_lo, lo), atomicMax(&shared_hi, hi);
-  }
-  __syncthreads();
-  // [lo, hi] holds the need-th largest key; cut it in bins until it is one value
-  uint32_t lo = shared_lo, hi = shared_hi, need = shared_need;
-  while (lo < hi) {
+  lo = __reduce_min_sync(0xffffffffu, lane < kPickThreads / 32 ? low[lane] : 0xffffffffu);
+  hi = __reduce_max_sync(0xffffffffu, lane < kPickThreads / 32 ? high[lane] : 0u);
+
+  // [lo, hi] holds the need-th largest of the keys that are not above hi
+  uint32_t inside = static_cast<uint32_t>(n);  // keys in [lo, hi]
+  while (lo < hi && inside > kRanked) {
     const int shift = max(0, 32 - __clz(static_cast<int>(hi - lo)) - 11);
-    for (int i = tid; i < kPickBins; i += kPickThreads) bins[i] = 0u;
-    __syncthreads();
-    for (int i = tid; i < n; i += kPickThreads) {
-      const uint32_t k = keys[i];
+    each_key([&](int, uint32_t k) {
       if (k >= lo && k <= hi) atomicAdd(&bins[(k - lo) >> shift], 1u);
-    }
+    });
     __syncthreads();
-    // counts from the highest bin down; four bins a thread
-    constexpr int kEach = kPickBins / kPickThreads;
-    uint32_t sum = 0u;
+    // counts from the highest bin down, some bins a thread; each is cleared for the next cut
+    constexpr int kEach = kBins / kPickThreads;
+    uint32_t count[kEach], sum = 0u, total;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) sum += bins[kPickBins - 1 - (tid * kEach + i)];
-    uint32_t incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+    for (int i = 0; i < kEach; ++i) {
+      const int bin = kBins - 1 - (tid * kEach + i);
+      count[i] = bins[bin];
+      bins[bin] = 0u;
+      sum += count[i];
     }
-    if (lane == 31) warp_a[warp] = incl;
-    __syncthreads();
-    uint32_t before = 0u;
-    for (int i = 0; i < warp; ++i) before += warp_a[i];
-    uint32_t above = before + incl - sum;  // keys in higher bins than this thread's
+    uint32_t above = block_scan(sum, sums, total);
     if (above < need && above + sum >= need) {
+#pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int bin = kPickBins - 1 - (tid * kEach + i);
-        if (above + bins[bin] >= need) {
-          shared_bin = static_cast<uint32_t>(bin);
-          shared_need = need - above;
-          break;
+        if (above < need && above + count[i] >= need) {
+          sh_bin = static_cast<uint32_t>(kBins - 1 - (tid * kEach + i));
+          sh_need = need - above;
+          sh_count = count[i];
         }
-        above += bins[bin];
+        above += count[i];
       }
     }
     __syncthreads();
-    need = shared_need;
-    lo += shared_bin << shift;
+    need = sh_need;
+    inside = sh_count;
+    lo += sh_bin << shift;
     hi = lo + min(hi - lo, (1u << shift) - 1u);
+  }
+  // Above hi: chosen. In [lo, hi]: the need largest, and of equal keys the lowest pages; where all are one
+  // value, simply the first.
+  const bool equal = lo == hi;
+  if (!equal) {
+    each_key([&](int i, uint32_t k) {
+      if (k >= lo && k <= hi) {
+        const uint32_t to = atomicAdd(&sh_ranked, 1u);  // `inside` in all, in any order
+        ranked_key[to] = k;
+        ranked_at[to] = static_cast<uint32_t>(i);
+      }
+    });
+    __syncthreads();
+    // the key and page of the last one chosen
+    for (uint32_t c = tid; c < inside; c += kPickThreads) {
+      const uint32_t k = ranked_key[c], at = ranked_at[c];
+      uint32_t rank = 0u;
+      for (uint32_t j = 0; j < inside; ++j) rank += ranked_key[j] > k || (ranked_key[j] == k && ranked_at[j] < at);
+      if (rank == need - 1u) sh_bin = k, sh_count = at;
+    }
     __syncthreads();
   }
-  // keys above lo, and the first `need` equal to it, in order of their pages
-  const int each = (n + kPickThreads - 1) / kPickThreads, a0 = min(n, tid * each), a1 = min(n, a0 + each);
-  uint32_t more = 0u, same = 0u;
-  for (int i = a0; i < a1; ++i) more += keys[i] > lo, same += keys[i] == lo;
-  uint32_t more_incl = more, same_incl = same;
+  const uint32_t last_key = equal ? lo : sh_bin, last_at = equal ? 0u : sh_count;
+  uint32_t placed = 0u, equals = 0u;
+  for (int base = 0; base < n; base += 32 * kPickThreads) {  // once, for up to 16,384 pages
+    const int stretch = min(n - base, 32 * kPickThreads), groups = (stretch + 31) / 32;
+    auto mark = [&](int g, uint32_t k) {
+      const int i = base + g * 32 + lane;
+      const bool same = i < n && k == last_key;
+      const bool take = i < n && (k > last_key || (!equal && same && static_cast<uint32_t>(i) <= last_at));
+      const unsigned bits = __ballot_sync(0xffffffffu, take), ties = __ballot_sync(0xffffffffu, equal && same);
+      if (lane == 0) words[g] = bits, bins[g] = ties;
+    };
+    if (fits) {  // (then base is 0)
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, more_incl, o), z = __shfl_up_sync(0xffffffffu, same_incl, o);
-    if (lane >= o) more_incl += y, same_incl += z;
-  }
-  if (lane == 31) warp_a[warp] = more_incl, warp_b[warp] = same_incl;
-  __syncthreads();
-  uint32_t more_at = more_incl - more, same_at = same_incl - same;
-  for (int i = 0; i < warp; ++i) more_at += warp_a[i], same_at += warp_b[i];
-  for (int i = a0; i < a1; ++i) {
-    const uint32_t k = keys[i];
-    const bool equal = k == lo;
-    if (k > lo || (equal && same_at < need)) out[p.first + more_at + min(same_at, need)] = p.first + i;
-    more_at += k > lo;
-    same_at += equal;
+      for (int u = 0; u < kKeys; ++u) {
+        if (u * kPickThreads >= n) break;
+        mark(u * (kPickThreads / 32) + warp, kept[u]);
+      }
+    } else {
+      for (int g = warp; g < groups; g += kPickThreads / 32) {
+        const int i = base + g * 32 + lane;
+        mark(g, i < n ? keys[i] : 0u);
+      }
+    }
+    __syncthreads();
+    uint32_t bits = tid < groups ? words[tid] : 0u, total;
+    if (equal) {  // of the ties the first `need`
+      uint32_t ties = tid < groups ? bins[tid] : 0u;
+      uint32_t room = block_scan(__popc(ties), sums, total) + equals;
+      equals += total;
+      room = room < need ? need - room : 0u;
+      while (__popc(ties) > static_cast<int>(room)) ties &= ~(0x80000000u >> __clz(static_cast<int>(ties)));
+      bits |= ties;
+    }
+    uint32_t to = block_scan(__popc(bits), sums, total) + placed;
+    placed += total;
+    for (; bits; bits &= bits - 1u) out[p.first + to++] = p.first + base + tid * 32 + __ffs(static_cast<int>(bits)) - 1;
+    __syncthreads();
   }
 }
 
 template <typename K, typename... A>
-cudaError_t launch_pdl(K kern, dim3 grid, int threads, cudaStream_t stream, A... args) {
+cudaError_t launch_pdl(K kern, unsigned grid, int threads, cudaStream_t stream, A... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -282,13 +417,13 @@ cudaError_t launch_pdl(K kern, dim3 grid, int threads, cudaStream_t stream, A...
 }
 
 template <typename T, int D>
-cudaError_t launch_score(int g, dim3 grid, cudaStream_t stream, const void* q, const SelectParams& p) {
+cudaError_t launch_score(int g, unsigned grid, cudaStream_t stream, const void* q, const SelectParams& p) {
   const T* src = static_cast<const T*>(q);
   switch (g) {
-    case 1: return launch_pdl(page_score_kernel<T, D, 1>, grid, kWarps * 32, stream, src, p);
-    case 2: return launch_pdl(page_score_kernel<T, D, 2>, grid, kWarps * 32, stream, src, p);
-    case 4: return launch_pdl(page_score_kernel<T, D, 4>, grid, kWarps * 32, stream, src, p);
-    default: return launch_pdl(page_score_kernel<T, D, 8>, grid, kWarps * 32, stream, src, p);
+    case 1: return launch_pdl(page_score_kernel<T, D, 1>, grid, kThreads, stream, src, p);
+    case 2: return launch_pdl(page_score_kernel<T, D, 2>, grid, kThreads, stream, src, p);
+    case 4: return launch_pdl(page_score_kernel<T, D, 4>, grid, kThreads, stream, src, p);
+    default: return launch_pdl(page_score_kernel<T, D, 8>, grid, kThreads, stream, src, p);
   }
 }
 
@@ -338,23 +473,28 @@ extern "C" ts_status ts_select_pages(const void* q, const int8_t* bounds, const 
   const size_t bytes = select_bytes(rows, H_kv, bt_stride);
   if (!workspace || workspace_bytes < bytes || reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign != 0)
     return fail(TS_ERR_WORKSPACE, "%s: workspace %zu B < %zu B needed or misaligned", who, workspace_bytes, bytes);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // Warps: those the device holds, or one for each tile of the longest sequences there can be.
+  const int64_t tiles = rows * H_kv * ((static_cast<int64_t>(bt_stride) + 15) / 16);
+  const int64_t full = static_cast<int64_t>(device_sm_count()) * kResident * kWarps;
+  const unsigned ctas = static_cast<unsigned>(((tiles < full ? tiles : full) + kWarps - 1) / kWarps);
   const SelectParams p{bounds,    bound_scale, block_table, seq_lens,
                        reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(workspace) + kWorkspaceAlign),
-                       page_idx,  static_cast<uint32_t*>(workspace), bt_stride, q_len, H_kv, page_size, num_pages,
-                       pages, first, last};
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
+                       page_idx,  static_cast<uint32_t*>(workspace), bt_stride, static_cast<int32_t>(rows), q_len, H_kv,
+                       page_size, num_pages, pages, first, last, static_cast<int32_t>(ctas) * kWarps};
   if (bt_stride > pages && pages > first + last) {  // else nothing is ranked
-    const dim3 grid(static_cast<unsigned>((bt_stride - 1) / kSlots + 1), static_cast<unsigned>(rows));
     LaunchTrace trace("page_score_kernel", s);
-    const cudaError_t e =
-        dtype == TS_BF16 ? (D == 64 ? launch_score<__nv_bfloat16, 64>(g, grid, s, q, p)
-                                    : launch_score<__nv_bfloat16, 128>(g, grid, s, q, p))
-                         : (D == 64 ? launch_score<float, 64>(g, grid, s, q, p)
-                                    : launch_score<float, 128>(g, grid, s, q, p));
+    const cudaError_t e = dtype == TS_BF16 ? (D == 64 ? launch_score<__nv_bfloat16, 64>(g, ctas, s, q, p)
+                                                      : launch_score<__nv_bfloat16, 128>(g, ctas, s, q, p))
+                                           : (D == 64 ? launch_score<float, 64>(g, ctas, s, q, p)
+                                                      : launch_score<float, 128>(g, ctas, s, q, p));
     const ts_status st = cuda_check(e, "ts_select_pages: launch");
     if (st != TS_OK) return st;
   }
+  // Threads of a choosing CTA: as many as hold all of its keys in registers, so that small ones leave room for others.
   LaunchTrace trace("page_pick_kernel", s);
-  return cuda_check(launch_pdl(page_pick_kernel, dim3(static_cast<unsigned>(rows * H_kv)), kPickThreads, s, p),
+  const unsigned items = static_cast<unsigned>(rows * H_kv);
+  return cuda_check(bt_stride <= 256 * kKeys ? launch_pdl(page_pick_kernel<256>, items, 256, s, p)
+                                             : launch_pdl(page_pick_kernel<1024>, items, 1024, s, p),
                     "ts_select_pages: launch");
 }

@@ -16,14 +16,17 @@
 // rows. D / 8 lanes hold a head, as two groups of four columns a lane, chosen so
 // that both columns of a pair are in one lane: nothing is exchanged but the sum
 // of squares. The heads of a step are taken kBatch steps at a time, loaded before
-// the row's place is known.
+// the row's place is known. Weights, cosines and sines of a lane's columns are two
+// factors per column, made once per row for the queries and once for the keys:
+//   y = inv * (x P + partner Q),
+// in packed multiply-adds, since instructions would bound it otherwise.
 //
 // Angles: a float32 product of position and frequency is off by 2^-24 of the
 // angle, a hundredth of a turn at position 131,072. Turns are counted in 64-bit
 // fixed point instead: inv_freq / (2 pi) mod 1 as a 64-bit fraction (a float64
-// product and its remainder), times the position modulo 2^64, is the angle in turns. Its nearest
-// quarter turn is taken off exactly and the rest, at most an eighth of a turn,
-// is rounded to float32 once: 2^-24 of pi / 4 at most.
+// product and its remainder, once per CTA), times the position modulo 2^64, is the
+// angle in turns. Its nearest quarter turn is taken off exactly and the rest, at
+// most an eighth of a turn, is rounded to float32 once: 2^-24 of pi / 4 at most.
 #include "ts_ragged.cuh"
 
 #include <cmath>
@@ -80,12 +83,16 @@ struct Quad<float> {
   __device__ __forceinline__ void set(const float (&x)[4]) { w = make_float4(x[0], x[1], x[2], x[3]); }
 };
 
-// Cosine and sine of pos * inv_freq (see the head of this file).
-__device__ __forceinline__ float2 turn(int pos, float inv_freq) {
+// inv_freq / (2 pi) modulo 1, in units of 2^-64.
+__device__ __forceinline__ unsigned long long turns_per_position(float inv_freq) {
   const double x = inv_freq, f = x * 0.15915494309189534;  // 1 / (2 pi), and what this product and constant leave
   const double low = fma(x, 0.15915494309189534, -f) + x * -9.839338337591243e-18;
-  const unsigned long long step = static_cast<unsigned long long>((f - floor(f)) * 18446744073709551616.0) +
-                                  static_cast<unsigned long long>(static_cast<long long>(low * 18446744073709551616.0));
+  return static_cast<unsigned long long>((f - floor(f)) * 18446744073709551616.0) +
+         static_cast<unsigned long long>(static_cast<long long>(low * 18446744073709551616.0));
+}
+
+// Cosine and sine of the angle at a position.
+__device__ __forceinline__ float2 turn(int pos, unsigned long long step) {
   const uint32_t t = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * step) >> 32);
   const uint32_t quarter = (t + 0x20000000u) >> 30;
   const int32_t rest = static_cast<int32_t>(t - (quarter << 30));  // within an eighth of a turn
@@ -95,41 +102,56 @@ __device__ __forceinline__ float2 turn(int pos, float inv_freq) {
   return make_float2((quarter + 1u) & 2u ? -u : u, quarter & 2u ? -v : v);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeParams<T> p) {
+template <typename T, int D, bool kInterleaved>
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 2) rope_append_kernel(const RopeParams<T> p) {
   // Programmatic dependent launch as in ts_kv_append.
   pdl_wait_primary();
   pdl_launch_dependents();
   constexpr int kLanes = D / 8, kVecs = 32 / kLanes;
+  __shared__ unsigned long long steps[D / 2];
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t r = w / p.parts;
+  const int64_t r = w / static_cast<uint32_t>(p.parts);
   const int part = static_cast<int>(w - r * p.parts);
-  if (r >= p.T_rows) return;
   const int l = lane % kLanes, vec = lane / kLanes;
   const bool turns = l < p.rot / 8;
-  const bool split = turns && !p.interleaved;
+  const bool split = turns && !kInterleaved;
   const int oa = split ? 4 * l : 8 * l, ob = split ? p.rot / 2 + 4 * l : 8 * l + 4;
-  const int heads = p.H_q + 2 * p.H_kv;
 
+  // Sections: the row's queries, keys, values; this warp takes every parts-th step of them in order.
+  int section = 0, s = part, heads = p.H_q;
+  const T* src = p.q + r * p.q_stride;
+  auto steps_of = [](int n) { return (n + kVecs - 1) / kVecs; };
+  // From a section's end to the first step of the next that is this warp's; false behind the last one.
+  auto settle = [&]() {
+    for (int n = steps_of(heads); s >= n; n = steps_of(heads)) {
+      while (s - p.parts >= n) s -= p.parts;  // (the last batch may have passed the end by some steps)
+      s -= n;
+      if (++section > 2) return false;
+      heads = p.H_kv;
+      src = (section == 1 ? p.k_new : p.v_new) + r * p.new_stride;
+    }
+    return true;
+  };
   Quad<T> xa[kBatch], xb[kBatch];
-  auto load = [&](int s0) {
+  auto load = [&]() {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int hv = (s0 + u * p.parts) * kVecs + vec;
-      if (hv < heads) {
-        const T* src = hv < p.H_q            ? p.q + r * p.q_stride + hv * D
-                       : hv < p.H_q + p.H_kv ? p.k_new + r * p.new_stride + (hv - p.H_q) * D
-                                             : p.v_new + r * p.new_stride + (hv - p.H_q - p.H_kv) * D;
-        xa[u].load(src + oa);
-        xb[u].load(src + ob);
+      const int h = (s + u * p.parts) * kVecs + vec;
+      if (h < heads) {
+        xa[u].load(src + h * D + oa);
+        xb[u].load(src + h * D + ob);
       } else {
         xa[u] = {};
         xb[u] = {};
       }
     }
   };
-  load(part);
+  bool any = r < p.T_rows && settle();
+  if (any) load();
+  for (int i = threadIdx.x; i < p.rot / 2; i += kWarps * 32) steps[i] = turns_per_position(p.inv_freq[i]);
+  __syncthreads();
+  if (!any) return;
   const int b = ragged_sequence(p.q_indptr, p.B, static_cast<int>(r), lane);
   if (b < 0) return;
   const int pos = p.seq_lens[b] - (p.q_indptr[b + 1] - static_cast<int>(r));
@@ -143,7 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopePara
     float2 own[kOwn];
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
-      own[i] = turns ? turn(pos, p.inv_freq[4 * l + vec * kOwn + i]) : make_float2(1.f, 0.f);
+      own[i] = turns ? turn(pos, steps[4 * l + vec * kOwn + i]) : make_float2(1.f, 0.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int from = i / kOwn * kLanes + l;
@@ -152,67 +174,90 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopePara
     }
   }
 
-  for (int s0 = part;;) {
+  // Factors of the columns a[0 .. 3], c[0 .. 3] and of their partners, two columns each.
+  float2 P[4], Q[4];
+  auto factors = [&](const T* weight) {
+    float a[4] = {1.f, 1.f, 1.f, 1.f}, c[4] = {1.f, 1.f, 1.f, 1.f};
+    if (weight != nullptr) {
+      Quad<T> q;
+      q.load(weight + oa);
+      q.get(a);
+      q.load(weight + ob);
+      q.get(c);
+    }
+    if (kInterleaved) {  // partners are neighbours
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        P[i] = make_float2(a[2 * i] * cs[i].x, a[2 * i + 1] * cs[i].x);
+        Q[i] = make_float2(-a[2 * i + 1] * cs[i].y, a[2 * i] * cs[i].y);
+        P[2 + i] = make_float2(c[2 * i] * cs[2 + i].x, c[2 * i + 1] * cs[2 + i].x);
+        Q[2 + i] = make_float2(-c[2 * i + 1] * cs[2 + i].y, c[2 * i] * cs[2 + i].y);
+      }
+    } else {  // partners of a are c
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        P[i] = make_float2(a[2 * i] * cs[2 * i].x, a[2 * i + 1] * cs[2 * i + 1].x);
+        Q[i] = make_float2(-c[2 * i] * cs[2 * i].y, -c[2 * i + 1] * cs[2 * i + 1].y);
+        P[2 + i] = make_float2(c[2 * i] * cs[2 * i].x, c[2 * i + 1] * cs[2 * i + 1].x);
+        Q[2 + i] = make_float2(a[2 * i] * cs[2 * i].y, a[2 * i + 1] * cs[2 * i + 1].y);
+      }
+    }
+  };
+  int made = -1;  // section that P and Q are of
+  for (;;) {
+    const T* weight = section == 0 ? p.q_weight : section == 1 ? p.k_weight : nullptr;
+    T* dst = section == 0   ? p.q_out + r * p.q_out_stride
+             : section == 1 ? p.k_pool + row * p.H_kv * D
+                            : p.v_pool + row * p.H_kv * D;
+    const bool stored = section == 0 || row >= 0;
+    const bool changes = section < 2 && (weight != nullptr || p.rot > 0);
+    if (changes && made != section) {
+      factors(weight);
+      made = section;
+    }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int hv = (s0 + u * p.parts) * kVecs + vec;
-      const bool is_q = hv < p.H_q, is_v = hv >= p.H_q + p.H_kv;
-      const T* weight = is_q ? p.q_weight : is_v ? nullptr : p.k_weight;
-      float a[4], c[4];
-      xa[u].get(a);
-      xb[u].get(c);
-      float ss = 0.f;
+      const int h = (s + u * p.parts) * kVecs + vec;
+      if (changes) {
+        float a[4], c[4];
+        xa[u].get(a);
+        xb[u].get(c);
+        const float2 x[4] = {{a[0], a[1]}, {a[2], a[3]}, {c[0], c[1]}, {c[2], c[3]}};
+        float2 y[4];
+        float2 inv = make_float2(1.f, 1.f);
+        if (weight != nullptr) {
+          float2 two = __fmul2_rn(x[0], x[0]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ss = fmaf(a[i], a[i], fmaf(c[i], c[i], ss));
+          for (int i = 1; i < 4; ++i) two = __ffma2_rn(x[i], x[i], two);
+          float ss = two.x + two.y;
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (weight != nullptr) {
-        const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-        Quad<T> wq;
-        float wt[4];
-        wq.load(weight + oa);
-        wq.get(wt);
+          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          inv.x = inv.y = rsqrtf(ss * (1.f / D) + p.eps);
+        }
+        if (turns) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = a[i] * inv * wt[i];
-        wq.load(weight + ob);
-        wq.get(wt);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = c[i] * inv * wt[i];
-      }
-      if (turns) {
-        if (p.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float a0 = a[2 * i], c0 = c[2 * i];
-            a[2 * i] = a0 * cs[i].x - a[2 * i + 1] * cs[i].y;
-            a[2 * i + 1] = a[2 * i + 1] * cs[i].x + a0 * cs[i].y;
-            c[2 * i] = c0 * cs[i + 2].x - c[2 * i + 1] * cs[i + 2].y;
-            c[2 * i + 1] = c[2 * i + 1] * cs[i + 2].x + c0 * cs[i + 2].y;
+          for (int i = 0; i < 4; ++i) {
+            const float2 partner = kInterleaved ? make_float2(x[i].y, x[i].x) : x[i ^ 2];
+            y[i] = __fmul2_rn(__ffma2_rn(x[i], P[i], __fmul2_rn(partner, Q[i])), inv);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a0 = a[i];
-            a[i] = a0 * cs[i].x - c[i] * cs[i].y;
-            c[i] = c[i] * cs[i].x + a0 * cs[i].y;
-          }
+          for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(__fmul2_rn(x[i], P[i]), inv);
+        }
+        if (turns || weight != nullptr) {  // columns that nothing touches stay as they are, bit for bit
+          const float ya[4] = {y[0].x, y[0].y, y[1].x, y[1].y}, yc[4] = {y[2].x, y[2].y, y[3].x, y[3].y};
+          xa[u].set(ya);
+          xb[u].set(yc);
         }
       }
-      if (!is_v && (turns || weight != nullptr)) {  // V and untouched columns stay as they are, bit for bit
-        xa[u].set(a);
-        xb[u].set(c);
-      }
-      if (hv < heads && (is_q || row >= 0)) {
-        T* dst = is_q    ? p.q_out + r * p.q_out_stride + hv * D
-                 : is_v ? p.v_pool + (row * p.H_kv + (hv - p.H_q - p.H_kv)) * D
-                        : p.k_pool + (row * p.H_kv + (hv - p.H_q)) * D;
-        xa[u].store(dst + oa);
-        xb[u].store(dst + ob);
+      if (h < heads && stored) {
+        xa[u].store(dst + h * D + oa);
+        xb[u].store(dst + h * D + ob);
       }
     }
-    s0 += kBatch * p.parts;
-    if (s0 * kVecs >= heads) return;
-    load(s0);
+    s += kBatch * p.parts;
+    if (!settle()) return;
+    load();
   }
 }
 
@@ -238,7 +283,8 @@ ts_status launch(int D, const void* q, const void* k_new, const void* v_new, con
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kern = D == 64 ? rope_append_kernel<T, 64> : rope_append_kernel<T, 128>;
+  auto kern = D == 64 ? (p.interleaved ? rope_append_kernel<T, 64, true> : rope_append_kernel<T, 64, false>)
+                      : (p.interleaved ? rope_append_kernel<T, 128, true> : rope_append_kernel<T, 128, false>);
   LaunchTrace trace("rope_append_kernel", stream);
   return cuda_check(cudaLaunchKernelEx(&cfg, kern, p), "ts_kv_append_chunk_rope: launch");
 }

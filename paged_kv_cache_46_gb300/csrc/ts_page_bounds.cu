@@ -27,32 +27,89 @@ struct BoundsParams {
   PageSize page_size;
 };
 
-// 16 bytes of K as floats.
+// Running maxima and minima of 16 bytes of K a row; NaN once there is one.
 template <typename T>
-__device__ __forceinline__ void widen(const uint4& w, float (&x)[16 / sizeof(T)]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Extremes;
+template <>
+struct Extremes<__nv_bfloat16> {
+  __nv_bfloat162 top[4], low[4];
+  __device__ __forceinline__ Extremes() {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 2) {
-      const float2 f = bf16x2_to_float2(u[i]);
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    } else {
-      x[i] = __uint_as_float(u[i]);
+    for (int i = 0; i < 4; ++i) set(top[i], 0xff80ff80u), set(low[i], 0x7f807f80u);  // -inf, +inf
+  }
+  __device__ __forceinline__ static void set(__nv_bfloat162& x, uint32_t w) { x = *reinterpret_cast<__nv_bfloat162*>(&w); }
+  __device__ __forceinline__ void add(const uint4& w) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 x;
+      set(x, u[i]);
+      top[i] = __hmax2_nan(top[i], x);
+      low[i] = __hmin2_nan(low[i], x);
     }
   }
-}
+  __device__ __forceinline__ void join(int o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      top[i] = __hmax2_nan(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+      low[i] = __hmin2_nan(low[i], __shfl_xor_sync(0xffffffffu, low[i], o));
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[8], bool upper) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __bfloat1622float2(upper ? top[i] : low[i]);
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+  }
+};
+template <>
+struct Extremes<float> {
+  float top[4], low[4];
+  __device__ __forceinline__ Extremes() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top[i] = -INFINITY, low[i] = INFINITY;
+  }
+  __device__ __forceinline__ static void max_of(float& x, float y) { asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(y)); }
+  __device__ __forceinline__ static void min_of(float& x, float y) { asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(y)); }
+  __device__ __forceinline__ void add(const uint4& w) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) max_of(top[i], __uint_as_float(u[i])), min_of(low[i], __uint_as_float(u[i]));
+  }
+  __device__ __forceinline__ void join(int o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      max_of(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+      min_of(low[i], __shfl_xor_sync(0xffffffffu, low[i], o));
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[4], bool upper) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = upper ? top[i] : low[i];
+  }
+};
 
-// Codes of n values, outward: ceil (up) or floor, within +-127; 0 where the page's scale is not finite.
+// Codes of n bounds, outward: ceil (upper) or floor of x / scale, within +-127; 0 where the scale is not
+// finite. `exact`: by a division each, for quotients that quotients() may not round as one.
 template <int N>
-__device__ __forceinline__ void store_codes(int8_t* to, const float (&x)[N], float scale, bool up) {
+__device__ __forceinline__ void store_codes(int8_t* to, const float (&x)[N], float scale, bool upper, bool exact) {
+  uint32_t byte[N];
+  const float inv = reciprocal(scale), sign = upper ? 1.f : -1.f;  // floor(y) = -ceil(-y)
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    float2 y = quotients(make_float2(x[i], x[i + 1]), make_float2(-scale, -scale), make_float2(inv, inv));
+    if (exact) y = make_float2(__fdiv_rn(x[i], scale), __fdiv_rn(x[i + 1], scale));
+    // 1.5 * 2^23 more: the whole number is in the last bits
+    byte[i] = __float_as_uint(fmaf(sign, fminf(ceilf(y.x * sign), 127.f), 12582912.f));
+    byte[i + 1] = __float_as_uint(fmaf(sign, fminf(ceilf(y.y * sign), 127.f), 12582912.f));
+  }
   uint32_t w[N / 4];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float y = __fdiv_rn(x[i], scale);
-    const int c = scale < INFINITY ? static_cast<int>(fminf(fmaxf(up ? ceilf(y) : floorf(y), -127.f), 127.f)) : 0;
-    const uint32_t byte = static_cast<uint32_t>(c) & 0xffu;
-    w[i / 4] = i % 4 ? w[i / 4] | byte << (8 * (i % 4)) : byte;
-  }
+  for (int i = 0; i < N / 4; ++i)
+    w[i] = scale < INFINITY ? __byte_perm(__byte_perm(byte[4 * i], byte[4 * i + 1], 0x0040),
+                                          __byte_perm(byte[4 * i + 2], byte[4 * i + 3], 0x0040), 0x5410)
+                            : 0u;
   if constexpr (N == 8)
     *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
   else
@@ -62,33 +119,44 @@ __device__ __forceinline__ void store_codes(int8_t* to, const float (&x)[N], flo
 // A warp takes `span` rows of the batch and one kv head; a row of D values is
 // held by kLanes lanes of 16 bytes, kRows rows at a time.
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) page_bounds_kernel(const T* k_pool, const BoundsParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 4) page_bounds_kernel(const T* k_pool, const BoundsParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   constexpr int kLanes = D * static_cast<int>(sizeof(T)) / 16, kRows = 32 / kLanes, kEach = 16 / sizeof(T);
+  constexpr int kAhead = 16 / kRows;  // loads in flight: sixteen rows
   const int lane = threadIdx.x & 31;
   const int h = blockIdx.y * kWarps + (threadIdx.x >> 5);
   if (h >= p.H_kv) return;
   const int ps = p.page_size.rows;
   // lane i looks at row i of the span: is it the first of its page in this batch?
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * p.span + lane;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.span, r = r0 + lane;
+  const int base = max(0, ragged_floor(p.q_indptr, p.B, static_cast<int>(r0), lane));
+  int b = base;
+  if (p.span > 1) {  // sequences that begin inside the span
+    const int at = base + 1 + lane;
+    const int begins = at < p.B ? p.q_indptr[at] : 0x7fffffff;
+    const int inside = __popc(__ballot_sync(0xffffffffu, begins < r0 + 32));
+    for (int k = 0; k < inside; ++k) b += __shfl_sync(0xffffffffu, begins, k) <= r;
+    if (inside == 32) {  // (many empty ones: search on)
+      int hi = p.B;
+      while (hi - b > 1) {
+        const int mid = (b + hi) >> 1;
+        if (p.q_indptr[mid] <= r)
+          b = mid;
+        else
+          hi = mid;
+      }
+    }
+  }
   int page = -1, count = 0;
   if (lane < p.span && r < p.T) {
-    int lo = 0, hi = p.B;  // the last b with q_indptr[b] <= r
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.q_indptr[mid] <= r)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    const int r0 = p.q_indptr[lo], r1 = p.q_indptr[lo + 1];
-    if (r0 <= r && r < r1) {
-      const int L = p.seq_lens[lo], pos = L - (r1 - static_cast<int>(r));
+    const int first = p.q_indptr[b], end = p.q_indptr[b + 1];
+    if (first <= r && r < end) {
+      const int L = p.seq_lens[b], pos = L - (end - static_cast<int>(r));
       const int slot = p.page_size.shift >= 0 ? pos >> p.page_size.shift : pos / ps;
       const int at = pos - slot * ps;
-      if (pos >= 0 && (r == r0 || at == 0) && slot < p.bt_stride) {
-        page = p.block_table[static_cast<int64_t>(lo) * p.bt_stride + slot];
+      if (pos >= 0 && (r == first || at == 0) && slot < p.bt_stride) {
+        page = p.block_table[static_cast<int64_t>(b) * p.bt_stride + slot];
         if (page >= p.num_pages) page = -1;
         count = min(ps, L - slot * ps);
       }
@@ -103,42 +171,43 @@ __global__ void __launch_bounds__(kWarps * 32) page_bounds_kernel(const T* k_poo
     const int n = __shfl_sync(0xffffffffu, count, from);
     const uint4* k = reinterpret_cast<const uint4*>(k_pool + (pg * ps * p.H_kv + h) * D) + l;
     const int64_t step = static_cast<int64_t>(p.H_kv) * D * sizeof(T) / 16;
+    Extremes<T> e;
+    for (int t0 = sub; t0 < n; t0 += kAhead * kRows) {
+      uint4 w[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) w[u] = k[min(t0 + u * kRows, n - 1) * step];  // (a row again changes nothing)
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) e.add(w[u]);
+    }
+#pragma unroll
+    for (int o = 16; o >= kLanes; o >>= 1) e.join(o);
     float top[kEach], low[kEach];
-    uint32_t largest = 0u;
+    e.get(top, true);
+    e.get(low, false);
+    uint32_t largest = 0u, least = 0xffffffffu;  // magnitudes order as their bits do, NaN above all
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) top[i] = -INFINITY, low[i] = INFINITY;
-    for (int t0 = sub; t0 < n; t0 += 4 * kRows) {
-      uint4 w[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) w[u] = k[min(t0 + u * kRows, n - 1) * step];  // (a row again changes nothing)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        float x[kEach];
-        widen<T>(w[u], x);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          top[i] = fmaxf(top[i], x[i]);
-          low[i] = fminf(low[i], x[i]);
-          largest = max(largest, __float_as_uint(x[i]) & 0x7fffffffu);  // orders as magnitudes, NaN above all
-        }
-      }
+    for (int i = 0; i < kEach; ++i) {
+      const uint32_t a = __float_as_uint(top[i]) & 0x7fffffffu, c = __float_as_uint(low[i]) & 0x7fffffffu;
+      largest = max(largest, max(a, c));
+      least = min(least, min(a - 1u, c - 1u));  // (zeros last)
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, o));
-#pragma unroll
-    for (int o = 16; o >= kLanes; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
-        low[i] = fminf(low[i], __shfl_xor_sync(0xffffffffu, low[i], o));
-      }
+    largest = __reduce_max_sync(0xffffffffu, largest);
     const float scale = largest >= 0x7f800000u ? INFINITY : fmaxf(__uint_as_float(largest), 1e-10f) * (1.f / 127.f);
-    if (sub == 0) {
-      int8_t* to = p.bounds + (pg * p.H_kv + h) * 2 * D + l * kEach;
-      store_codes(to, top, scale, true);
-      store_codes(to + D, low, scale, false);
-      if (l == 0) p.scale[pg * p.H_kv + h] = scale;
+    // quotients below 2^-11, and scales whose reciprocal may not be the rounded one: see quotient()
+    const bool exact = __any_sync(0xffffffffu, least != 0xffffffffu && __uint_as_float(least) < scale * 0x1p-11f) ||
+                       all_ones(scale);
+    int8_t* to = p.bounds + (pg * p.H_kv + h) * 2 * D + l * kEach;
+    if (kRows == 1) {
+      store_codes(to, top, scale, true, exact);
+      store_codes(to + D, low, scale, false, exact);
+    } else if (sub < 2) {  // a half each
+      const bool upper = sub == 0;
+      float x[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) x[i] = upper ? top[i] : low[i];
+      store_codes(to + sub * D, x, scale, upper, exact);
     }
+    if (lane == 0) p.scale[pg * p.H_kv + h] = scale;
   }
 }
 
@@ -183,7 +252,7 @@ extern "C" ts_status ts_kv_page_bounds(const void* k_pool, int8_t* bounds, float
   if (reinterpret_cast<uintptr_t>(bound_scale) % 4 != 0)
     return fail(TS_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", who);
   // Few rows: a warp each, so that the pages of a decode step are taken at once.
-  const int span = T <= 2048 ? 1 : 32;
+  const int span = T <= 2048 ? 1 : 16;
   const BoundsParams p{bounds, bound_scale, block_table, seq_lens, q_indptr, bt_stride, T,
                        B,      H_kv,        num_pages,   span,     PageSize(page_size)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -6,11 +6,11 @@
 
 namespace ts {
 
-// The sequence whose rows hold `row`, or -1. A whole warp calls it with one
-// row; each step compares 32 entries, so a batch of up to 1024 sequences takes
-// two dependent loads before the check. Entries out of order cannot lead out
-// of [0, B): the result is checked against the sequence's own bounds.
-__device__ __forceinline__ int ragged_sequence(const int32_t* __restrict__ indptr, int B, int row, int lane) {
+// The last sequence that begins at `row` or in front of it, or -1. A whole warp
+// calls it with one row; each step compares 32 entries, so a batch of up to 1024
+// sequences takes two dependent loads. Entries out of order cannot lead out of
+// [0, B).
+__device__ __forceinline__ int ragged_floor(const int32_t* __restrict__ indptr, int B, int row, int lane) {
   int lo = 0, hi = B;  // the last b in [lo, hi) with indptr[b] <= row
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
@@ -20,7 +20,14 @@ __device__ __forceinline__ int ragged_sequence(const int32_t* __restrict__ indpt
     lo += (31 - __clz(static_cast<int>(below))) * step;
     hi = min(hi, lo + step);
   }
-  return indptr[lo] <= row && row < indptr[lo + 1] ? lo : -1;
+  return lo;
+}
+
+// The sequence whose rows hold `row`, or -1; as ragged_floor, and checked against
+// the sequence's own bounds.
+__device__ __forceinline__ int ragged_sequence(const int32_t* __restrict__ indptr, int B, int row, int lane) {
+  const int b = ragged_floor(indptr, B, row, lane);
+  return b >= 0 && indptr[b] <= row && row < indptr[b + 1] ? b : -1;
 }
 
 // A page size and its logarithm (-1 where it is no power of two: the appends and

@@ -18,6 +18,9 @@ namespace {
 constexpr int kMaxBuffers = 128;  // of a launch
 constexpr int kThreads = 256;
 constexpr int kPiece = 16384;
+constexpr int kScanThreads = 1024;
+// Tables and pools that one CTA plans alone, in one launch instead of three.
+constexpr int kPlanEntries = 32768, kPlanWords = 8192;
 
 struct Buffers {
   uint8_t* data[kMaxBuffers];
@@ -111,8 +114,15 @@ struct CompactParams {
 };
 
 __device__ __forceinline__ bool holds(const CompactParams& p, int64_t entry) {
-  const int b = static_cast<int>(entry / p.bt_stride), slot = static_cast<int>(entry % p.bt_stride);
-  return static_cast<int64_t>(slot) * p.page_size < p.seq_lens[b];
+  int64_t b, slot;
+  if (entry < (1ll << 31)) {  // (a division of 64 bits takes several times as long)
+    b = static_cast<uint32_t>(entry) / static_cast<uint32_t>(p.bt_stride);
+    slot = entry - b * p.bt_stride;
+  } else {
+    b = entry / p.bt_stride;
+    slot = entry % p.bt_stride;
+  }
+  return slot * p.page_size < p.seq_lens[b];
 }
 
 __global__ void __launch_bounds__(kThreads) page_clear_kernel(const CompactParams p) {
@@ -135,18 +145,16 @@ __global__ void __launch_bounds__(kThreads) page_mark_kernel(const CompactParams
   }
 }
 
-// One CTA: prefix sums over the words of bits, then the lists of moves.
-__global__ void __launch_bounds__(1024) page_scan_kernel(const CompactParams p) {
-  pdl_wait_primary();
-  pdl_launch_dependents();
+// Prefix sums over the words of `bits` by a CTA of kScanThreads, then the lists of moves.
+__device__ __forceinline__ void scan_pages(const CompactParams& p, const uint32_t* bits) {
   __shared__ int32_t warp_sum[32];
   __shared__ int32_t front;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int each = (p.words + 1023) / 1024;
+  const int each = (p.words + kScanThreads - 1) / kScanThreads;
   const int64_t w0 = min(static_cast<int64_t>(p.words), static_cast<int64_t>(tid) * each);
   const int64_t w1 = min(static_cast<int64_t>(p.words), w0 + each);
   int sum = 0;
-  for (int64_t w = w0; w < w1; ++w) sum += __popc(p.bits[w]);
+  for (int64_t w = w0; w < w1; ++w) sum += __popc(bits[w]);
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -155,16 +163,14 @@ __global__ void __launch_bounds__(1024) page_scan_kernel(const CompactParams p) 
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  int at = incl - sum, U = 0;
-  for (int i = 0; i < 32; ++i) {
-    if (i < warp) at += warp_sum[i];
-    U += warp_sum[i];
-  }
+  const int of_lane = warp_sum[lane];
+  const int U = __reduce_add_sync(0xffffffffu, of_lane);
+  const int at = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? of_lane : 0);
   int rank = at;
   if (tid == 0) front = U;  // of pages 0 .. P - 1 with U == P
   __syncthreads();
   for (int64_t w = w0; w < w1; ++w) {
-    const uint32_t x = p.bits[w];
+    const uint32_t x = bits[w];
     p.before[w] = rank;
     if (w == U >> 5) front = rank + __popc(x & ((1u << (U & 31)) - 1u));
     rank += __popc(x);
@@ -173,7 +179,7 @@ __global__ void __launch_bounds__(1024) page_scan_kernel(const CompactParams p) 
   const int kept = front;  // held pages in front of page U: they stay
   rank = at;
   for (int64_t w = w0; w < w1; ++w) {
-    const uint32_t x = p.bits[w];
+    const uint32_t x = bits[w];
     const int64_t page0 = w * 32;
     if (page0 + 32 > U) {  // held pages from U on
       uint32_t far = page0 >= U ? x : x & ~((1u << (U - page0)) - 1u);
@@ -193,6 +199,30 @@ __global__ void __launch_bounds__(1024) page_scan_kernel(const CompactParams p) 
     p.counts[1] = kept;
     p.counts[2] = U - kept;
   }
+}
+
+__global__ void __launch_bounds__(kScanThreads) page_scan_kernel(const CompactParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  scan_pages(p, p.bits);
+}
+
+// All three steps of a small plan by one CTA: bits in shared memory, kept in the workspace for the moves.
+__global__ void __launch_bounds__(kScanThreads) page_plan_kernel(const CompactParams p) {
+  __shared__ uint32_t bits[kPlanWords];
+  pdl_launch_dependents();
+  for (int i = threadIdx.x; i < p.words; i += kScanThreads) bits[i] = 0u;
+  __syncthreads();
+  pdl_wait_primary();
+  const int entries = p.B * p.bt_stride;  // kPlanEntries at most
+#pragma unroll 4
+  for (int i = threadIdx.x; i < entries; i += kScanThreads) {
+    const int page = p.block_table[i];
+    if (holds(p, i) && page >= 0 && page < p.num_pages) atomicOr(bits + (page >> 5), 1u << (page & 31));
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.words; i += kScanThreads) p.bits[i] = bits[i];
+  scan_pages(p, bits);
 }
 
 // Where a page moves: itself below U, a target from U on, -1 if no row holds it.
@@ -338,29 +368,24 @@ extern "C" ts_status ts_kv_compact(void* const* buffers, const int64_t* page_byt
                   bt_stride, B, page_size, num_pages, static_cast<int32_t>((static_cast<int64_t>(num_pages) + 31) / 32), 1};
   const unsigned sms = static_cast<unsigned>(device_sm_count());
   const int64_t entries = static_cast<int64_t>(B) * bt_stride;
-  {
-    LaunchTrace trace("page_clear_kernel", s);
-    const ts_status done = cuda_check(launch_pdl(page_clear_kernel, grid_for(p.words, 8 * sms), kThreads, s, p),
-                                      "ts_kv_compact: launch");
-    if (done != TS_OK) return done;
+  auto step = [&](const char* name, auto kern, unsigned grid, int threads) {
+    LaunchTrace trace(name, s);
+    return cuda_check(launch_pdl(kern, grid, threads, s, p), "ts_kv_compact: launch");
+  };
+  ts_status done = TS_OK;
+  if (entries <= kPlanEntries && p.words <= kPlanWords) {
+    done = step("page_plan_kernel", page_plan_kernel, 1u, kScanThreads);
+  } else {
+    done = step("page_clear_kernel", page_clear_kernel, grid_for(p.words, 8 * sms), kThreads);
+    if (done == TS_OK && B > 0) done = step("page_mark_kernel", page_mark_kernel, grid_for(entries, 8 * sms), kThreads);
+    if (done == TS_OK) done = step("page_scan_kernel", page_scan_kernel, 1u, kScanThreads);
   }
-  if (B > 0) {
-    LaunchTrace trace("page_mark_kernel", s);
-    const ts_status done = cuda_check(launch_pdl(page_mark_kernel, grid_for(entries, 8 * sms), kThreads, s, p),
-                                      "ts_kv_compact: launch");
-    if (done != TS_OK) return done;
-  }
-  {
-    LaunchTrace trace("page_scan_kernel", s);
-    const ts_status done = cuda_check(launch_pdl(page_scan_kernel, 1u, 1024, s, p), "ts_kv_compact: launch");
-    if (done != TS_OK) return done;
-  }
+  if (done != TS_OK) return done;
   for (int32_t at = 0; at == 0 || at < n_buffers; at += kMaxBuffers, p.tables = 0) {
     Buffers b;
     const int64_t pieces = take_buffers(b, buffers, page_bytes, at, n_buffers);
     LaunchTrace trace("page_move_kernel", s);
-    const ts_status done = cuda_check(launch_pdl(page_move_kernel, 8 * sms, kThreads, s, b, p, pieces),
-                                      "ts_kv_compact: launch");
+    done = cuda_check(launch_pdl(page_move_kernel, 8 * sms, kThreads, s, b, p, pieces), "ts_kv_compact: launch");
     if (done != TS_OK) return done;
   }
   return TS_OK;

@@ -253,6 +253,35 @@ def _pointers(*tensors):
     return out
 
 
+def _marshal(stream, *tensors):
+    """Pointers of contiguous tensors on the current CUDA device (None stays None), and the
+    handle of the call's stream behind them."""
+    here = -2
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        at = t.get_device()
+        if at != here:
+            if at < 0 or here != -2 or at != torch.cuda.current_device():
+                raise ValueError(f"tensors must be on the current CUDA device (got {t.device})")
+            here = at
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        out.append(t.data_ptr())
+    out.append(_raw_stream(here) if stream is None and _raw_stream is not None else _stream(stream))
+    return out
+
+
+def _row_step(t: torch.Tensor, rows: int, heads: int, D: int) -> int:
+    """Row step (elements) of a [rows, heads, D] tensor whose rows are contiguous."""
+    step, head_step, unit = t.stride()
+    if (unit != 1 and D > 1) or (head_step != D and heads > 1):
+        raise ValueError("the heads of a row must be contiguous")
+    return step if rows > 1 else heads * D
+
+
 def _require_i32(*ts):
     for t in ts:
         if t.dtype != torch.int32:
@@ -483,45 +512,52 @@ def ts_kv_append_chunk_rope(q, k_new, v_new, k_pool, v_pool, block_table, seq_le
     ts_attn.h). ``inv_freq`` (float32, radians per position) has one entry per rotated pair.
     Rows may be a part of wider rows. Returns the queries, in ``q_out`` (which may be ``q``)."""
     B = _require_chunks(seq_lens, q_indptr, block_table)
-    T, H_q, D = q.shape
-    if not q.dtype == k_new.dtype == k_pool.dtype == v_pool.dtype:
+    q_shape, new_shape, pool_shape = q.shape, k_new.shape, k_pool.shape
+    T, H_q, D = q_shape
+    P, ps, H_kv, D_pool = pool_shape
+    dtype = q.dtype
+    if k_new.dtype != dtype or v_new.dtype != dtype or k_pool.dtype != dtype or v_pool.dtype != dtype:
         raise TypeError("queries, new rows and pools must have one dtype")
-    k, v, step = _chunk_rows(k_new, v_new, k_pool, v_pool)
-    P, ps, H_kv, D_pool = k_pool.shape
-    if D != D_pool or T != k_new.shape[0]:
-        raise ValueError("q must be [T, H_q, D] with the new rows' T and D")
+    if v_pool.shape != pool_shape or D != D_pool or new_shape != (T, H_kv, D) or v_new.shape != new_shape:
+        raise ValueError("q must be [T, H_q, D], new rows [T, H_kv, D], pools [num_pages, page_size, H_kv, D]")
     for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != q.dtype or w.shape != (D,)):
+        if w is not None and (w.dtype != dtype or w.shape != (D,)):
             raise ValueError("weights must be [D] of the queries' dtype")
     rot = 0
     if inv_freq is not None:
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
             raise TypeError("inv_freq must be float32 [rot_dim / 2]")
-        rot = 2 * inv_freq.shape[0]
-    qp, q_step = _rows(q)
+        rot = 2 * inv_freq.numel()
+    step = _row_step(k_new, T, H_kv, D)
+    if _row_step(v_new, T, H_kv, D) != step:
+        raise ValueError("k_new and v_new rows must be equally far apart")
+    q_step = out_step = _row_step(q, T, H_q, D)
     if q_out is None:
         with _made_for(stream):
-            q_out = torch.empty(T, H_q, D, dtype=q.dtype, device=q.device)
-    if q_out.dtype != q.dtype or q_out.shape != q.shape:
-        raise ValueError("q_out must have the queries' shape and dtype")
-    op, out_step = _rows(q_out)
+            q_out = torch.empty(T, H_q, D, dtype=dtype, device=q.device)
+    if q_out is not q:
+        if q_out.dtype != dtype or q_out.shape != q_shape:
+            raise ValueError("q_out must have the queries' shape and dtype")
+        out_step = _row_step(q_out, T, H_q, D)
     at = k_pool.get_device()
-    if q.get_device() != at or q_out.get_device() != at:
-        raise ValueError("queries and pools must be on one device")
-    kp, vp, bt, lens, ptr, freq, qw, kw = _pointers(k_pool, v_pool, block_table, seq_lens, q_indptr, inv_freq, q_weight,
-                                                    k_weight)
-    _check(lib().ts_kv_append_chunk_rope(qp, q_step, k, v, step, qw, kw, eps, freq, rot, bool(interleaved), kp, vp, bt,
-                                         block_table.shape[1], lens, ptr, T, B, H_q, H_kv, D, ps, P, _dt(q), op,
-                                         out_step, _stream(stream)))
+    if q.get_device() != at or k_new.get_device() != at or v_new.get_device() != at or q_out.get_device() != at:
+        raise ValueError("queries, new rows and pools must be on one device")
+    kp, vp, bt, lens, ptr, freq, qw, kw, on = _marshal(stream, k_pool, v_pool, block_table, seq_lens, q_indptr, inv_freq,
+                                                       q_weight, k_weight)
+    _check(lib().ts_kv_append_chunk_rope(q.data_ptr(), q_step, k_new.data_ptr(), v_new.data_ptr(), step, qw, kw, eps,
+                                         freq, rot, interleaved, kp, vp, bt, block_table.shape[1], lens, ptr, T, B, H_q,
+                                         H_kv, D, ps, P, _dt(q), q_out.data_ptr(), out_step, on))
     return q_out
 
 
 def _require_bounds(bounds, bound_scale, D):
-    """Page bounds int8 [num_pages, H_kv, 2, D] and their scales float32 [num_pages, H_kv]."""
+    """Page bounds int8 [num_pages, H_kv, 2, D] and their scales float32 [num_pages, H_kv]: (num_pages, H_kv)."""
     if bounds.dtype != torch.int8 or bound_scale.dtype != torch.float32:
         raise TypeError("page bounds are int8, their scales float32")
-    if bounds.dim() != 4 or bounds.shape[2] != 2 or bounds.shape[3] != D or bound_scale.shape != bounds.shape[:2]:
+    of = bound_scale.shape
+    if len(of) != 2 or bounds.shape != (*of, 2, D):
         raise ValueError("page bounds must be [num_pages, H_kv, 2, D], their scales [num_pages, H_kv]")
+    return of
 
 
 def ts_kv_page_bounds(k_pool, bounds, bound_scale, block_table, seq_lens, q_indptr, rows: int, stream=None) -> None:
@@ -530,12 +566,11 @@ def ts_kv_page_bounds(k_pool, bounds, bound_scale, block_table, seq_lens, q_indp
     [num_pages, H_kv] (see ts_attn.h). Other pages' bounds stay."""
     B = _require_chunks(seq_lens, q_indptr, block_table)
     P, ps, H_kv, D = k_pool.shape
-    _require_bounds(bounds, bound_scale, D)
-    if bounds.shape[:2] != (P, H_kv):
+    if _require_bounds(bounds, bound_scale, D) != (P, H_kv):
         raise ValueError("page bounds must have the pool's pages and kv heads")
-    kp, bp, sp, bt, lens, ptr = _pointers(k_pool, bounds, bound_scale, block_table, seq_lens, q_indptr)
+    kp, bp, sp, bt, lens, ptr, on = _marshal(stream, k_pool, bounds, bound_scale, block_table, seq_lens, q_indptr)
     _check(lib().ts_kv_page_bounds(kp, bp, sp, bt, block_table.shape[1], lens, ptr, rows, B, H_kv, D, ps, P,
-                                   _dt(k_pool), _stream(stream)))
+                                   _dt(k_pool), on))
 
 
 def ts_select_pages_workspace_size(B: int, q_len: int, H_kv: int, bt_stride: int) -> int:
@@ -549,27 +584,40 @@ def ts_select_pages(q, bounds, bound_scale, block_table, seq_lens, page_size: in
     -1 behind the last; the first ``first`` and last ``last`` pages are always among them
     (see ts_attn.h)."""
     B = _require_chunks(seq_lens, None, block_table)
-    shape = q.shape
-    q_len = 1 if len(shape) == 3 else shape[1]
-    H_q, D = shape[-2:]
-    _require_bounds(bounds, bound_scale, D)
-    P, H_kv = bound_scale.shape
-    if shape[0] != B or len(shape) not in (3, 4):
-        raise ValueError("q must be [B, H_q, D] or [B, q_len, H_q, D]")
-    want = (*shape[:-2], H_kv, pages)
+    rows, q_len, H_q, D = _query_rows(q, B)
+    P, H_kv = _require_bounds(bounds, bound_scale, D)
+    want = (*rows, H_kv, pages)
     if page_idx is None:
         with _made_for(stream):
             page_idx = torch.empty(want, dtype=_INT32, device=q.device)
     elif page_idx.dtype != _INT32 or page_idx.shape != want:
         raise ValueError("page_idx must be int32 [B, (q_len,) H_kv, pages]")
-    qp, bp, sp, bt, lens, ip, wp = _pointers(q, bounds, bound_scale, block_table, seq_lens, page_idx, workspace)
+    qp, bp, sp, bt, lens, ip, wp, on = _marshal(stream, q, bounds, bound_scale, block_table, seq_lens, page_idx,
+                                                workspace)
+    slots = block_table.shape[1]
     if workspace is None:
         with _made_for(stream):
-            workspace = new_workspace(ts_select_pages_workspace_size(B, q_len, H_kv, block_table.shape[1]), q.device)
+            workspace = new_workspace(ts_select_pages_workspace_size(B, q_len, H_kv, slots), q.device)
         wp = workspace.data_ptr()
-    _check(lib().ts_select_pages(qp, bp, sp, bt, block_table.shape[1], lens, B, q_len, H_q, H_kv, D, page_size, P, pages,
-                                 first, last, _dt(q), ip, wp, workspace.nbytes, _stream(stream)))
+    _check(lib().ts_select_pages(qp, bp, sp, bt, slots, lens, B, q_len, H_q, H_kv, D, page_size, P, pages, first, last,
+                                 _dt(q), ip, wp, workspace.nbytes, on))
     return page_idx
+
+
+def _query_rows(q, B):
+    """Leading sizes, q_len, H_q and D of queries [B, H_q, D] or [B, q_len, H_q, D]."""
+    shape = q.shape
+    if len(shape) == 3:
+        n, H_q, D = shape
+        rows, q_len = (n,), 1
+    elif len(shape) == 4:
+        n, q_len, H_q, D = shape
+        rows = (n, q_len)
+    else:
+        n = -1
+    if n != B:
+        raise ValueError("q must be [B, H_q, D] or [B, q_len, H_q, D]")
+    return rows, q_len, H_q, D
 
 
 def ts_paged_decode_sparse_workspace_size(B: int, q_len: int, H_q: int, H_kv: int, D: int, page_size: int,
@@ -584,37 +632,35 @@ def ts_paged_decode_sparse_attn(q, k_pool, v_pool, block_table, seq_lens, page_i
     a sequence, at position ``seq_lens[b] - q_len + j``, attends the listed pages' tokens up to
     itself. Returns ``out`` (and ``lse``)."""
     B = _require_chunks(seq_lens, None, block_table)
-    shape = q.shape
-    q_len = 1 if len(shape) == 3 else shape[1]
-    H_q, D = shape[-2:]
-    P, ps, H_kv, D_pool = k_pool.shape
-    if k_pool.dtype != q.dtype or v_pool.dtype != q.dtype:
+    rows, q_len, H_q, D = _query_rows(q, B)
+    pool_shape, dtype = k_pool.shape, q.dtype
+    P, ps, H_kv, D_pool = pool_shape
+    if k_pool.dtype != dtype or v_pool.dtype != dtype:
         raise TypeError("queries and pools must have one dtype")
-    if k_pool.shape != v_pool.shape or D_pool != D:
+    if v_pool.shape != pool_shape or D_pool != D:
         raise ValueError("pools must be [num_pages, page_size, H_kv, D] with the queries' D")
-    if shape[0] != B or len(shape) not in (3, 4):
-        raise ValueError("q must be [B, H_q, D] or [B, q_len, H_q, D]")
-    pages = page_idx.shape[-1]
-    if page_idx.dtype != _INT32 or page_idx.shape != (*shape[:-2], H_kv, pages):
+    of = page_idx.shape
+    pages = of[-1]
+    if page_idx.dtype != _INT32 or of != (*rows, H_kv, pages):
         raise ValueError("page_idx must be int32 [B, (q_len,) H_kv, pages]")
     if out is None:
         with _made_for(stream):
-            out = torch.empty(shape, dtype=q.dtype, device=q.device)
+            out = torch.empty(*rows, H_q, D, dtype=dtype, device=q.device)
     if lse is None and return_lse:
         with _made_for(stream):
-            lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
-    if out.dtype != q.dtype or out.shape != shape:
+            lse = torch.empty(*rows, H_q, dtype=torch.float32, device=q.device)
+    if out.dtype != dtype or out.shape != (*rows, H_q, D):
         raise ValueError("out must have the queries' shape and dtype")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:-1]):
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (*rows, H_q)):
         raise ValueError("lse must be float32 of the queries' rows and heads")
-    qp, kp, vp, bt, lens, ip, op, lp, wp = _pointers(q, k_pool, v_pool, block_table, seq_lens, page_idx, out, lse,
-                                                     workspace)
+    qp, kp, vp, bt, lens, ip, op, lp, wp, on = _marshal(stream, q, k_pool, v_pool, block_table, seq_lens, page_idx, out,
+                                                        lse, workspace)
     if workspace is None:
         with _made_for(stream):
             workspace = new_workspace(ts_paged_decode_sparse_workspace_size(B, q_len, H_q, H_kv, D, ps, pages), q.device)
         wp = workspace.data_ptr()
     _check(lib().ts_paged_decode_sparse_attn(qp, kp, vp, bt, block_table.shape[1], lens, ip, pages, B, q_len, H_q, H_kv,
-                                             D, ps, P, scale, _dt(q), op, lp, wp, workspace.nbytes, _stream(stream)))
+                                             D, ps, P, scale, _dt(q), op, lp, wp, workspace.nbytes, on))
     return (out, lse) if return_lse else out
 
 
@@ -662,9 +708,9 @@ def ts_kv_fork(buffers, block_table, seq_lens, parents, children, fresh, page_si
     for t in (parents, children, fresh):
         if t.dtype != _INT32 or t.numel() != n:
             raise TypeError("parents, children and fresh must be int32 of one length")
-    bt, lens, pp, cp, fp = _pointers(block_table, seq_lens, parents, children, fresh)
+    bt, lens, pp, cp, fp, on = _marshal(stream, block_table, seq_lens, parents, children, fresh)
     _check(lib().ts_kv_fork(buffers.data, buffers.page_bytes, buffers.count, bt, block_table.shape[1], lens, B, pp, cp,
-                            fp, n, page_size, buffers.num_pages, _stream(stream)))
+                            fp, n, page_size, buffers.num_pages, on))
 
 
 def ts_kv_compact_workspace_size(num_pages: int) -> int:
@@ -679,23 +725,25 @@ def ts_kv_compact(buffers, block_table, seq_lens, page_size: int, table_out=None
     the pages from there on are free. See ts_attn.h."""
     B = _require_chunks(seq_lens, None, block_table)
     buffers = _require_buffers(buffers, block_table)
-    P, device = buffers.num_pages, block_table.device
-    with _made_for(stream):
-        if table_out is None:
-            table_out = torch.empty_like(block_table)
-        if page_map is None:
-            page_map = torch.empty(P, dtype=_INT32, device=device)
-        if used is None:
-            used = torch.empty(1, dtype=_INT32, device=device)
-        if workspace is None:
-            workspace = new_workspace(ts_kv_compact_workspace_size(P), device)
+    P = buffers.num_pages
+    if table_out is None or page_map is None or used is None or workspace is None:
+        device = block_table.device
+        with _made_for(stream):
+            if table_out is None:
+                table_out = torch.empty_like(block_table)
+            if page_map is None:
+                page_map = torch.empty(P, dtype=_INT32, device=device)
+            if used is None:
+                used = torch.empty(1, dtype=_INT32, device=device)
+            if workspace is None:
+                workspace = new_workspace(ts_kv_compact_workspace_size(P), device)
     if table_out.dtype != _INT32 or page_map.dtype != _INT32 or used.dtype != _INT32:
         raise TypeError("tables and page ids must be int32")
     if table_out.shape != block_table.shape or page_map.numel() != P or used.numel() != 1:
         raise ValueError("table_out must be the block table's shape, page_map [num_pages], used [1]")
-    bt, to, lens, mp, up, wp = _pointers(block_table, table_out, seq_lens, page_map, used, workspace)
+    bt, to, lens, mp, up, wp, on = _marshal(stream, block_table, table_out, seq_lens, page_map, used, workspace)
     _check(lib().ts_kv_compact(buffers.data, buffers.page_bytes, buffers.count, bt, to, block_table.shape[1], lens, B,
-                               page_size, P, mp, up, wp, workspace.nbytes, _stream(stream)))
+                               page_size, P, mp, up, wp, workspace.nbytes, on))
     return table_out, page_map, used
 
 

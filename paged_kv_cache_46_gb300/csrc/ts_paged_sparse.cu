@@ -23,8 +23,11 @@
 // time that their 8 KB take to arrive. Both operands of P V are bf16: the weights
 // enter as two terms, rounded weights in the rows of the heads and what the
 // rounding left in the eight rows of padding, so that they count with 16 bits.
-// float32 (sparse_f32_kernel): on the CUDA cores, 16 bytes of a row per lane,
-// four rows of K and V in flight.
+// float32 (sparse_f32_kernel): on the CUDA cores, packed multiply-adds. Tiles of
+// eight tokens, two (D = 64: four) per warp in flight. For the scores a lane takes a
+// key and a quarter of its columns, so that a value of K is read once for the g
+// heads and the sums need two exchanges, not five per head; for P V it takes four
+// columns of all keys, with the weights from shared memory.
 #include "ts_ranges.cuh"
 #include "ts_tcgen05.cuh"
 
@@ -385,13 +388,40 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
 // float32
 // ---------------------------------------------------------------------------
 
+// A stage: 8 rows of K, then of V, in boxes of 32 columns (rows of 128 bytes, 128-byte swizzle). Behind the
+// stages, per warp: the item's queries, a quarter of the columns per 16-byte step in the banks, and the
+// weights and scales of a tile.
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads) sparse_f32_kernel(const SparseParams p) {
+struct F32Smem {
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kOperand = 8 * D * 4, kStage = 2 * kOperand;
+  static constexpr int kPart = D / 4 + 4;  // floats of a quarter of a query, and their padding
+  static constexpr int kQuery = G * 4 * kPart * 4, kWeights = G * 8 * 4;
+  static constexpr int kWarp = kQuery + kWeights + G * 4 + (G < 4 ? 16 - G * 4 : 0);
+  static constexpr int kBytes = kWarps * (kStages * kStage + kWarp);
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 2) sparse_f32_kernel(const __grid_constant__ SparseParams p,
+                                                                 const __grid_constant__ CUtensorMap kmap,
+                                                                 const __grid_constant__ CUtensorMap vmap) {
   pdl_launch_dependents();
-  constexpr int kEach = 4, kLanes = D / kEach, kRows = 32 / kLanes, kAhead = 4;
+  using S = F32Smem<D, G>;
+  constexpr int kStages = S::kStages, kPart = S::kPart;
+  constexpr int kMine = G >= 4 ? G / 4 : 1;  // heads whose scores a lane keeps
+  extern __shared__ __align__(1024) unsigned char ring[];
+  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ int64_t before[kThreads + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % kLanes, sub = lane / kLanes;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t worker = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  if ((smem_u32(ring) & 1023u) != 0u) {
+    if (threadIdx.x == 0) set_device_error(p.err_word, TS_DEVERR_SMEM_ALIGN);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(&bars[0][0] + i), 1);
+    fence_mbar_init();
+  }
   make_plan<kThreads>(p, before);
   const int64_t range = range_of(p, before[kThreads] * p.H_kv);
   Walk w;
@@ -400,110 +430,208 @@ __global__ void __launch_bounds__(kThreads) sparse_f32_kernel(const SparseParams
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= kThreads; i += kThreads) p.plan[i] = before[i];
   if (!any) return;
-  const int64_t step = static_cast<int64_t>(p.H_kv) * D;  // elements between rows
+
+  unsigned char* stages = ring + warp * kStages * S::kStage;
+  unsigned char* own = ring + kWarps * kStages * S::kStage + warp * S::kWarp;
+  float* qs = reinterpret_cast<float*>(own);
+  float* weights = reinterpret_cast<float*>(own + S::kQuery);                 // [G][8]
+  float* scales = reinterpret_cast<float*>(own + S::kQuery + S::kWeights);    // [G]
+  const uint32_t stage0 = smem_u32(stages), bar0 = smem_u32(&bars[warp][0]);
+  // scores: a lane takes one of the eight keys and a quarter of the columns; the heads it keeps follow from it
+  const int key = lane & 7, part = lane >> 3;
+  int mine = 0;
+#pragma unroll
+  for (int n = G / 2, o = 16; n > 0 && o >= 8; n >>= 1, o >>= 1) mine += (lane & o) ? n : 0;
+  // P V: four columns of all keys (D = 64: of the half of the keys), rows of V as K's
+  const int vlane = D == 128 ? lane : lane & 15, vhalf = D == 128 ? 0 : lane >> 4;
+  constexpr int kVRows = D == 128 ? 8 : 4;
+  const int groups = p.page_size >> 3;  // of eight rows, in a page: 1, 2 or 4
+  const int gshift = groups >> 1;       // its logarithm
+  uint32_t stage = 0, parity = 0;       // of the next tile to be waited for
+  bool ok = true;
+
   do {
     const int pos = row_position(p, w.row);
-    float q[G][kEach], acc[G][kEach], m[G], sum[G];
-    const float* qsrc =
-        static_cast<const float*>(p.q) + (static_cast<int64_t>(w.row) * p.H_kv * G + w.h * G) * D + l * kEach;
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      const float4 x = *reinterpret_cast<const float4*>(qsrc + i * D);
-      q[i][0] = x.x * p.scale_log2, q[i][1] = x.y * p.scale_log2;
-      q[i][2] = x.z * p.scale_log2, q[i][3] = x.w * p.scale_log2;
-      m[i] = -INFINITY;
-      sum[i] = 0.f;
-#pragma unroll
-      for (int d = 0; d < kEach; ++d) acc[i][d] = 0.f;
+    {
+      const float* src = static_cast<const float*>(p.q) + (static_cast<int64_t>(w.row) * p.H_kv * G + w.h * G) * D;
+      __syncwarp();  // the item before has read its queries
+      for (int i = lane; i < G * D / 4; i += 32) {
+        const int head = i / (D / 4), d = i % (D / 4) * 4;
+        float4 x = *reinterpret_cast<const float4*>(src + head * D + d);
+        x = make_float4(x.x * p.scale_log2, x.y * p.scale_log2, x.z * p.scale_log2, x.w * p.scale_log2);
+        *reinterpret_cast<float4*>(qs + (head * 4 + d / (D / 4)) * kPart + d % (D / 4)) = x;
+      }
+      __syncwarp();
     }
-    for (int c0 = w.i0; c0 < w.i1; c0 += 32) {
+    float m[kMine], sum[kMine];
+    float2 acc[G][2];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) m[i] = -INFINITY, sum[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < G; ++i) acc[i][0] = acc[i][1] = make_float2(0.f, 0.f);
+
+    for (int c0 = w.i0; c0 < w.i1 && ok; c0 += 32) {
       const Listed e = listed_page(p, w, pos, c0 + lane);
-      for (unsigned todo = __ballot_sync(0xffffffffu, e.tokens > 0); todo; todo &= todo - 1) {
-        const int from = __ffs(todo) - 1;
-        const int64_t page = __shfl_sync(0xffffffffu, e.page, from);
-        const int n = __shfl_sync(0xffffffffu, e.tokens, from);
-        const int64_t base = (page * p.page_size * p.H_kv + w.h) * D + l * kEach;
-        const float* kp = static_cast<const float*>(p.k_pool) + base;
-        const float* vp = static_cast<const float*>(p.v_pool) + base;
-        for (int t0 = sub; t0 - sub < n; t0 += kAhead * kRows) {
-          float4 k[kAhead], v[kAhead];
+      const int tiles = min(32, w.i1 - c0) * groups;
+      // pool row of tile t, and how many of its rows are seen
+      auto tile = [&](int t, int& row) {
+        const int from = t >> gshift, at = (t & (groups - 1)) * 8;
+        row = __shfl_sync(0xffffffffu, e.page, from) * p.page_size + at;
+        return min(8, __shfl_sync(0xffffffffu, e.tokens, from) - at);
+      };
+      auto issue = [&](int t, uint32_t st) {
+        int row;
+        const int n = tile(t, row);
+        if (lane == 0) {
+          const uint32_t bar = bar0 + 8 * st, to = stage0 + st * S::kStage;
+          mbar_arrive_expect_tx(bar, n > 0 ? S::kStage : 0);
+          if (n > 0) {
 #pragma unroll
-          for (int u = 0; u < kAhead; ++u) {
-            const int64_t at = min(t0 + u * kRows, n - 1) * step;
-            k[u] = *reinterpret_cast<const float4*>(kp + at);
-            v[u] = *reinterpret_cast<const float4*>(vp + at);
-          }
-          float s[kAhead][G];
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u) {
-#pragma unroll
-            for (int i = 0; i < G; ++i)
-              s[u][i] = fmaf(q[i][3], k[u].w, fmaf(q[i][2], k[u].z, fmaf(q[i][1], k[u].y, q[i][0] * k[u].x)));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1)
-#pragma unroll
-              for (int i = 0; i < G; ++i) s[u][i] += __shfl_xor_sync(0xffffffffu, s[u][i], o);
-            if (t0 + u * kRows >= n) {
-#pragma unroll
-              for (int i = 0; i < G; ++i) s[u][i] = -INFINITY;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < G; ++i) {
-            float top = m[i];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) top = fmaxf(top, s[u][i]);
-            const float ref = top == -INFINITY ? 0.f : top;
-            const float scale = fast_exp2(m[i] - ref);
-            m[i] = top;
-            sum[i] *= scale;
-#pragma unroll
-            for (int j = 0; j < kEach; ++j) acc[i][j] *= scale;
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-              s[u][i] = fast_exp2(s[u][i] - ref);
-              sum[i] += s[u][i];
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u) {
-            if (t0 + u * kRows >= n) continue;  // (what such rows hold must not count, not even NaN)
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-              acc[i][0] = fmaf(s[u][i], v[u].x, acc[i][0]);
-              acc[i][1] = fmaf(s[u][i], v[u].y, acc[i][1]);
-              acc[i][2] = fmaf(s[u][i], v[u].z, acc[i][2]);
-              acc[i][3] = fmaf(s[u][i], v[u].w, acc[i][3]);
+            for (int x = 0; x < D / 32; ++x) {
+              tma_load_3d(to + x * 1024, &kmap, 32 * x, w.h, row, bar);
+              tma_load_3d(to + S::kOperand + x * 1024, &vmap, 32 * x, w.h, row, bar);
             }
           }
         }
+        __syncwarp();
+      };
+      uint32_t put = stage;
+      for (int t = 0; t < kStages && t < tiles; ++t) {
+        issue(t, put);
+        put = put + 1 == kStages ? 0 : put + 1;
+      }
+      for (int t = 0; t < tiles; ++t) {
+        int row;
+        const int n = tile(t, row);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8 * stage, parity));
+        if (!ok) {  // leave, but not with copies in flight
+          for (int i = t; i < tiles && i < t + kStages; ++i) {
+            mbar_wait(bar0 + 8 * stage, parity);
+            if (++stage == kStages) stage = 0, parity ^= 1u;
+          }
+          break;
+        }
+        if (n > 0) {
+          const unsigned char* ks = stages + stage * S::kStage;
+          const unsigned char* vs = ks + S::kOperand;
+          // a quarter of the columns of this lane's key
+          constexpr int kChunks = D / 16;  // of four columns
+          const unsigned char* krow = ks + (D == 128 ? part : part >> 1) * 1024 + key * 128;
+          const int chunk0 = D == 128 ? 0 : (part & 1) * 4;
+          float2 two[G];
+#pragma unroll
+          for (int i = 0; i < G; ++i) two[i] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            const float4 x = *reinterpret_cast<const float4*>(krow + (((chunk0 + c) ^ key) << 4));
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+              const float4 y = *reinterpret_cast<const float4*>(qs + (i * 4 + part) * kPart + 4 * c);
+              two[i] = __ffma2_rn(make_float2(x.x, x.y), make_float2(y.x, y.y), two[i]);
+              two[i] = __ffma2_rn(make_float2(x.z, x.w), make_float2(y.z, y.w), two[i]);
+            }
+          }
+          float s[G];
+#pragma unroll
+          for (int i = 0; i < G; ++i) s[i] = two[i].x + two[i].y;
+          int o = 16;
+#pragma unroll
+          for (int k = G / 2; k > 0 && o >= 8; k >>= 1, o >>= 1) {
+            const bool upper = (lane & o) != 0;
+#pragma unroll
+            for (int i = 0; i < k; ++i) {
+              const float send = upper ? s[i] : s[i + k];
+              s[i] = (upper ? s[i + k] : s[i]) + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+          }
+#pragma unroll
+          for (; o >= 8; o >>= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+          bool rises = false;
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            if (key >= n) s[i] = -INFINITY;
+            float top = s[i];
+#pragma unroll
+            for (int x = 4; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            float scale = 1.f;
+            if (top > m[i]) {
+              scale = fast_exp2(m[i] - top);
+              m[i] = top;
+              sum[i] *= scale;
+              rises = true;
+            }
+            const float weight = fast_exp2(s[i] - (m[i] == -INFINITY ? 0.f : m[i]));
+            sum[i] += weight;
+            weights[(mine + i) * 8 + key] = weight;
+            if (key == 0) scales[mine + i] = scale;
+          }
+          rises = __any_sync(0xffffffffu, rises);
+          __syncwarp();
+          if (rises) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+              const float scale = scales[i];
+              acc[i][0] = make_float2(acc[i][0].x * scale, acc[i][0].y * scale);
+              acc[i][1] = make_float2(acc[i][1].x * scale, acc[i][1].y * scale);
+            }
+          }
+          const unsigned char* vcol = vs + (vlane >> 3) * 1024;
+#pragma unroll
+          for (int k4 = 0; k4 < kVRows; k4 += 4) {
+            const int first = vhalf * 4 + k4;
+            float4 pw[G];
+#pragma unroll
+            for (int i = 0; i < G; ++i) pw[i] = *reinterpret_cast<const float4*>(weights + i * 8 + first);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = first + k;
+              if (r >= n) continue;  // (what such rows hold must not count, not even NaN)
+              const float4 v = *reinterpret_cast<const float4*>(vcol + r * 128 + (((vlane & 7) ^ r) << 4));
+#pragma unroll
+              for (int i = 0; i < G; ++i) {
+                const float x = k == 0 ? pw[i].x : k == 1 ? pw[i].y : k == 2 ? pw[i].z : pw[i].w;
+                acc[i][0] = __ffma2_rn(make_float2(x, x), make_float2(v.x, v.y), acc[i][0]);
+                acc[i][1] = __ffma2_rn(make_float2(x, x), make_float2(v.z, v.w), acc[i][1]);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (t + kStages < tiles) issue(t + kStages, stage);
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1u;
+        }
       }
     }
-    // joined over the groups of lanes
+    if (!ok) break;
+    // sums over the keys, to all lanes
 #pragma unroll
-    for (int o = 16; o >= kLanes; o >>= 1) {
+    for (int i = 0; i < kMine; ++i) {
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m[i], o), top = fmaxf(m[i], m2);
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float a = fast_exp2(m[i] - ref), c = fast_exp2(m2 - ref);
-        m[i] = top;
-        sum[i] = a * sum[i] + c * __shfl_xor_sync(0xffffffffu, sum[i], o);
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) acc[i][j] = a * acc[i][j] + c * __shfl_xor_sync(0xffffffffu, acc[i][j], o);
-      }
+      for (int x = 4; x > 0; x >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], x);
+      if (key == 0) weights[mine + i] = sum[i], scales[mine + i] = m[i];
     }
-    if (sub == 0) {
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        const Target<float, D> to(p, w, worker, G, i);
-        const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];  // (NaN stays NaN)
-        to.put(l * kEach, acc[i][0] * inv, acc[i][1] * inv);
-        to.put(l * kEach + 2, acc[i][2] * inv, acc[i][3] * inv);
-        if (l == 0) to.put_lse(sum[i] == 0.f ? -INFINITY : (m[i] == -INFINITY ? 0.f : m[i]) + log2f(sum[i]));
+    for (int i = 0; i < G; ++i) {
+      const float total = weights[i], top = scales[i];
+      const Target<float, D> to(p, w, worker, G, i);
+      float x[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
+      if (D == 64) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] += __shfl_xor_sync(0xffffffffu, x[j], 16);
       }
+      const float inv = total == 0.f ? 0.f : 1.f / total;  // (NaN stays NaN)
+      if (vhalf == 0) {
+        to.put(4 * vlane, x[0] * inv, x[1] * inv);
+        to.put(4 * vlane + 2, x[2] * inv, x[3] * inv);
+      }
+      if (lane == 0) to.put_lse(total == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) + log2f(total));
     }
+    __syncwarp();  // before the next item's weights
   } while (w.next(p));
+  if (!ok && lane == 0) set_device_error(p.err_word, TS_DEVERR_TIMEOUT);
 }
 
 // ---------------------------------------------------------------------------
@@ -611,48 +739,50 @@ cudaError_t launch_pdl(K kern, unsigned grid, int threads, size_t smem, cudaStre
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// 3-D map over a pool [rows][H_kv][D] bf16 with a box of 64 columns of one kv head's
-// `rows` rows, 128-byte swizzle.
-ts_status make_pool_map(CUtensorMap* map, const void* pool, int64_t pool_rows, int H_kv, int D, int rows) {
+// 3-D map over a pool [rows][H_kv][D] of es-byte values with a box of 128 bytes of one
+// kv head's `rows` rows, 128-byte swizzle.
+ts_status make_pool_map(CUtensorMap* map, const void* pool, int64_t pool_rows, int H_kv, int D, int es, int rows) {
   auto fn = tensor_map_encoder();
   if (!fn) return fail(TS_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H_kv),
                               static_cast<cuuint64_t>(pool_rows)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(H_kv) * D * 2};
-  const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(rows)}, ones[3] = {1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, ones,
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * es, static_cast<cuuint64_t>(H_kv) * D * es};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), 1, static_cast<cuuint32_t>(rows)}, ones[3] = {1, 1, 1};
+  const CUresult r = fn(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(pool), dims, strides, box, ones,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(TS_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
   return TS_OK;
 }
 
-template <int D>
-ts_status prepare_mma(const void* kernel) {
-  return cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MmaSmem<D>::kBytes),
+template <int kBytes>
+ts_status prepare_ring(const void* kernel) {
+  return cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes),
                     "ts_paged_decode_sparse_attn: shared memory");
 }
 
 template <typename T, int D, int G>
 ts_status launch(const SparseParams& p, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(p.warps / kWarps);
-  const char* what = "ts_paged_decode_sparse_attn: launch";
-  ts_status st;
-  if constexpr (sizeof(T) == 2) {
-    const auto kern = sparse_mma_kernel<D, G>;
-    st = prepare_once(reinterpret_cast<const void*>(kern), prepare_mma<D>);
-    if (st != TS_OK) return st;
-    CUtensorMap kmap, vmap;
-    const int64_t pool_rows = static_cast<int64_t>(p.num_pages) * p.page_size;
-    const int box = p.page_size < 16 ? p.page_size : 16;
-    st = make_pool_map(&kmap, p.k_pool, pool_rows, p.H_kv, D, box);
-    if (st == TS_OK) st = make_pool_map(&vmap, p.v_pool, pool_rows, p.H_kv, D, box);
-    if (st != TS_OK) return st;
-    LaunchTrace trace("sparse_mma_kernel", s);
-    st = cuda_check(launch_pdl(kern, grid, kThreads, MmaSmem<D>::kBytes, s, p, kmap, vmap), what);
-  } else {
-    LaunchTrace trace("sparse_f32_kernel", s);
-    st = cuda_check(launch_pdl(sparse_f32_kernel<D, G>, grid, kThreads, 0, s, p), what);
+  constexpr bool kBf16 = sizeof(T) == 2;
+  constexpr int kBytes = kBf16 ? MmaSmem<D>::kBytes : F32Smem<D, G>::kBytes;
+  const auto kern = [] {
+    if constexpr (kBf16)
+      return sparse_mma_kernel<D, G>;
+    else
+      return sparse_f32_kernel<D, G>;
+  }();
+  ts_status st = prepare_once(reinterpret_cast<const void*>(kern), prepare_ring<kBytes>);
+  if (st != TS_OK) return st;
+  CUtensorMap kmap, vmap;
+  const int64_t pool_rows = static_cast<int64_t>(p.num_pages) * p.page_size;
+  const int box = kBf16 && p.page_size >= 16 ? 16 : 8;
+  st = make_pool_map(&kmap, p.k_pool, pool_rows, p.H_kv, D, sizeof(T), box);
+  if (st == TS_OK) st = make_pool_map(&vmap, p.v_pool, pool_rows, p.H_kv, D, sizeof(T), box);
+  if (st != TS_OK) return st;
+  {
+    LaunchTrace trace(kBf16 ? "sparse_mma_kernel" : "sparse_f32_kernel", s);
+    st = cuda_check(launch_pdl(kern, static_cast<unsigned>(p.warps / kWarps), kThreads, kBytes, s, p, kmap, vmap),
+                    "ts_paged_decode_sparse_attn: launch");
   }
   if (st != TS_OK) return st;
   LaunchTrace trace("sparse_merge_kernel", s);

@@ -30,6 +30,7 @@
 #include "ts_ragged.cuh"
 
 #include <cmath>
+#include <type_traits>
 
 namespace ts {
 namespace {
@@ -102,13 +103,14 @@ __device__ __forceinline__ float2 turn(int pos, unsigned long long step) {
   return make_float2((quarter + 1u) & 2u ? -u : u, quarter & 2u ? -v : v);
 }
 
-template <typename T, int D, bool kInterleaved>
-__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 2) rope_append_kernel(const RopeParams<T> p) {
+template <typename T, int D, bool kInterleaved, bool kMixed>
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3) rope_append_kernel(const RopeParams<T> p) {
   // Programmatic dependent launch as in ts_kv_append.
   pdl_wait_primary();
   pdl_launch_dependents();
   constexpr int kLanes = D / 8, kVecs = 32 / kLanes;
   __shared__ unsigned long long steps[D / 2];
+  __shared__ float2 angles[kWarps][D / 2];  // cosine and sine of each warp's row
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t r = w / static_cast<uint32_t>(p.parts);
@@ -118,36 +120,57 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 2) rope_appe
   const bool split = turns && !kInterleaved;
   const int oa = split ? 4 * l : 8 * l, ob = split ? p.rot / 2 + 4 * l : 8 * l + 4;
 
-  // Sections: the row's queries, keys, values; this warp takes every parts-th step of them in order.
-  int section = 0, s = part, heads = p.H_q;
-  const T* src = p.q + r * p.q_stride;
-  auto steps_of = [](int n) { return (n + kVecs - 1) / kVecs; };
-  // From a section's end to the first step of the next that is this warp's; false behind the last one.
-  auto settle = [&]() {
-    for (int n = steps_of(heads); s >= n; n = steps_of(heads)) {
-      while (s - p.parts >= n) s -= p.parts;  // (the last batch may have passed the end by some steps)
-      s -= n;
-      if (++section > 2) return false;
-      heads = p.H_kv;
-      src = (section == 1 ? p.k_new : p.v_new) + r * p.new_stride;
-    }
-    return true;
+  // Steps of kVecs heads: the row's queries, its keys, its values; this warp takes every parts-th of them in order.
+  const int q_steps = (p.H_q + kVecs - 1) / kVecs, kv_steps = (p.H_kv + kVecs - 1) / kVecs;
+  const int all_steps = q_steps + 2 * kv_steps;
+  // 0: queries, 1: keys, 2: values; and the section's first step, rows and heads
+  auto section_of = [&](int g) { return g < q_steps ? 0 : g < q_steps + kv_steps ? 1 : 2; };
+  auto first_of = [&](int section) { return section == 0 ? 0 : section == 1 ? q_steps : q_steps + kv_steps; };
+  auto source_of = [&](int section) {
+    return section == 0 ? p.q + r * p.q_stride : (section == 1 ? p.k_new : p.v_new) + r * p.new_stride;
   };
   Quad<T> xa[kBatch], xb[kBatch];
+  auto load_step = [&](int u, const T* src, int h, int heads) {
+    if (h < heads) {
+      xa[u].load(src + h * D + oa);
+      xb[u].load(src + h * D + ob);
+    } else {
+      xa[u] = {};
+      xb[u] = {};
+    }
+  };
+  // Mixed batches are of any steps. Others end with their section: section, its next step, heads and rows.
+  int section = 0, g = part, heads = p.H_q;
+  const T* src = p.q + r * p.q_stride;
+  // From a section's end to the first step of the next that is this warp's; false behind the last one.
+  auto settle = [&]() {
+    if constexpr (kMixed) {
+      return g < all_steps;
+    } else {
+      for (int n = section == 0 ? q_steps : kv_steps; g >= n; n = kv_steps) {
+        while (g - p.parts >= n) g -= p.parts;  // (the last batch may have passed the end by some steps)
+        g -= n;
+        if (++section > 2) return false;
+        heads = p.H_kv;
+        src = source_of(section);
+      }
+      return true;
+    }
+  };
   auto load = [&]() {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int h = (s + u * p.parts) * kVecs + vec;
-      if (h < heads) {
-        xa[u].load(src + h * D + oa);
-        xb[u].load(src + h * D + ob);
+      const int step = g + u * p.parts;
+      if constexpr (kMixed) {
+        const int of = section_of(step);
+        load_step(u, source_of(of), (step - first_of(of)) * kVecs + vec,
+                  step >= all_steps ? 0 : of == 0 ? p.H_q : p.H_kv);
       } else {
-        xa[u] = {};
-        xb[u] = {};
+        load_step(u, src, step * kVecs + vec, heads);
       }
     }
   };
-  bool any = r < p.T_rows && settle();
+  const bool any = r < p.T_rows && settle();
   if (any) load();
   for (int i = threadIdx.x; i < p.rot / 2; i += kWarps * 32) steps[i] = turns_per_position(p.inv_freq[i]);
   __syncthreads();
@@ -159,25 +182,21 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 2) rope_appe
   const int64_t row = pool_row(p.block_table, p.bt_stride, b, pos, p.page_size, p.num_pages);
 
   // pair 4 l + i of the lane, i < 4: each of the kVecs lanes that share them computes 4 / kVecs
-  float2 cs[4];
-  {
+  float2* turned = angles[threadIdx.x >> 5];
+  if (turns) {
     constexpr int kOwn = 4 / kVecs;
-    float2 own[kOwn];
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i)
-      own[i] = turns ? turn(pos, steps[4 * l + vec * kOwn + i]) : make_float2(1.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int from = i / kOwn * kLanes + l;
-      cs[i].x = __shfl_sync(0xffffffffu, own[i % kOwn].x, from);
-      cs[i].y = __shfl_sync(0xffffffffu, own[i % kOwn].y, from);
-    }
+    for (int i = 0; i < kOwn; ++i) turned[4 * l + vec * kOwn + i] = turn(pos, steps[4 * l + vec * kOwn + i]);
   }
+  __syncwarp();
 
   // Factors of the columns a[0 .. 3], c[0 .. 3] and of their partners, two columns each.
   float2 P[4], Q[4];
   auto factors = [&](const T* weight) {
     float a[4] = {1.f, 1.f, 1.f, 1.f}, c[4] = {1.f, 1.f, 1.f, 1.f};
+    float2 cs[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cs[i] = turns ? turned[4 * l + i] : make_float2(1.f, 0.f);
     if (weight != nullptr) {
       Quad<T> q;
       q.load(weight + oa);
@@ -204,58 +223,71 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 2) rope_appe
     }
   };
   int made = -1;  // section that P and Q are of
+  auto finish_step = [&](int u, int section, const T* weight, T* dst, int h, int heads) {
+    if (section < 2 && (weight != nullptr || p.rot > 0)) {
+      if (made != section) {
+        factors(weight);
+        made = section;
+      }
+      float a[4], c[4];
+      xa[u].get(a);
+      xb[u].get(c);
+      const float2 x[4] = {{a[0], a[1]}, {a[2], a[3]}, {c[0], c[1]}, {c[2], c[3]}};
+      float2 y[4];
+      float2 inv = make_float2(1.f, 1.f);
+      if (weight != nullptr) {
+        float2 two = __fmul2_rn(x[0], x[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) two = __ffma2_rn(x[i], x[i], two);
+        float ss = two.x + two.y;
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        inv.x = inv.y = rsqrtf(ss * (1.f / D) + p.eps);
+      }
+      if (turns) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 partner = kInterleaved ? make_float2(x[i].y, x[i].x) : x[i ^ 2];
+          y[i] = __fmul2_rn(__ffma2_rn(x[i], P[i], __fmul2_rn(partner, Q[i])), inv);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(__fmul2_rn(x[i], P[i]), inv);
+      }
+      if (turns || weight != nullptr) {  // columns that nothing touches stay as they are, bit for bit
+        const float ya[4] = {y[0].x, y[0].y, y[1].x, y[1].y}, yc[4] = {y[2].x, y[2].y, y[3].x, y[3].y};
+        xa[u].set(ya);
+        xb[u].set(yc);
+      }
+    }
+    if (h < heads) {
+      xa[u].store(dst + h * D + oa);
+      xb[u].store(dst + h * D + ob);
+    }
+  };
+  auto weight_of = [&](int section) { return section == 0 ? p.q_weight : section == 1 ? p.k_weight : nullptr; };
+  auto target_of = [&](int section) {
+    return section == 0 ? p.q_out + r * p.q_out_stride : (section == 1 ? p.k_pool : p.v_pool) + row * p.H_kv * D;
+  };
+  const int kv_heads = row >= 0 ? p.H_kv : 0;  // that are stored
   for (;;) {
-    const T* weight = section == 0 ? p.q_weight : section == 1 ? p.k_weight : nullptr;
-    T* dst = section == 0   ? p.q_out + r * p.q_out_stride
-             : section == 1 ? p.k_pool + row * p.H_kv * D
-                            : p.v_pool + row * p.H_kv * D;
-    const bool stored = section == 0 || row >= 0;
-    const bool changes = section < 2 && (weight != nullptr || p.rot > 0);
-    if (changes && made != section) {
-      factors(weight);
-      made = section;
-    }
+    if constexpr (kMixed) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int h = (s + u * p.parts) * kVecs + vec;
-      if (changes) {
-        float a[4], c[4];
-        xa[u].get(a);
-        xb[u].get(c);
-        const float2 x[4] = {{a[0], a[1]}, {a[2], a[3]}, {c[0], c[1]}, {c[2], c[3]}};
-        float2 y[4];
-        float2 inv = make_float2(1.f, 1.f);
-        if (weight != nullptr) {
-          float2 two = __fmul2_rn(x[0], x[0]);
-#pragma unroll
-          for (int i = 1; i < 4; ++i) two = __ffma2_rn(x[i], x[i], two);
-          float ss = two.x + two.y;
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          inv.x = inv.y = rsqrtf(ss * (1.f / D) + p.eps);
-        }
-        if (turns) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 partner = kInterleaved ? make_float2(x[i].y, x[i].x) : x[i ^ 2];
-            y[i] = __fmul2_rn(__ffma2_rn(x[i], P[i], __fmul2_rn(partner, Q[i])), inv);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(__fmul2_rn(x[i], P[i]), inv);
-        }
-        if (turns || weight != nullptr) {  // columns that nothing touches stay as they are, bit for bit
-          const float ya[4] = {y[0].x, y[0].y, y[1].x, y[1].y}, yc[4] = {y[2].x, y[2].y, y[3].x, y[3].y};
-          xa[u].set(ya);
-          xb[u].set(yc);
-        }
+      for (int u = 0; u < kBatch; ++u) {
+        const int step = g + u * p.parts, of = section_of(step);
+        if (step < all_steps)
+          finish_step(u, of, weight_of(of), target_of(of), (step - first_of(of)) * kVecs + vec,
+                      of == 0 ? p.H_q : kv_heads);
       }
-      if (h < heads && stored) {
-        xa[u].store(dst + h * D + oa);
-        xb[u].store(dst + h * D + ob);
-      }
+    } else {
+      const T* weight = weight_of(section);
+      T* dst = target_of(section);
+      const int stored = section == 0 ? p.H_q : kv_heads;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        finish_step(u, section, weight, dst, (g + u * p.parts) * kVecs + vec, stored);
     }
-    s += kBatch * p.parts;
+    g += kBatch * p.parts;
     if (!settle()) return;
     load();
   }
@@ -268,7 +300,7 @@ ts_status launch(int D, const void* q, const void* k_new, const void* v_new, con
   p.q = static_cast<const T*>(q), p.k_new = static_cast<const T*>(k_new), p.v_new = static_cast<const T*>(v_new);
   p.q_weight = static_cast<const T*>(q_weight), p.k_weight = static_cast<const T*>(k_weight);
   p.k_pool = static_cast<T*>(k_pool), p.v_pool = static_cast<T*>(v_pool), p.q_out = static_cast<T*>(q_out);
-  const int steps = (p.H_q + 2 * p.H_kv + 256 / D - 1) / (256 / D);
+  const int vecs = 256 / D, steps = (p.H_q + vecs - 1) / vecs + 2 * ((p.H_kv + vecs - 1) / vecs);
   // shares of a row: enough warps to fill the device twice over, each with a step at least
   const int64_t want = static_cast<int64_t>(device_sm_count()) * 64;
   p.parts = static_cast<int32_t>(want / p.T_rows);
@@ -283,8 +315,16 @@ ts_status launch(int D, const void* q, const void* k_new, const void* v_new, con
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kern = D == 64 ? (p.interleaved ? rope_append_kernel<T, 64, true> : rope_append_kernel<T, 64, false>)
-                      : (p.interleaved ? rope_append_kernel<T, 128, true> : rope_append_kernel<T, 128, false>);
+  // A row of few steps is taken in batches that mix queries, keys and values: fewer waits one after another.
+  const bool mixed = steps <= 3 * kBatch;
+  auto pick = [&](auto interleaved, auto mix) {
+    return D == 64 ? rope_append_kernel<T, 64, decltype(interleaved)::value, decltype(mix)::value>
+                   : rope_append_kernel<T, 128, decltype(interleaved)::value, decltype(mix)::value>;
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  auto kern = p.interleaved ? (mixed ? pick(Yes(), Yes()) : pick(Yes(), No()))
+                            : (mixed ? pick(No(), Yes()) : pick(No(), No()));
   LaunchTrace trace("rope_append_kernel", stream);
   return cuda_check(cudaLaunchKernelEx(&cfg, kern, p), "ts_kv_append_chunk_rope: launch");
 }

@@ -38,7 +38,6 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kParts = 32;         // ranges that an item is cut into at most, and one more at its end
-constexpr int kMergeThreads = 512;
 constexpr float kLog2eS = 1.4426950408889634f;
 constexpr float kLn2S = 0.6931471805599453f;
 
@@ -639,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_f32_kernel(const __grid_co
 // Joins the states of items that were cut, and writes the rows that see nothing. A
 // CTA per query row and kv head; g D / 4 threads hold four columns each, as often
 // as they fit, and share the states.
-template <typename T, int D, int G>
+template <typename T, int D, int G, int kMergeThreads>
 __global__ void __launch_bounds__(kMergeThreads) sparse_merge_kernel(const SparseParams p) {
   constexpr int kCols = G * D / 4, kShares = kMergeThreads / kCols;
   __shared__ int32_t warp_sum[kMergeThreads / 32];
@@ -785,9 +784,16 @@ ts_status launch(const SparseParams& p, cudaStream_t s) {
                     "ts_paged_decode_sparse_attn: launch");
   }
   if (st != TS_OK) return st;
+  // Items that fill the device are cut into few parts each: small CTAs, so that all are resident at once (512
+  // items of 4 x 128: the call 90 us, with 512 threads 93). Few items are cut into many parts, which more
+  // threads share. (Joined in the first kernel by the last warp to arrive, the call takes 94 us, and one of 2
+  // items 16.0 instead of 8.0: the fences and atomics in a row take longer than a launch that waits early.)
+  const int64_t items = static_cast<int64_t>(p.rows) * p.H_kv;
+  constexpr int kSmall = G * D / 4 < 128 ? 128 : G * D / 4;
   LaunchTrace trace("sparse_merge_kernel", s);
-  return cuda_check(launch_pdl(sparse_merge_kernel<T, D, G>, static_cast<unsigned>(p.rows * p.H_kv), kMergeThreads, 0,
-                               s, p),
+  const unsigned grid = static_cast<unsigned>(items);
+  return cuda_check(items * 4 >= p.warps ? launch_pdl(sparse_merge_kernel<T, D, G, kSmall>, grid, kSmall, 0, s, p)
+                                         : launch_pdl(sparse_merge_kernel<T, D, G, 512>, grid, 512, 0, s, p),
                     "ts_paged_decode_sparse_attn: merge launch");
 }
 

@@ -39,9 +39,11 @@
  *     append and paged-attention kernels may start while the previous kernel
  *     of the stream is still running, if that kernel allows it (a kernel that
  *     does not use programmatic dependent launch never does). Before waiting
- *     for it, ts_paged_decode_attn reads only seq_lens, the block table and,
+ *     for it, ts_paged_decode_attn, ts_select_pages and
+ *     ts_paged_decode_sparse_attn read only seq_lens, the block table and,
  *     in cascade mode, the group descriptors; so a kernel that triggers its
- *     dependents early must not write those. Every other input is read, and
+ *     dependents early must not write those (ts_kv_fork and ts_kv_compact,
+ *     which write them, do not). Every other input is read, and
  *     every output written, after the wait. The library's own kernels follow
  *     this rule, so back-to-back calls are safe.
  */
@@ -503,7 +505,7 @@ TS_API size_t ts_select_pages_workspace_size(int32_t B, int32_t q_len, int32_t H
  *              bytes, 256-byte aligned, the error word in front
  * Pages past the block table's row do not take part (TS_DEVERR_PAGE_RANGE).
  * Supported: D in {64, 128}, H_q / H_kv and H_kv in {1, 2, 4, 8}, any page_size,
- * up to 65,535 query rows. B == 0 returns TS_OK with nothing enqueued.
+ * up to 2^24 query rows. B == 0 returns TS_OK with nothing enqueued.
  */
 TS_API ts_status ts_select_pages(const void* q, const int8_t* bounds, const float* bound_scale,
                                  const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,

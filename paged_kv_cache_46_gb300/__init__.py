@@ -545,7 +545,7 @@ def ts_kv_append_chunk_rope(q, k_new, v_new, k_pool, v_pool, block_table, seq_le
     kp, vp, bt, lens, ptr, freq, qw, kw, on = _marshal(stream, k_pool, v_pool, block_table, seq_lens, q_indptr, inv_freq,
                                                        q_weight, k_weight)
     _check(lib().ts_kv_append_chunk_rope(q.data_ptr(), q_step, k_new.data_ptr(), v_new.data_ptr(), step, qw, kw, eps,
-                                         freq, rot, interleaved, kp, vp, bt, block_table.shape[1], lens, ptr, T, B, H_q,
+                                         freq, rot, bool(interleaved), kp, vp, bt, block_table.shape[1], lens, ptr, T, B, H_q,
                                          H_kv, D, ps, P, _dt(q), q_out.data_ptr(), out_step, on))
     return q_out
 

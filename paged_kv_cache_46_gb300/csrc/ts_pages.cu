@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kThreads) kv_fork_kernel(const __grid_constant
   if (piece == 0 && p.tables) {
     for (int s = threadIdx.x; s < slots; s += kThreads) to[s] = cut && s == slots - 1 ? dst : from[s];
     if (threadIdx.x == 0) p.seq_lens[child] = L;
+    __threadfence();  // seen by a kernel that reads tables and lengths before it waits for this one
   }
 }
 
@@ -247,6 +248,7 @@ __global__ void __launch_bounds__(kThreads) page_move_kernel(const __grid_consta
       p.table_out[i] = holds(p, i) && page >= 0 && page < p.num_pages ? moved_to(p, page, U, kept) : page;
     }
     if (i0 == 0) p.used[0] = U;
+    __threadfence();  // seen by a kernel that reads the table before it waits for this one
   }
   const int64_t todo = static_cast<int64_t>(p.counts[2]) * pieces;
   for (int64_t u = blockIdx.x; u < todo; u += gridDim.x)
@@ -325,13 +327,17 @@ extern "C" ts_status ts_kv_fork(void* const* buffers, const int64_t* page_bytes,
   if (n == 0 || B == 0) return TS_OK;
   if (!block_table || !seq_lens || !parents || !children || !fresh)
     return fail(TS_ERR_INVALID_ARG, "%s: null pointer", who);
+  for (int32_t at = 0; at < n_buffers; at += kMaxBuffers) {
+    Buffers b;
+    if (take_buffers(b, buffers, page_bytes, at, n_buffers) * n > 0x7fffffff)
+      return fail(TS_ERR_UNSUPPORTED, "%s: more than 2^31 pieces to copy", who);
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ForkParams p{block_table, seq_lens, parents, children, fresh, bt_stride, B, page_size, num_pages, 1};
   for (int32_t at = 0; at == 0 || at < n_buffers; at += kMaxBuffers, p.tables = 0) {
     Buffers b;
     int64_t pieces = take_buffers(b, buffers, page_bytes, at, n_buffers);
     if (pieces == 0) pieces = 1;
-    if (pieces * n > 0x7fffffff) return fail(TS_ERR_UNSUPPORTED, "%s: more than 2^31 pieces to copy", who);
     LaunchTrace trace("kv_fork_kernel", s);
     const ts_status done = cuda_check(
         launch_pdl(kv_fork_kernel, static_cast<unsigned>(pieces * n), kThreads, s, b, p, pieces), "ts_kv_fork: launch");

@@ -435,7 +435,7 @@ size_t select_bytes(int64_t rows, int H_kv, int bt_stride) {
 }  // namespace ts
 
 extern "C" size_t ts_select_pages_workspace_size(int32_t B, int32_t q_len, int32_t H_kv, int32_t bt_stride) {
-  if (B < 0 || q_len <= 0 || H_kv <= 0 || H_kv > 8 || bt_stride <= 0 || static_cast<int64_t>(B) * q_len > 0x7fffffff)
+  if (B < 0 || q_len <= 0 || H_kv <= 0 || H_kv > 8 || bt_stride <= 0 || static_cast<int64_t>(B) * q_len > (1 << 24))
     return 0;
   return ts::select_bytes(static_cast<int64_t>(B) * q_len, H_kv, bt_stride);
 }
@@ -463,7 +463,7 @@ extern "C" ts_status ts_select_pages(const void* q, const int8_t* bounds, const 
     return fail(TS_ERR_UNSUPPORTED, "%s: H_q=%d H_kv=%d D=%d (H_q / H_kv and H_kv in {1, 2, 4, 8}, D in {64, 128})",
                 who, H_q, H_kv, D);
   const int64_t rows = static_cast<int64_t>(B) * q_len;
-  if (rows > 65535) return fail(TS_ERR_UNSUPPORTED, "%s: more than 65535 query rows", who);
+  if (rows > (1 << 24)) return fail(TS_ERR_UNSUPPORTED, "%s: more than 2^24 query rows", who);
   if (B == 0) return TS_OK;
   if (!q || !bounds || !bound_scale || !block_table || !seq_lens || !page_idx)
     return fail(TS_ERR_INVALID_ARG, "%s: null pointer", who);

@@ -62,7 +62,7 @@ def test_select_pages_refuses_on_the_host(lib):
                 dict(lens=None), dict(q=ctypes.c_void_p(8)), dict(bounds=ctypes.c_void_p(8)),
                 dict(first=2 ** 31 - 1, last=2 ** 31 - 1)):
         assert call(**bad) == INVALID, bad
-    assert call(D=96) == call(H_q=24) == call(H_kv=3, H_q=12) == call(H_kv=16) == call(B=65536) == UNSUPPORTED
+    assert call(D=96) == call(H_q=24) == call(H_kv=3, H_q=12) == call(H_kv=16) == call(B=(1 << 24) + 1) == UNSUPPORTED
     assert call(B=0, q=None, ws=None, wsb=0) == OK
     size = lib.ts_select_pages_workspace_size
     assert size(2, 1, 8, 40) >= 256 + 2 * 8 * 40 * 4
@@ -109,6 +109,8 @@ def test_forks_and_compaction_refuse_on_the_host(lib):
     assert call(n=0, bt=None) == call(B=0, bt=None) == OK
     large = _buffers(1 << 30)
     assert call(data=large[0], size=large[1], nb=1, n=1 << 20) == UNSUPPORTED
+    many = _buffers(*[16] * 200, 1 << 30)  # the last buffers alone are too many pieces: nothing of the call runs
+    assert call(data=many[0], size=many[1], nb=201, n=1 << 20) == UNSUPPORTED
     compact = dict(data=data, size=size, nb=2, bt=VP, out=VP, bts=4, lens=VP, B=4, ps=16, P=8, page_map=VP, used=VP,
                    ws=VP, wsb=1 << 40, stream=None)
     call = lambda **o: _call(lib.ts_kv_compact, compact, **o)  # noqa: E731

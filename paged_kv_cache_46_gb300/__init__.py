@@ -542,11 +542,11 @@ def ts_kv_append_chunk_rope(q, k_new, v_new, k_pool, v_pool, block_table, seq_le
     at = k_pool.get_device()
     if q.get_device() != at or k_new.get_device() != at or v_new.get_device() != at or q_out.get_device() != at:
         raise ValueError("queries, new rows and pools must be on one device")
-    kp, vp, bt, lens, ptr, freq, qw, kw, on = _marshal(stream, k_pool, v_pool, block_table, seq_lens, q_indptr, inv_freq,
-                                                       q_weight, k_weight)
+    kp, vp, bt, lens, ptr, freq, qw, kw, on = _marshal(stream, k_pool, v_pool, block_table, seq_lens, q_indptr,
+                                                       inv_freq, q_weight, k_weight)
     _check(lib().ts_kv_append_chunk_rope(q.data_ptr(), q_step, k_new.data_ptr(), v_new.data_ptr(), step, qw, kw, eps,
-                                         freq, rot, bool(interleaved), kp, vp, bt, block_table.shape[1], lens, ptr, T, B, H_q,
-                                         H_kv, D, ps, P, _dt(q), q_out.data_ptr(), out_step, on))
+                                         freq, rot, bool(interleaved), kp, vp, bt, block_table.shape[1], lens, ptr, T,
+                                         B, H_q, H_kv, D, ps, P, _dt(q), q_out.data_ptr(), out_step, on))
     return q_out
 
 
@@ -657,7 +657,8 @@ def ts_paged_decode_sparse_attn(q, k_pool, v_pool, block_table, seq_lens, page_i
                                                         lse, workspace)
     if workspace is None:
         with _made_for(stream):
-            workspace = new_workspace(ts_paged_decode_sparse_workspace_size(B, q_len, H_q, H_kv, D, ps, pages), q.device)
+            size = ts_paged_decode_sparse_workspace_size(B, q_len, H_q, H_kv, D, ps, pages)
+            workspace = new_workspace(size, q.device)
         wp = workspace.data_ptr()
     _check(lib().ts_paged_decode_sparse_attn(qp, kp, vp, bt, block_table.shape[1], lens, ip, pages, B, q_len, H_q, H_kv,
                                              D, ps, P, scale, _dt(q), op, lp, wp, workspace.nbytes, on))

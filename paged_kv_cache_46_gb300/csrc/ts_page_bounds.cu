@@ -37,7 +37,9 @@ struct Extremes<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) set(top[i], 0xff80ff80u), set(low[i], 0x7f807f80u);  // -inf, +inf
   }
-  __device__ __forceinline__ static void set(__nv_bfloat162& x, uint32_t w) { x = *reinterpret_cast<__nv_bfloat162*>(&w); }
+  __device__ __forceinline__ static void set(__nv_bfloat162& x, uint32_t w) {
+    x = *reinterpret_cast<__nv_bfloat162*>(&w);
+  }
   __device__ __forceinline__ void add(const uint4& w) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -70,8 +72,12 @@ struct Extremes<float> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) top[i] = -INFINITY, low[i] = INFINITY;
   }
-  __device__ __forceinline__ static void max_of(float& x, float y) { asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(y)); }
-  __device__ __forceinline__ static void min_of(float& x, float y) { asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(y)); }
+  __device__ __forceinline__ static void max_of(float& x, float y) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(y));
+  }
+  __device__ __forceinline__ static void min_of(float& x, float y) {
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(y));
+  }
   __device__ __forceinline__ void add(const uint4& w) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll

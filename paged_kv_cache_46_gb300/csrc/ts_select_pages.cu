@@ -89,6 +89,21 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// 16 of a page's bytes of bounds, read once; L2 fetches the rest of them (2 D: 256 or 128 bytes) with the first.
+template <int kBytes>
+__device__ __forceinline__ uint4 load_codes(const uint4* p) {
+  uint4 w;
+  if constexpr (kBytes == 256)
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "l"(p));
+  else
+    asm volatile("ld.global.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "l"(p));
+  return w;
+}
+
 // Bytes that hold four whole numbers below zero, and those that do not.
 __device__ __forceinline__ uint32_t negative_bytes(uint32_t w) { return ((w >> 7) & 0x01010101u) * 0xffu; }
 
@@ -136,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, kResident) page_score_kernel(const T
         const int64_t place = static_cast<int64_t>(good[t][r] ? page[t][r] : 0) * p.H_kv + h;
         const uint4* src = reinterpret_cast<const uint4*>(p.bounds + place * 2 * D) + quarter;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) w[t][r][c] = src[4 * c];
+        for (int c = 0; c < kChunks; ++c) w[t][r][c] = load_codes<2 * D>(src + 4 * c);
         s[t][r] = p.bound_scale[place];
       }
     };
@@ -153,7 +168,8 @@ __global__ void __launch_bounds__(kThreads, kResident) page_score_kernel(const T
     uint32_t code[kChunks][4];
     float q_scale = 0.f;
     {
-      const T* src = q + (static_cast<int64_t>(row) * p.H_kv * G + h * G + (G < 8 ? min(at, G - 1) : at)) * D + 16 * quarter;
+      const int64_t head = (static_cast<int64_t>(row) * p.H_kv + h) * G + (G < 8 ? min(at, G - 1) : at);
+      const T* src = q + head * D + 16 * quarter;
       uint32_t largest = 0u;
 #pragma unroll
       for (int c = 0; c < kChunks / 2; ++c)
@@ -174,10 +190,10 @@ __global__ void __launch_bounds__(kThreads, kResident) page_score_kernel(const T
           for (int k = 0; k < 4; ++k) {
             const float4 x = load4(src + 64 * c + 4 * k);
             // 1.5 * 2^23 more: the rounded number is in the last bits
-            const uint32_t u0 = __float_as_uint(divide(x.x) + 12582912.f), u1 = __float_as_uint(divide(x.y) + 12582912.f);
-            const uint32_t u2 = __float_as_uint(divide(x.z) + 12582912.f), u3 = __float_as_uint(divide(x.w) + 12582912.f);
-            const uint32_t word = odd ? 0u : __byte_perm(__byte_perm(u0, u1, 0x0040), __byte_perm(u2, u3, 0x0040), 0x5410);
-            const uint32_t below = negative_bytes(word);
+            auto bits = [&](float v) { return __float_as_uint(divide(v) + 12582912.f); };
+            const uint32_t low = __byte_perm(bits(x.x), bits(x.y), 0x0040);
+            const uint32_t high = __byte_perm(bits(x.z), bits(x.w), 0x0040);
+            const uint32_t word = odd ? 0u : __byte_perm(low, high, 0x5410), below = negative_bytes(word);
             code[c][k] = word & ~below;
             code[kChunks / 2 + c][k] = word & below;
           }

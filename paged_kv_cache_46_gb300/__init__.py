@@ -253,25 +253,50 @@ def _pointers(*tensors):
     return out
 
 
+_get_device, _is_contiguous, _data_ptr = torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.data_ptr
+_here = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _marshal(stream, *tensors):
-    """Pointers of contiguous tensors on the current CUDA device (None stays None), and the
-    handle of the call's stream behind them."""
-    here = -2
-    out = []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        at = t.get_device()
-        if at != here:
-            if at < 0 or here != -2 or at != torch.cuda.current_device():
-                raise ValueError(f"tensors must be on the current CUDA device (got {t.device})")
-            here = at
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-        out.append(t.data_ptr())
-    out.append(_raw_stream(here) if stream is None and _raw_stream is not None else _stream(stream))
-    return out
+    """Pointers of contiguous tensors on the current CUDA device, and the handle of the call's
+    stream behind them."""
+    devices = set(map(_get_device, tensors))
+    at = devices.pop()
+    if devices or at < 0 or at != _here():
+        raise ValueError(f"tensors must be on the current CUDA device (got {', '.join(str(t.device) for t in tensors)})")
+    if not all(map(_is_contiguous, tensors)):
+        raise ValueError("tensors must be contiguous")
+    return (*map(_data_ptr, tensors), _raw_stream(at) if stream is None and _raw_stream is not None else _stream(stream))
+
+
+def _optional(like, t):
+    """Pointer of an optional tensor on another one's device (None stays None)."""
+    if t is None:
+        return None
+    if t.get_device() != like.get_device() or not t.is_contiguous():
+        raise ValueError("tensors must be contiguous and on the current CUDA device")
+    return t.data_ptr()
+
+
+_DTYPES = {torch.float32: TS_F32, torch.bfloat16: TS_BF16}
+
+
+def _dtype_code(dtype):
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    return code
+
+
+def _require_batch(seq_lens, indptr, block_table):
+    """_require_chunks, and the block table's row length."""
+    if seq_lens.dtype != _INT32 or block_table.dtype != _INT32 or (indptr is not None and indptr.dtype != _INT32):
+        raise TypeError("block tables, lengths and row offsets must be int32")
+    B = seq_lens.numel()
+    rows, slots = block_table.shape
+    if rows != B or (indptr is not None and indptr.numel() != B + 1):
+        raise ValueError("a batch of B sequences has B lengths, B block-table rows and B + 1 row offsets")
+    return B, slots
 
 
 def _row_step(t: torch.Tensor, rows: int, heads: int, D: int) -> int:
@@ -511,7 +536,7 @@ def ts_kv_append_chunk_rope(q, k_new, v_new, k_pool, v_pool, block_table, seq_le
     of a ragged batch of chunks by their positions, and write K and V into the pools (see
     ts_attn.h). ``inv_freq`` (float32, radians per position) has one entry per rotated pair.
     Rows may be a part of wider rows. Returns the queries, in ``q_out`` (which may be ``q``)."""
-    B = _require_chunks(seq_lens, q_indptr, block_table)
+    B, slots = _require_batch(seq_lens, q_indptr, block_table)
     q_shape, new_shape, pool_shape = q.shape, k_new.shape, k_pool.shape
     T, H_q, D = q_shape
     P, ps, H_kv, D_pool = pool_shape
@@ -521,7 +546,7 @@ def ts_kv_append_chunk_rope(q, k_new, v_new, k_pool, v_pool, block_table, seq_le
     if v_pool.shape != pool_shape or D != D_pool or new_shape != (T, H_kv, D) or v_new.shape != new_shape:
         raise ValueError("q must be [T, H_q, D], new rows [T, H_kv, D], pools [num_pages, page_size, H_kv, D]")
     for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != dtype or w.shape != (D,)):
+        if w is not None and (w.dtype != dtype or w.numel() != D):
             raise ValueError("weights must be [D] of the queries' dtype")
     rot = 0
     if inv_freq is not None:
@@ -535,18 +560,20 @@ def ts_kv_append_chunk_rope(q, k_new, v_new, k_pool, v_pool, block_table, seq_le
     if q_out is None:
         with _made_for(stream):
             q_out = torch.empty(T, H_q, D, dtype=dtype, device=q.device)
-    if q_out is not q:
+        out_step = H_q * D
+    elif q_out is not q:
         if q_out.dtype != dtype or q_out.shape != q_shape:
             raise ValueError("q_out must have the queries' shape and dtype")
         out_step = _row_step(q_out, T, H_q, D)
     at = k_pool.get_device()
     if q.get_device() != at or k_new.get_device() != at or v_new.get_device() != at or q_out.get_device() != at:
         raise ValueError("queries, new rows and pools must be on one device")
-    kp, vp, bt, lens, ptr, freq, qw, kw, on = _marshal(stream, k_pool, v_pool, block_table, seq_lens, q_indptr,
-                                                       inv_freq, q_weight, k_weight)
-    _check(lib().ts_kv_append_chunk_rope(q.data_ptr(), q_step, k_new.data_ptr(), v_new.data_ptr(), step, qw, kw, eps,
-                                         freq, rot, bool(interleaved), kp, vp, bt, block_table.shape[1], lens, ptr, T,
-                                         B, H_q, H_kv, D, ps, P, _dt(q), q_out.data_ptr(), out_step, on))
+    kp, vp, bt, lens, ptr, on = _marshal(stream, k_pool, v_pool, block_table, seq_lens, q_indptr)
+    _check(lib().ts_kv_append_chunk_rope(q.data_ptr(), q_step, k_new.data_ptr(), v_new.data_ptr(), step,
+                                         _optional(k_pool, q_weight), _optional(k_pool, k_weight), eps,
+                                         _optional(k_pool, inv_freq), rot, bool(interleaved), kp, vp, bt, slots, lens,
+                                         ptr, T, B, H_q, H_kv, D, ps, P, _dtype_code(dtype), q_out.data_ptr(), out_step,
+                                         on))
     return q_out
 
 
@@ -564,13 +591,13 @@ def ts_kv_page_bounds(k_pool, bounds, bound_scale, block_table, seq_lens, q_indp
     """Bounds of the keys of every page that holds one of the newest tokens (those of ``q_indptr``,
     ``rows`` in all), into ``bounds`` int8 [num_pages, H_kv, 2, D] and ``bound_scale`` float32
     [num_pages, H_kv] (see ts_attn.h). Other pages' bounds stay."""
-    B = _require_chunks(seq_lens, q_indptr, block_table)
+    B, slots = _require_batch(seq_lens, q_indptr, block_table)
     P, ps, H_kv, D = k_pool.shape
     if _require_bounds(bounds, bound_scale, D) != (P, H_kv):
         raise ValueError("page bounds must have the pool's pages and kv heads")
     kp, bp, sp, bt, lens, ptr, on = _marshal(stream, k_pool, bounds, bound_scale, block_table, seq_lens, q_indptr)
-    _check(lib().ts_kv_page_bounds(kp, bp, sp, bt, block_table.shape[1], lens, ptr, rows, B, H_kv, D, ps, P,
-                                   _dt(k_pool), on))
+    _check(lib().ts_kv_page_bounds(kp, bp, sp, bt, slots, lens, ptr, rows, B, H_kv, D, ps, P,
+                                   _dtype_code(k_pool.dtype), on))
 
 
 def ts_select_pages_workspace_size(B: int, q_len: int, H_kv: int, bt_stride: int) -> int:
@@ -583,7 +610,7 @@ def ts_select_pages(q, bounds, bound_scale, block_table, seq_lens, page_size: in
     kv head: q [B, H_q, D] or [B, q_len, H_q, D] -> int32 [B, (q_len,) H_kv, pages], ascending,
     -1 behind the last; the first ``first`` and last ``last`` pages are always among them
     (see ts_attn.h)."""
-    B = _require_chunks(seq_lens, None, block_table)
+    B, slots = _require_batch(seq_lens, None, block_table)
     rows, q_len, H_q, D = _query_rows(q, B)
     P, H_kv = _require_bounds(bounds, bound_scale, D)
     want = (*rows, H_kv, pages)
@@ -592,15 +619,12 @@ def ts_select_pages(q, bounds, bound_scale, block_table, seq_lens, page_size: in
             page_idx = torch.empty(want, dtype=_INT32, device=q.device)
     elif page_idx.dtype != _INT32 or page_idx.shape != want:
         raise ValueError("page_idx must be int32 [B, (q_len,) H_kv, pages]")
-    qp, bp, sp, bt, lens, ip, wp, on = _marshal(stream, q, bounds, bound_scale, block_table, seq_lens, page_idx,
-                                                workspace)
-    slots = block_table.shape[1]
+    qp, bp, sp, bt, lens, ip, on = _marshal(stream, q, bounds, bound_scale, block_table, seq_lens, page_idx)
     if workspace is None:
         with _made_for(stream):
             workspace = new_workspace(ts_select_pages_workspace_size(B, q_len, H_kv, slots), q.device)
-        wp = workspace.data_ptr()
     _check(lib().ts_select_pages(qp, bp, sp, bt, slots, lens, B, q_len, H_q, H_kv, D, page_size, P, pages, first, last,
-                                 _dt(q), ip, wp, workspace.nbytes, on))
+                                 _dtype_code(q.dtype), ip, _optional(q, workspace), workspace.nbytes, on))
     return page_idx
 
 
@@ -631,7 +655,7 @@ def ts_paged_decode_sparse_attn(q, k_pool, v_pool, block_table, seq_lens, page_i
     [B, (q_len,) H_kv, pages] of block-table slots (negative: none; see ts_select_pages). Token j of
     a sequence, at position ``seq_lens[b] - q_len + j``, attends the listed pages' tokens up to
     itself. Returns ``out`` (and ``lse``)."""
-    B = _require_chunks(seq_lens, None, block_table)
+    B, slots = _require_batch(seq_lens, None, block_table)
     rows, q_len, H_q, D = _query_rows(q, B)
     pool_shape, dtype = k_pool.shape, q.dtype
     P, ps, H_kv, D_pool = pool_shape
@@ -653,15 +677,14 @@ def ts_paged_decode_sparse_attn(q, k_pool, v_pool, block_table, seq_lens, page_i
         raise ValueError("out must have the queries' shape and dtype")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (*rows, H_q)):
         raise ValueError("lse must be float32 of the queries' rows and heads")
-    qp, kp, vp, bt, lens, ip, op, lp, wp, on = _marshal(stream, q, k_pool, v_pool, block_table, seq_lens, page_idx, out,
-                                                        lse, workspace)
+    qp, kp, vp, bt, lens, ip, op, on = _marshal(stream, q, k_pool, v_pool, block_table, seq_lens, page_idx, out)
     if workspace is None:
         with _made_for(stream):
             size = ts_paged_decode_sparse_workspace_size(B, q_len, H_q, H_kv, D, ps, pages)
             workspace = new_workspace(size, q.device)
-        wp = workspace.data_ptr()
-    _check(lib().ts_paged_decode_sparse_attn(qp, kp, vp, bt, block_table.shape[1], lens, ip, pages, B, q_len, H_q, H_kv,
-                                             D, ps, P, scale, _dt(q), op, lp, wp, workspace.nbytes, on))
+    _check(lib().ts_paged_decode_sparse_attn(qp, kp, vp, bt, slots, lens, ip, pages, B, q_len, H_q, H_kv, D, ps, P,
+                                             scale, _dtype_code(dtype), op, _optional(q, lse), _optional(q, workspace),
+                                             workspace.nbytes, on))
     return (out, lse) if return_lse else out
 
 
@@ -703,15 +726,15 @@ def ts_kv_fork(buffers, block_table, seq_lens, parents, children, fresh, page_si
     """Row ``children[i]`` of ``block_table`` and ``seq_lens`` becomes a continuation of row
     ``parents[i]``: whole pages are shared, a partly filled last page is copied to page ``fresh[i]``
     in all ``buffers`` (a list of tensors [num_pages, ...], or kv_buffers of one). See ts_attn.h."""
-    B = _require_chunks(seq_lens, None, block_table)
+    B, slots = _require_batch(seq_lens, None, block_table)
     buffers = _require_buffers(buffers, block_table)
     n = parents.numel()
     for t in (parents, children, fresh):
         if t.dtype != _INT32 or t.numel() != n:
             raise TypeError("parents, children and fresh must be int32 of one length")
     bt, lens, pp, cp, fp, on = _marshal(stream, block_table, seq_lens, parents, children, fresh)
-    _check(lib().ts_kv_fork(buffers.data, buffers.page_bytes, buffers.count, bt, block_table.shape[1], lens, B, pp, cp,
-                            fp, n, page_size, buffers.num_pages, on))
+    _check(lib().ts_kv_fork(buffers.data, buffers.page_bytes, buffers.count, bt, slots, lens, B, pp, cp, fp, n,
+                            page_size, buffers.num_pages, on))
 
 
 def ts_kv_compact_workspace_size(num_pages: int) -> int:
@@ -724,7 +747,7 @@ def ts_kv_compact(buffers, block_table, seq_lens, page_size: int, table_out=None
     tensors [num_pages, ...], or kv_buffers of one). Returns the new block table (``table_out``, which
     may be ``block_table``), each page's new id (-1: free) and the number of pages in use (int32 [1]):
     the pages from there on are free. See ts_attn.h."""
-    B = _require_chunks(seq_lens, None, block_table)
+    B, slots = _require_batch(seq_lens, None, block_table)
     buffers = _require_buffers(buffers, block_table)
     P = buffers.num_pages
     if table_out is None or page_map is None or used is None or workspace is None:
@@ -743,8 +766,8 @@ def ts_kv_compact(buffers, block_table, seq_lens, page_size: int, table_out=None
     if table_out.shape != block_table.shape or page_map.numel() != P or used.numel() != 1:
         raise ValueError("table_out must be the block table's shape, page_map [num_pages], used [1]")
     bt, to, lens, mp, up, wp, on = _marshal(stream, block_table, table_out, seq_lens, page_map, used, workspace)
-    _check(lib().ts_kv_compact(buffers.data, buffers.page_bytes, buffers.count, bt, to, block_table.shape[1], lens, B,
-                               page_size, P, mp, up, wp, workspace.nbytes, on))
+    _check(lib().ts_kv_compact(buffers.data, buffers.page_bytes, buffers.count, bt, to, slots, lens, B, page_size,
+                               P, mp, up, wp, workspace.nbytes, on))
     return table_out, page_map, used
 
 

@@ -10,6 +10,12 @@
 // row of the batch: row r is a page's first of the batch if it is its sequence's
 // first, or the first of the page. Pages are computed anew from their K rows, so
 // a call may be repeated, and a page given to another sequence needs no reset.
+//
+// HBM bounds a prompt step, latency a decode step: 15,000 rows of 8 x 128 in bf16 7.3
+// us (38 MB, 5.1 TB/s; from a cold L2 14 us under a profiler), one new row of each of
+// 64 sequences 2.6 us, of which three dependent lookups and the launch are most.
+// Extremes stay packed, two bf16 an instruction that keeps a NaN; with widened values
+// and a division each, 15,000 rows took 18 us.
 #include "ts_ragged.cuh"
 
 namespace ts {
@@ -257,7 +263,8 @@ extern "C" ts_status ts_kv_page_bounds(const void* k_pool, int8_t* bounds, float
       return fail(TS_ERR_INVALID_ARG, "%s: pool and bounds must be 16-byte aligned", who);
   if (reinterpret_cast<uintptr_t>(bound_scale) % 4 != 0)
     return fail(TS_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", who);
-  // Few rows: a warp each, so that the pages of a decode step are taken at once.
+  // Few rows: a warp each, so that the pages of a decode step are taken at once (64 rows: 2.6 us); many: a warp
+  // looks 16 over for the first of each page (15,000 rows: 7.3 us, with 8 8.9, with 32 10.6, a warp each 27).
   const int span = T <= 2048 ? 1 : 16;
   const BoundsParams p{bounds, bound_scale, block_table, seq_lens, q_indptr, bt_stride, T,
                        B,      H_kv,        num_pages,   span,     PageSize(page_size)};

@@ -18,16 +18,24 @@
 //
 // bf16 (sparse_mma_kernel): tiles of 16 tokens, two (D = 64: four) per warp in
 // flight, brought by the TMA as boxes of one kv head's 8 or 16 rows and 64 columns,
-// with the 128-byte swizzle so that ldmatrix meets every bank once. The g query heads are the rows of an m16n8k16 product, padded to 16: a 128-row
-// tcgen05 tile would be 4 / 128 full, and these products take a tenth of the
-// time that their 8 KB take to arrive. Both operands of P V are bf16: the weights
-// enter as two terms, rounded weights in the rows of the heads and what the
-// rounding left in the eight rows of padding, so that they count with 16 bits.
+// with the 128-byte swizzle so that ldmatrix meets every bank once. (Copies of a row
+// each by its lane, cp.async.bulk, issue one after another: issue slots 32 % active,
+// with boxes 20 %.) The g query heads are the rows of an m16n8k16 product, padded to
+// 16: a 128-row tcgen05 tile would be 4 / 128 full, and these products keep the
+// tensor pipe active 13 % of the time. Both operands of P V are bf16: the weights
+// enter as two terms, rounded weights in the rows of the heads and what the rounding
+// left in the eight rows of padding, so that they count with 16 bits. 64 rows of 128
+// pages of 16 (8 kv heads of 128, 4 queries each): 90 us with the join, 536 MB at 6.0
+// TB/s; the first kernel's warps end 76 to 85 us after the start. Two stages and two
+// CTAs an SM: 93.5 us when that was measured, three stages 97.3, six stages and one
+// CTA 103, two stages and three CTAs 96.9, one stage and four CTAs 101.
 // float32 (sparse_f32_kernel): on the CUDA cores, packed multiply-adds. Tiles of
 // eight tokens, two (D = 64: four) per warp in flight. For the scores a lane takes a
 // key and a quarter of its columns, so that a value of K is read once for the g
 // heads and the sums need two exchanges, not five per head; for P V it takes four
-// columns of all keys, with the weights from shared memory.
+// columns of all keys, with the weights from shared memory. 20 sequences of 57 pages
+// of 32, 4 kv heads of 128 (146 MB): one query a head 30 us, 4.9 TB/s (a row over all
+// lanes 48 us); eight queries a head 45 us, bound by multiply-adds and shared reads (85).
 #include "ts_ranges.cuh"
 #include "ts_tcgen05.cuh"
 
@@ -37,7 +45,7 @@ namespace ts {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kParts = 32;         // ranges that an item is cut into at most, and one more at its end
+constexpr int kParts = 32;  // ranges that an item is cut into at most, and one more at its end
 constexpr float kLog2eS = 1.4426950408889634f;
 constexpr float kLn2S = 0.6931471805599453f;
 
@@ -376,7 +384,8 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
       const Target<__nv_bfloat16, D> to(p, w, worker, G, head);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays NaN)
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) to.put(8 * j + 2 * quarter, both_terms(o[j][0], o[j][2]) * inv, both_terms(o[j][1], o[j][3]) * inv);
+      for (int j = 0; j < D / 8; ++j)
+        to.put(8 * j + 2 * quarter, both_terms(o[j][0], o[j][2]) * inv, both_terms(o[j][1], o[j][3]) * inv);
       if (quarter == 0) to.put_lse(sum == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + log2f(sum));
     }
   } while (w.next(p));
@@ -708,7 +717,8 @@ __global__ void __launch_bounds__(kMergeThreads) sparse_merge_kernel(const Spars
 
 // Warps of the grid: two CTAs on each SM, or as many as lists of full length keep busy.
 int sparse_warps(int64_t items, int pages) {
-  const int64_t least = (pages + kParts - 1) / kParts, most = (items * pages + least - 1) / least, full = static_cast<int64_t>(paged_decode_ctas()) * 2 * kWarps;
+  const int64_t least = (pages + kParts - 1) / kParts, most = (items * pages + least - 1) / least;
+  const int64_t full = static_cast<int64_t>(paged_decode_ctas()) * 2 * kWarps;
   const int64_t n = most < full ? most : full;
   return static_cast<int>((n < 1 ? 1 : n) + kWarps - 1) / kWarps * kWarps;
 }
@@ -747,7 +757,8 @@ ts_status make_pool_map(CUtensorMap* map, const void* pool, int64_t pool_rows, i
                               static_cast<cuuint64_t>(pool_rows)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * es, static_cast<cuuint64_t>(H_kv) * D * es};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), 1, static_cast<cuuint32_t>(rows)}, ones[3] = {1, 1, 1};
-  const CUresult r = fn(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(pool), dims, strides, box, ones,
+  const auto type = es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  const CUresult r = fn(map, type, 3, const_cast<void*>(pool), dims, strides, box, ones,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(TS_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));

@@ -5,7 +5,14 @@
 // layer) that one block table serves, and are bound by HBM: each page read once
 // and written once. A page of a buffer is cut into pieces of kPiece bytes; a CTA
 // takes a piece, found by a search over the buffers' first pieces, which are
-// kernel parameters: nothing is kept on the device between calls.
+// kernel parameters: nothing is kept on the device between calls. 48 buffers (K, V,
+// bounds and scales of 12 layers, pages of 32 KB): 64 forks 14.9 us, 97 MB at 6.6 TB/s;
+// 32 sequences' pages moved to the front 157 us, 966 MB at 6.1 TB/s. Pieces of 8 KB:
+// 172 us; of 32 KB: the same.
+//
+// Compaction: a bit for every page that some row names; a prefix sum over the words
+// of bits gives each page its rank, the number of pages U, and the lists of what
+// moves where. Nothing is sorted, and equal calls give equal pages.
 //
 // They write the block table, which the attention kernels of a stream read
 // before they wait for the kernel in front of them: so neither lets its
@@ -19,7 +26,8 @@ constexpr int kMaxBuffers = 128;  // of a launch
 constexpr int kThreads = 256;
 constexpr int kPiece = 16384;
 constexpr int kScanThreads = 1024;
-// Tables and pools that one CTA plans alone, in one launch instead of three.
+// Tables and pools that one CTA plans alone, in one launch instead of three (a pool of 70 pages: the call 10.1 us,
+// with three 15).
 constexpr int kPlanEntries = 32768, kPlanWords = 8192;
 
 struct Buffers {
@@ -371,7 +379,8 @@ extern "C" ts_status ts_kv_compact(void* const* buffers, const int64_t* page_byt
   CompactParams p{block_table, table_out, seq_lens, page_map, used, reinterpret_cast<uint32_t*>(w + ws.bits),
                   reinterpret_cast<int32_t*>(w + ws.before), reinterpret_cast<int32_t*>(w + kWorkspaceAlign),
                   reinterpret_cast<int32_t*>(w + ws.sources), reinterpret_cast<int32_t*>(w + ws.targets),
-                  bt_stride, B, page_size, num_pages, static_cast<int32_t>((static_cast<int64_t>(num_pages) + 31) / 32), 1};
+                  bt_stride, B, page_size, num_pages,
+                  static_cast<int32_t>((static_cast<int64_t>(num_pages) + 31) / 32), 1};
   const unsigned sms = static_cast<unsigned>(device_sm_count());
   const int64_t entries = static_cast<int64_t>(B) * bt_stride;
   auto step = [&](const char* name, auto kern, unsigned grid, int threads) {

@@ -48,7 +48,10 @@ __device__ __forceinline__ void make_plan(const P& p, int64_t (&before)[kThreads
 
 // Entries of each of `warps` ranges.
 __device__ __forceinline__ int64_t even_range(int64_t total, int32_t warps) {
-  if (total < (1ll << 31)) return (static_cast<uint32_t>(total) + static_cast<uint32_t>(warps) - 1u) / static_cast<uint32_t>(warps);
+  if (total < (1ll << 31)) {  // (a division of 64 bits takes several times as long)
+    const uint32_t n = static_cast<uint32_t>(warps);
+    return (static_cast<uint32_t>(total) + n - 1u) / n;
+  }
   return (total + warps - 1) / warps;
 }
 

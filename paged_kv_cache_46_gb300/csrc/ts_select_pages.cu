@@ -16,11 +16,17 @@
 // along the sum is free, so that a lane's operands are 16 bytes of a page's codes as
 // they lie in memory, and 16 bytes of a query head's; nothing goes through shared
 // memory.
+// The tiles of all rows and heads are cut evenly over one wave of warps (ts_ranges):
+// 64 sequences of 4,096 .. 32,768 tokens (8 kv heads of 128, 4 queries each, pages of
+// 16) 30 us, 158 MB at 5.3 TB/s; the fastest SMs are done after 24. The tensor pipe is
+// active 42 % of the time (65 clocks a product). With dp4a, sixteen lanes a page, 49 us.
 // page_pick_kernel: a CTA per query row and kv head. One histogram of 2048 equal
 // bins between the smallest and the largest key finds the bin of the threshold;
 // the few keys in it are ranked against each other (key, then page); a bit per
 // chosen page and a sum over the words of bits give each its place in the list.
-// Where many keys share the bin, it is cut in 2048 again first.
+// Where many keys share the bin, it is cut in 2048 again first. Latency bounds it:
+// 8,192 keys 4.9 us, of which loading them is 1.4, the histogram 1.2, the ranking 0.8
+// and the list 1.5.
 #include "ts_ranges.cuh"
 
 #include <cmath>
@@ -28,7 +34,8 @@
 namespace ts {
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32, kResident = 5;  // CTAs on an SM
+// kResident: CTAs on an SM (64 sequences: 37.1 us with 5; 4 39.5, 6 39.8; two waves of 5 42)
+constexpr int kThreads = 128, kWarps = kThreads / 32, kResident = 5;
 constexpr int kBins = 2048, kKeys = 16, kRanked = 96;  // kKeys: in a thread's registers
 
 struct SelectParams {
@@ -507,7 +514,8 @@ extern "C" ts_status ts_select_pages(const void* q, const int8_t* bounds, const 
     const ts_status st = cuda_check(e, "ts_select_pages: launch");
     if (st != TS_OK) return st;
   }
-  // Threads of a choosing CTA: as many as hold all of its keys in registers, so that small ones leave room for others.
+  // Threads of a choosing CTA: as many as hold all of its keys in registers, 16 each; more keys are read again for
+  // every step. Small CTAs leave room for others (64 sequences of 2,048 pages: 256 threads, all 512 CTAs at once).
   LaunchTrace trace("page_pick_kernel", s);
   const unsigned items = static_cast<unsigned>(rows * H_kv);
   return cuda_check(bt_stride <= 256 * kKeys ? launch_pdl(page_pick_kernel<256>, items, 256, s, p)

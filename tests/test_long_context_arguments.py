@@ -139,7 +139,8 @@ def test_binding_refuses_what_it_would_have_to_guess():
              (dict(q=torch.zeros(6, 4, 128)), ValueError), (dict(q=q.transpose(1, 2)), ValueError),
              (dict(q_weight=torch.ones(32)), ValueError), (dict(k_weight=torch.ones(64).to(bf)), ValueError),
              (dict(inv_freq=torch.ones(32).double()), TypeError), (dict(inv_freq=torch.ones(4, 8)), TypeError),
-             (dict(q_out=q[:5]), ValueError), (dict(q_out=q.to(bf)), ValueError), (dict(q_indptr=ptr.long()), TypeError),
+             (dict(q_out=q[:5]), ValueError), (dict(q_out=q.to(bf)), ValueError),
+             (dict(q_indptr=ptr.long()), TypeError),
              (dict(v_new=torch.zeros(6, 5, 64)[:, :2]), ValueError), (dict(q_indptr=i32(0, 6)), ValueError))
     bounds, scale = torch.zeros(3, 2, 2, 64, dtype=torch.int8), torch.zeros(3, 2)
     shapes = ((dict(bounds=bounds.float()), TypeError), (dict(bound_scale=scale.double()), TypeError),

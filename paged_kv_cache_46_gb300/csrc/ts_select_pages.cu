@@ -34,8 +34,9 @@
 namespace ts {
 namespace {
 
-// kResident: CTAs on an SM (64 sequences: 37.1 us with 5; 4 39.5, 6 39.8; two waves of 5 42)
-constexpr int kThreads = 128, kWarps = kThreads / 32, kResident = 5;
+// kResident: CTAs on an SM, 128 registers a thread (64 sequences 37.9 us and 131,072 tokens alone 11.9; with 5 37.1
+// and 13.1, with 6 39.8; two waves of 5 42).
+constexpr int kThreads = 128, kWarps = kThreads / 32, kResident = 4;
 constexpr int kBins = 2048, kKeys = 16, kRanked = 96;  // kKeys: in a thread's registers
 
 struct SelectParams {

@@ -14,7 +14,8 @@
 // sequences cost what they hold. Warps are workers of their own: nothing in a
 // CTA is shared but the prefix sums of that plan. A range that ends inside an
 // item leaves a float32 state, at most two per warp, which sparse_merge_kernel
-// joins; an item within one range is written at once.
+// joins; an item within one range is written at once. Few items (take_whole) go to a
+// CTA of eight warps each instead, which join their states in shared memory.
 //
 // bf16 (sparse_mma_kernel): tiles of 16 tokens, two (D = 64: four) per warp in
 // flight, brought by the TMA as boxes of one kv head's 8 or 16 rows and 64 columns,
@@ -45,6 +46,7 @@ namespace ts {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kWholeWarps = 8;  // of a CTA that takes an item whole
 constexpr int kParts = 32;  // ranges that an item is cut into at most, and one more at its end
 constexpr float kLog2eS = 1.4426950408889634f;
 constexpr float kLn2S = 0.6931471805599453f;
@@ -138,6 +140,47 @@ struct Target {
   }
 };
 
+// A warp's part of an item that its CTA takes whole.
+template <int kOf>
+__device__ __forceinline__ bool start_whole(const SparseParams& p, Walk& w, int warp) {
+  w.row = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.H_kv));
+  w.h = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.H_kv));
+  w.count = row_entries(p, w.row);
+  w.i0 = static_cast<int>(static_cast<int64_t>(w.count) * warp / kOf);
+  w.i1 = static_cast<int>(static_cast<int64_t>(w.count) * (warp + 1) / kOf);
+  w.at = w.end = w.item0 = 0;
+  return true;
+}
+
+// The warps' states of an item, [warps][G][D] with their references and sums, to its result.
+template <typename T, int D, int G, int kOf>
+__device__ __forceinline__ void join_warps(const SparseParams& p, const Walk& w, const float* states,
+                                           const float (&m)[kOf][G], const float (&sum)[kOf][G]) {
+  __syncthreads();
+  for (int e = threadIdx.x; e < G * D / 4; e += kOf * 32) {
+    const int i = e / (D / 4), d = e % (D / 4) * 4;
+    float top = m[0][i];
+#pragma unroll
+    for (int k = 1; k < kOf; ++k) top = fmaxf(top, m[k][i]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float total = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kOf; ++k) {
+      const float a = fast_exp2(m[k][i] - ref);
+      const float4 x = *reinterpret_cast<const float4*>(states + (k * G + i) * D + d);
+      total = fmaf(a, sum[k][i], total);
+      o = make_float4(fmaf(a, x.x, o.x), fmaf(a, x.y, o.y), fmaf(a, x.z, o.z), fmaf(a, x.w, o.w));
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;  // (NaN stays NaN)
+    const int64_t at = (static_cast<int64_t>(w.row) * p.H_kv + w.h) * G + i;
+    T* out = static_cast<T*>(p.out) + at * D + d;
+    store2(out, o.x * inv, o.y * inv);
+    store2(out + 2, o.z * inv, o.w * inv);
+    if (d == 0 && p.lse != nullptr) p.lse[at] = total == 0.f ? -INFINITY : (ref + log2f(total)) * kLn2S;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // bf16
 // ---------------------------------------------------------------------------
@@ -187,22 +230,25 @@ template <int D>
 struct MmaSmem {
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kOperand = 16 * D * 2, kStage = 2 * kOperand;
-  static constexpr int kBytes = kWarps * kStages * kStage;
+  static constexpr int bytes(int warps) { return warps * kStages * kStage; }
 };
 
 // The bits of the first n of eight rows.
 __device__ __forceinline__ unsigned first_rows(int n) { return n >= 8 ? 0xffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
-template <int D, int G>
-__global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
+// kWhole: a CTA per item instead of even ranges.
+template <int D, int G, bool kWhole>
+__global__ void __launch_bounds__((kWhole ? kWholeWarps : kWarps) * 32, kWhole ? 1 : 2) sparse_mma_kernel(
     const __grid_constant__ SparseParams p, const __grid_constant__ CUtensorMap kmap,
     const __grid_constant__ CUtensorMap vmap) {
   pdl_launch_dependents();
   using S = MmaSmem<D>;
   constexpr int kStages = S::kStages;
   extern __shared__ __align__(1024) unsigned char ring[];
-  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
-  __shared__ int64_t before[kThreads + 1];
+  constexpr int kOf = kWhole ? kWholeWarps : kWarps;
+  __shared__ __align__(8) uint64_t bars[kOf][kStages];
+  __shared__ int64_t before[kWhole ? 1 : kThreads + 1];
+  __shared__ float sh_m[kWhole ? kOf : 1][G], sh_sum[kWhole ? kOf : 1][G];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t worker = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   if ((smem_u32(ring) & 1023u) != 0u) {
@@ -210,15 +256,21 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(&bars[0][0] + i), 1);
+    for (int i = 0; i < kOf * kStages; ++i) mbar_init(smem_u32(&bars[0][0] + i), 1);
     fence_mbar_init();
   }
-  make_plan<kThreads>(p, before);
-  const int64_t range = range_of(p, before[kThreads] * p.H_kv);
   Walk w;
-  const bool any = w.start<kThreads>(p, before, worker * range, (worker + 1) * range, lane);
+  bool any;
+  if constexpr (kWhole) {
+    any = start_whole<kOf>(p, w, warp);
+    __syncthreads();  // the barriers are set up
+  } else {
+    make_plan<kThreads>(p, before);
+    const int64_t range = range_of(p, before[kThreads] * p.H_kv);
+    any = w.start<kThreads>(p, before, worker * range, (worker + 1) * range, lane);
+  }
   pdl_wait_primary();  // so far the lengths alone were read
-  if (blockIdx.x == 0)
+  if (!kWhole && blockIdx.x == 0)
     for (int i = threadIdx.x; i <= kThreads; i += kThreads) p.plan[i] = before[i];
   if (!any) return;
 
@@ -377,10 +429,22 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mma_kernel(
         }
       }
     }
-    if (!ok) break;
+    if (!kWhole && !ok) break;
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if (head < G) {
+    if constexpr (kWhole) {
+      __syncthreads();  // all stages have been read: the ring takes the states
+      float* states = reinterpret_cast<float*>(ring);
+      if (head < G) {
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+          store2(states + (warp * G + head) * D + 8 * j + 2 * quarter, both_terms(o[j][0], o[j][2]),
+                 both_terms(o[j][1], o[j][3]));
+        if (quarter == 0) sh_m[warp][head] = m, sh_sum[warp][head] = sum;
+      }
+      join_warps<__nv_bfloat16, D, G, kOf>(p, w, states, sh_m, sh_sum);
+      break;
+    } else if (head < G) {
       const Target<__nv_bfloat16, D> to(p, w, worker, G, head);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays NaN)
 #pragma unroll
@@ -406,20 +470,22 @@ struct F32Smem {
   static constexpr int kPart = D / 4 + 4;  // floats of a quarter of a query, and their padding
   static constexpr int kQuery = G * 4 * kPart * 4, kWeights = G * 8 * 4;
   static constexpr int kWarp = kQuery + kWeights + G * 4 + (G < 4 ? 16 - G * 4 : 0);
-  static constexpr int kBytes = kWarps * (kStages * kStage + kWarp);
+  static constexpr int bytes(int warps) { return warps * (kStages * kStage + kWarp); }
 };
 
-template <int D, int G>
-__global__ void __launch_bounds__(kThreads, 2) sparse_f32_kernel(const __grid_constant__ SparseParams p,
-                                                                 const __grid_constant__ CUtensorMap kmap,
-                                                                 const __grid_constant__ CUtensorMap vmap) {
+template <int D, int G, bool kWhole>
+__global__ void __launch_bounds__((kWhole ? kWholeWarps : kWarps) * 32, kWhole ? 1 : 2) sparse_f32_kernel(
+    const __grid_constant__ SparseParams p, const __grid_constant__ CUtensorMap kmap,
+    const __grid_constant__ CUtensorMap vmap) {
   pdl_launch_dependents();
   using S = F32Smem<D, G>;
   constexpr int kStages = S::kStages, kPart = S::kPart;
   constexpr int kMine = G >= 4 ? G / 4 : 1;  // heads whose scores a lane keeps
   extern __shared__ __align__(1024) unsigned char ring[];
-  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
-  __shared__ int64_t before[kThreads + 1];
+  constexpr int kOf = kWhole ? kWholeWarps : kWarps;
+  __shared__ __align__(8) uint64_t bars[kOf][kStages];
+  __shared__ int64_t before[kWhole ? 1 : kThreads + 1];
+  __shared__ float sh_m[kWhole ? kOf : 1][G], sh_sum[kWhole ? kOf : 1][G];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t worker = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   if ((smem_u32(ring) & 1023u) != 0u) {
@@ -427,20 +493,26 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_f32_kernel(const __grid_co
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(&bars[0][0] + i), 1);
+    for (int i = 0; i < kOf * kStages; ++i) mbar_init(smem_u32(&bars[0][0] + i), 1);
     fence_mbar_init();
   }
-  make_plan<kThreads>(p, before);
-  const int64_t range = range_of(p, before[kThreads] * p.H_kv);
   Walk w;
-  const bool any = w.start<kThreads>(p, before, worker * range, (worker + 1) * range, lane);
+  bool any;
+  if constexpr (kWhole) {
+    any = start_whole<kOf>(p, w, warp);
+    __syncthreads();  // the barriers are set up
+  } else {
+    make_plan<kThreads>(p, before);
+    const int64_t range = range_of(p, before[kThreads] * p.H_kv);
+    any = w.start<kThreads>(p, before, worker * range, (worker + 1) * range, lane);
+  }
   pdl_wait_primary();  // so far the lengths alone were read
-  if (blockIdx.x == 0)
+  if (!kWhole && blockIdx.x == 0)
     for (int i = threadIdx.x; i <= kThreads; i += kThreads) p.plan[i] = before[i];
   if (!any) return;
 
   unsigned char* stages = ring + warp * kStages * S::kStage;
-  unsigned char* own = ring + kWarps * kStages * S::kStage + warp * S::kWarp;
+  unsigned char* own = ring + kOf * kStages * S::kStage + warp * S::kWarp;
   float* qs = reinterpret_cast<float*>(own);
   float* weights = reinterpret_cast<float*>(own + S::kQuery);                 // [G][8]
   float* scales = reinterpret_cast<float*>(own + S::kQuery + S::kWeights);    // [G]
@@ -612,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_f32_kernel(const __grid_co
         }
       }
     }
-    if (!ok) break;
+    if (!kWhole && !ok) break;
     // sums over the keys, to all lanes
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
@@ -621,21 +693,39 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_f32_kernel(const __grid_co
       if (key == 0) weights[mine + i] = sum[i], scales[mine + i] = m[i];
     }
     __syncwarp();
+    if constexpr (kWhole) {
+      __syncthreads();  // all stages have been read: the ring takes the states
+      float* states = reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      const float total = weights[i], top = scales[i];
-      const Target<float, D> to(p, w, worker, G, i);
-      float x[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
-      if (D == 64) {
+      for (int i = 0; i < G; ++i) {
+        float x[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
+        if (D == 64) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] += __shfl_xor_sync(0xffffffffu, x[j], 16);
+          for (int j = 0; j < 4; ++j) x[j] += __shfl_xor_sync(0xffffffffu, x[j], 16);
+        }
+        if (vhalf == 0)
+          *reinterpret_cast<float4*>(states + (warp * G + i) * D + 4 * vlane) = make_float4(x[0], x[1], x[2], x[3]);
+        if (lane == 0) sh_m[warp][i] = scales[i], sh_sum[warp][i] = weights[i];
       }
-      const float inv = total == 0.f ? 0.f : 1.f / total;  // (NaN stays NaN)
-      if (vhalf == 0) {
-        to.put(4 * vlane, x[0] * inv, x[1] * inv);
-        to.put(4 * vlane + 2, x[2] * inv, x[3] * inv);
+      join_warps<float, D, G, kOf>(p, w, states, sh_m, sh_sum);
+      break;
+    } else {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const float total = weights[i], top = scales[i];
+        const Target<float, D> to(p, w, worker, G, i);
+        float x[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
+        if (D == 64) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] += __shfl_xor_sync(0xffffffffu, x[j], 16);
+        }
+        const float inv = total == 0.f ? 0.f : 1.f / total;  // (NaN stays NaN)
+        if (vhalf == 0) {
+          to.put(4 * vlane, x[0] * inv, x[1] * inv);
+          to.put(4 * vlane + 2, x[2] * inv, x[3] * inv);
+        }
+        if (lane == 0) to.put_lse(total == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) + log2f(total));
       }
-      if (lane == 0) to.put_lse(total == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) + log2f(total));
     }
     __syncwarp();  // before the next item's weights
   } while (w.next(p));
@@ -771,15 +861,27 @@ ts_status prepare_ring(const void* kernel) {
                     "ts_paged_decode_sparse_attn: shared memory");
 }
 
-template <typename T, int D, int G>
-ts_status launch(const SparseParams& p, cudaStream_t s) {
+// Up to two items an SM: a CTA takes an item whole and joins its warps' states itself, one launch instead of two,
+// unless the lists are so long and the items so few that most SMs would wait for them. Times of the call's kernels,
+// whole and cut evenly, 8 kv heads of 128 (items of 0.5 MB are 64 pages of 16 in bf16): 8 items of 0.5 MB 9.6 and
+// 8.3 us (the call, host-bound, 10.2 and 13.0), of 1 MB 16.4 and 9.9; 80 of 1 MB 16.9 and 17.6 (float32 with eight
+// queries a head, 1.9 MB: 66 and 45); 128 of 0.5 MB 10.4 and 16.1, float32 of 1 MB 28 and 36; 256 of 0.5 MB 26.9 and
+// 31.0; 512 of 0.5 MB 54.4 and 52.0.
+bool take_whole(int64_t items, int64_t item_bytes) {
+  const int64_t sms = paged_decode_ctas();
+  return items <= 2 * sms && (item_bytes <= (512 << 10) || (4 * items >= 3 * sms && item_bytes <= (1 << 20)));
+}
+
+template <typename T, int D, int G, bool kWhole>
+ts_status launch_first(const SparseParams& p, cudaStream_t s) {
   constexpr bool kBf16 = sizeof(T) == 2;
-  constexpr int kBytes = kBf16 ? MmaSmem<D>::kBytes : F32Smem<D, G>::kBytes;
+  constexpr int kOf = kWhole ? kWholeWarps : kWarps;
+  constexpr int kBytes = kBf16 ? MmaSmem<D>::bytes(kOf) : F32Smem<D, G>::bytes(kOf);
   const auto kern = [] {
     if constexpr (kBf16)
-      return sparse_mma_kernel<D, G>;
+      return sparse_mma_kernel<D, G, kWhole>;
     else
-      return sparse_f32_kernel<D, G>;
+      return sparse_f32_kernel<D, G, kWhole>;
   }();
   ts_status st = prepare_once(reinterpret_cast<const void*>(kern), prepare_ring<kBytes>);
   if (st != TS_OK) return st;
@@ -789,17 +891,22 @@ ts_status launch(const SparseParams& p, cudaStream_t s) {
   st = make_pool_map(&kmap, p.k_pool, pool_rows, p.H_kv, D, sizeof(T), box);
   if (st == TS_OK) st = make_pool_map(&vmap, p.v_pool, pool_rows, p.H_kv, D, sizeof(T), box);
   if (st != TS_OK) return st;
-  {
-    LaunchTrace trace(kBf16 ? "sparse_mma_kernel" : "sparse_f32_kernel", s);
-    st = cuda_check(launch_pdl(kern, static_cast<unsigned>(p.warps / kWarps), kThreads, kBytes, s, p, kmap, vmap),
-                    "ts_paged_decode_sparse_attn: launch");
-  }
+  const unsigned grid = static_cast<unsigned>(kWhole ? static_cast<int64_t>(p.rows) * p.H_kv : p.warps / kWarps);
+  LaunchTrace trace(kBf16 ? "sparse_mma_kernel" : "sparse_f32_kernel", s);
+  return cuda_check(launch_pdl(kern, grid, kOf * 32, kBytes, s, p, kmap, vmap), "ts_paged_decode_sparse_attn: launch");
+}
+
+template <typename T, int D, int G>
+ts_status launch(const SparseParams& p, cudaStream_t s) {
+  const int64_t items = static_cast<int64_t>(p.rows) * p.H_kv;
+  const int64_t item_bytes = static_cast<int64_t>(p.pages) * p.page_size * (2 * D * sizeof(T));
+  if (take_whole(items, item_bytes)) return launch_first<T, D, G, true>(p, s);
+  const ts_status st = launch_first<T, D, G, false>(p, s);
   if (st != TS_OK) return st;
   // Items that fill the device are cut into few parts each: small CTAs, so that all are resident at once (512
   // items of 4 x 128: the call 90 us, with 512 threads 93). Few items are cut into many parts, which more
   // threads share. (Joined in the first kernel by the last warp to arrive, the call takes 94 us, and one of 2
   // items 16.0 instead of 8.0: the fences and atomics in a row take longer than a launch that waits early.)
-  const int64_t items = static_cast<int64_t>(p.rows) * p.H_kv;
   constexpr int kSmall = G * D / 4 < 128 ? 128 : G * D / 4;
   LaunchTrace trace("sparse_merge_kernel", s);
   const unsigned grid = static_cast<unsigned>(items);

@@ -15,7 +15,7 @@ namespace {
 template <typename P>
 __device__ __forceinline__ int row_position(const P& p, int row) {
   const int b = row / p.q_len;
-  return p.seq_lens[b] - p.q_len + (row - b * p.q_len);
+  return max(p.seq_lens[b], 0) - p.q_len + (row - b * p.q_len);
 }
 
 // Rows of a chunk: a CTA's threads take a chunk each.

@@ -76,9 +76,10 @@ def _case(seed, lens, q_len, g, H_kv, D, pages, ps=16, dtype="bf16", order="asce
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("g,H_kv", [(4, 8), (1, 1), (2, 4), (8, 2), (8, 1), (1, 8)])
 @pytest.mark.parametrize("ps", [8, 16, 32])
-def test_shapes(dtype, D, g, H_kv, ps):
+@pytest.mark.parametrize("ctas", [None, 1])  # items whole, and cut into even ranges
+def test_shapes(dtype, D, g, H_kv, ps, ctas):
     c, q, idx = _case(51, [700, 1, 0, 16, 333, 64], 1, g, H_kv, D, 9, ps, dtype)
-    out, lse, err = _run(c, q, idx)
+    out, lse, err = _run(c, q, idx, ctas)
     assert err == 0
     _check(c, q, idx, out, lse)
 
@@ -94,9 +95,10 @@ def test_lists_of_any_length_cut_anywhere(pages, ctas):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("q_len", [2, 5, 17])
-def test_several_tokens(dtype, q_len):
+@pytest.mark.parametrize("ctas", [None, 3])
+def test_several_tokens(dtype, q_len, ctas):
     c, q, idx = _case(53, [300, 18, 3, 16 * 9 + 2], q_len, 4, 2, 64, 7, dtype=dtype, order="any")
-    out, lse, err = _run(c, q, idx)
+    out, lse, err = _run(c, q, idx, ctas)
     assert err == 0
     _check(c, q, idx, out, lse)
 
@@ -116,28 +118,30 @@ def test_all_pages_listed_is_the_whole_attention(dtype):
     assert (lse[:, 0] - l).abs().max() <= 1e-4
 
 
-def test_entries_that_are_not_pages():
+@pytest.mark.parametrize("ctas", [None, 1])
+def test_entries_that_are_not_pages(ctas):
     c, q, idx = _case(55, [200, 90, 40], 2, 2, 2, 64, 6, slots=3)
     idx[0, 0, 0] = [-1, -5, 12, -(2 ** 31), -1, 3]
     idx[0, 1, 1] = -1                                   # sees nothing
     idx[1, 0, 0] = [2 ** 31 - 1, 1000000, 6, 7, 5, -1]  # behind the position: skipped, not absent pages
     idx[2, 1, 0] = [2, 2, 1, 1, 0, -1]                  # a slot twice; three pages: three entries are taken
-    out, lse, err = _run(c, q, idx)
+    out, lse, err = _run(c, q, idx, ctas)
     assert err == 0
     _check(c, q, idx, out, lse)
     assert not out[0, 1, 2:].any() and torch.isneginf(lse[0, 1, 2:]).all()
 
 
-def test_bad_pages_are_absent_and_flagged():
+@pytest.mark.parametrize("ctas", [None, 1])
+def test_bad_pages_are_absent_and_flagged(ctas):
     c, q, idx = _case(56, [400, 300, 200], 1, 4, 2, 128, 12)
     c.table[0, 3:20] = c.P
     c.table[1, 0:9] = -1
-    out, lse, err = _run(c, q, idx)
+    out, lse, err = _run(c, q, idx, ctas)
     assert err == ts.TS_DEVERR_PAGE_RANGE
     _check(c, q, idx, out, lse)
     c, q, idx = _case(57, [400, 300, 200], 1, 4, 2, 128, 12)
     c.table = np.ascontiguousarray(c.table[:, :11])  # lists name slots past the table's row
-    out, lse, err = _run(c, q, idx)
+    out, lse, err = _run(c, q, idx, ctas)
     assert err == ts.TS_DEVERR_PAGE_RANGE
     _check(c, q, idx, out, lse)
 
@@ -145,8 +149,9 @@ def test_bad_pages_are_absent_and_flagged():
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
 def test_scales(scale):
     c, q, idx = _case(58, [500, 77], 1, 4, 2, 64, 10)
-    out, lse, _ = _run(c, q, idx, scale=scale)
-    _check(c, q, idx, out, lse, scale)
+    for ctas in (None, 1):
+        out, lse, _ = _run(c, q, idx, ctas, scale=scale)
+        _check(c, q, idx, out, lse, scale)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -156,7 +161,7 @@ def test_scores_that_are_not_finite(dtype):
     c.k_pool[c.table[0, 5], 3, 1] = float("nan")
     c.k_pool[c.table[1, 0], 0, 0, 7] = float("inf")  # scores of + and - infinity
     c.v_pool[c.table[2, 9], 2, 0, 11] = float("nan")
-    for ctas in (1, 50):
+    for ctas in (1, 50, None):
         out, lse, _ = _run(c, q, idx, ctas)
         assert torch.isnan(out[0, 0, 2:]).all() and torch.isnan(lse[0, 0, 2:]).all()
         up = (q[1, 0, :2, 7] > 0).to(DEV)
@@ -169,8 +174,9 @@ def test_scores_that_are_not_finite(dtype):
     c.k_pool = minus
     q[:, :, :, 0] = -1.0
     c.v_pool = torch.nan_to_num(c.v_pool)
-    out, lse, _ = _run(c, q, idx)  # every score is -infinity: nothing is seen
-    assert not out.any() and torch.isneginf(lse).all()
+    for ctas in (1, None):
+        out, lse, _ = _run(c, q, idx, ctas)  # every score is -infinity: nothing is seen
+        assert not out.any() and torch.isneginf(lse).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -179,7 +185,7 @@ def test_infinite_values_make_their_columns_infinite(dtype):
     want = _run(c, q, idx)[0]
     c.v_pool[c.table[0, 7], 3, 1, 9] = float("inf")
     c.v_pool[c.table[1, 30], 15, 0, 0] = -float("inf")
-    for ctas in (1, 50):
+    for ctas in (1, 50, None):
         out, lse, _ = _run(c, q, idx, ctas)
         assert (out[0, 0, 4:, 9] == float("inf")).all() and (out[1, 0, :4, 0] == -float("inf")).all()
         out[0, 0, 4:, 9], out[1, 0, :4, 0] = want[0, 0, 4:, 9], want[1, 0, :4, 0]
@@ -203,13 +209,16 @@ def test_rising_scores():
 
 def test_equal_calls_give_equal_bits_and_workspaces_may_be_shared_in_order():
     c, q, idx = _case(61, [1700, 31, 500], 1, 4, 2, 128, 60)
-    first, l_first, _ = _run(c, q, idx, single=True)
-    for _ in range(5):
-        out, lse, _ = _run(c, q, idx, single=True)
-        assert torch.equal(out, first) and torch.equal(lse, l_first)
+    for ctas in (None, 2):
+        first, l_first, _ = _run(c, q, idx, ctas, single=True)
+        for _ in range(5):
+            out, lse, _ = _run(c, q, idx, ctas, single=True)
+            assert torch.equal(out, first) and torch.equal(lse, l_first)
 
 
-def test_captured_step_with_other_lists_and_lengths():
+@pytest.mark.parametrize("ctas", ["152", "1"])
+def test_captured_step_with_other_lists_and_lengths(ctas, monkeypatch):
+    monkeypatch.setenv("TS_PAGED_DECODE_CTAS", ctas)
     c, q, idx = _case(62, [1000, 64, 300], 1, 4, 2, 64, 20)
     d = c.device()
     ws = ts.new_workspace(ts.ts_paged_decode_sparse_workspace_size(3, 1, 8, 2, 64, 16, 20))
@@ -232,11 +241,13 @@ def test_captured_step_with_other_lists_and_lengths():
         _check(c, q, idx, a["out"].view(q.shape), a["lse"].view(3, 1, 8))
 
 
-def test_pages_past_two_to_the_31_elements():
+@pytest.mark.parametrize("ctas", ["152", "1"])
+def test_pages_past_two_to_the_31_elements(ctas, monkeypatch):
     """A pool of 4.3 G elements: the listed pages lie at its end."""
     P, ps, H_kv, D = (1 << 18) + 100, 16, 8, 128
     if torch.cuda.mem_get_info()[0] < 30 << 30:
         pytest.skip("not enough free memory")
+    monkeypatch.setenv("TS_PAGED_DECODE_CTAS", ctas)
     k, v = (torch.empty(P, ps, H_kv, D, dtype=torch.bfloat16, device=DEV) for _ in "kv")
     c, q, idx = _case(63, [500, 100], 1, 4, 8, 128, 10)
     at = P - c.P

@@ -27,6 +27,7 @@
 // Where many keys share the bin, it is cut in 2048 again first. Latency bounds it:
 // 8,192 keys 4.9 us, of which loading them is 1.4, the histogram 1.2, the ranking 0.8
 // and the list 1.5.
+// page_select_kernel: both for smaller calls (whole_threads), a CTA an item, its keys in shared memory.
 #include "ts_ranges.cuh"
 
 #include <cmath>
@@ -37,6 +38,7 @@ namespace {
 // kResident: CTAs on an SM, 128 registers a thread (64 sequences 37.9 us and 131,072 tokens alone 11.9; with 5 37.1
 // and 13.1, with 6 39.8; two waves of 5 42).
 constexpr int kThreads = 128, kWarps = kThreads / 32, kResident = 4;
+constexpr int kWholePages = 2048;  // at most, of a CTA that scores and chooses
 constexpr int kBins = 2048, kKeys = 16, kRanked = 96;  // kKeys: in a thread's registers
 
 struct SelectParams {
@@ -115,141 +117,145 @@ __device__ __forceinline__ uint4 load_codes(const uint4* p) {
 // Bytes that hold four whole numbers below zero, and those that do not.
 __device__ __forceinline__ uint32_t negative_bytes(uint32_t w) { return ((w >> 7) & 0x01010101u) * 0xffu; }
 
+// Keys of slots i .. end - 1 of a query row and kv head; a whole warp calls it. The first call of a kernel waits for
+// the kernel in front of it once it has read lengths and block table.
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kThreads, kResident) page_score_kernel(const T* q, const SelectParams p) {
-  pdl_launch_dependents();
-  constexpr int kChunks = 2 * D / 64;  // of 64 codes: a quad of lanes holds 16 each
-  constexpr int kTiles = D == 128 ? 1 : 2;  // in flight
-  __shared__ int64_t before[kThreads + 1];
+__device__ __forceinline__ void score_pages(const T* q, const SelectParams& p, int row, int h, int i, int end,
+                                            uint32_t* keys, bool& waited) {
+  constexpr int kChunks = 2 * D / 64;       // of 64 codes: a quad of lanes holds 16 each
+  constexpr int kTiles = D == 128 ? 1 : 2;  // of sixteen pages, in flight
   const int lane = threadIdx.x & 31, quarter = lane & 3, at = lane >> 2;
-  const int64_t worker = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  make_plan<kThreads>(p, before);
-  const int64_t range = even_range(before[kThreads] * p.H_kv, p.warps);
-  Walk walk;
-  if (!walk.start<kThreads>(p, before, worker * range, (worker + 1) * range, lane)) {
-    pdl_wait_primary();
-    return;
-  }
-
-  bool waited = false;
-  do {
-    const int row = walk.row, h = walk.h;
-    bool past;
-    const int have = pages_of(p, row, &past);
-    const int end = min(have, 16 * walk.i1);
-    const int32_t* table = p.block_table + static_cast<int64_t>(row / p.q_len) * p.bt_stride;
-    // rows `at` and `at` + 8 of the tiles in flight: pages, looked up a step ahead of their codes and scales
-    int32_t page[kTiles][2];
-    uint4 w[kTiles][2][kChunks];
-    float s[kTiles][2];
-    bool good[kTiles][2];
-    auto look_up = [&](int first) {
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int slot = first + 16 * t + 8 * r + at;
-          page[t][r] = slot < end ? table[slot] : -1;
-        }
-    };
-    auto load = [&](int t) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        good[t][r] = static_cast<uint32_t>(page[t][r]) < static_cast<uint32_t>(p.num_pages);
-        const int64_t place = static_cast<int64_t>(good[t][r] ? page[t][r] : 0) * p.H_kv + h;
-        const uint4* src = reinterpret_cast<const uint4*>(p.bounds + place * 2 * D) + quarter;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) w[t][r][c] = load_codes<2 * D>(src + 4 * c);
-        s[t][r] = p.bound_scale[place];
-      }
-    };
-    int i = 16 * walk.i0;
-    look_up(i);
-    if (!waited) pdl_wait_primary();  // so far lengths and block table alone were read
-    waited = true;
+  const int32_t* table = p.block_table + static_cast<int64_t>(row / p.q_len) * p.bt_stride;
+  // rows `at` and `at` + 8 of the tiles in flight: pages, looked up a step ahead of their codes and scales
+  int32_t page[kTiles][2];
+  uint4 w[kTiles][2][kChunks];
+  float s[kTiles][2];
+  bool good[kTiles][2];
+  auto look_up = [&](int first) {
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
-      if (i + 16 * t < end) load(t);
-    look_up(i + 16 * kTiles);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int slot = first + 16 * t + 8 * r + at;
+        page[t][r] = slot < end ? table[slot] : -1;
+      }
+  };
+  auto load = [&](int t) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      good[t][r] = static_cast<uint32_t>(page[t][r]) < static_cast<uint32_t>(p.num_pages);
+      const int64_t place = static_cast<int64_t>(good[t][r] ? page[t][r] : 0) * p.H_kv + h;
+      const uint4* src = reinterpret_cast<const uint4*>(p.bounds + place * 2 * D) + quarter;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) w[t][r][c] = load_codes<2 * D>(src + 4 * c);
+      s[t][r] = p.bound_scale[place];
+    }
+  };
+  look_up(i);
+  if (!waited) pdl_wait_primary();  // so far lengths and block table alone were read
+  waited = true;
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+    if (i + 16 * t < end) load(t);
+  look_up(i + 16 * kTiles);
 
-    // the codes of query head `at`, as columns of B: above zero beside the upper bounds, below beside the lower
-    uint32_t code[kChunks][4];
-    float q_scale = 0.f;
-    {
-      const int64_t head = (static_cast<int64_t>(row) * p.H_kv + h) * G + (G < 8 ? min(at, G - 1) : at);
-      const T* src = q + head * D + 16 * quarter;
-      uint32_t largest = 0u;
+  // the codes of query head `at`, as columns of B: above zero beside the upper bounds, below beside the lower
+  uint32_t code[kChunks][4];
+  float q_scale = 0.f;
+  {
+    const int64_t head = (static_cast<int64_t>(row) * p.H_kv + h) * G + (G < 8 ? min(at, G - 1) : at);
+    const T* src = q + head * D + 16 * quarter;
+    uint32_t largest = 0u;
+#pragma unroll
+    for (int c = 0; c < kChunks / 2; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 x = load4(src + 64 * c + 4 * k);
+        largest = max(max(max(magnitude(x.x), magnitude(x.y)), max(magnitude(x.z), magnitude(x.w))), largest);
+      }
+    largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
+    largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
+    const bool odd = largest >= 0x7f800000u;  // (its scale stays infinite or NaN, and so do its scores)
+    q_scale = odd ? __uint_as_float(largest) : fmaxf(__uint_as_float(largest), 1e-10f) * (1.f / 127.f);
+    const float inv = reciprocal(q_scale);
+    auto quantize = [&](auto&& divide) {
 #pragma unroll
       for (int c = 0; c < kChunks / 2; ++c)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float4 x = load4(src + 64 * c + 4 * k);
-          largest = max(max(max(magnitude(x.x), magnitude(x.y)), max(magnitude(x.z), magnitude(x.w))), largest);
+          // 1.5 * 2^23 more: the rounded number is in the last bits
+          auto bits = [&](float v) { return __float_as_uint(divide(v) + 12582912.f); };
+          const uint32_t low = __byte_perm(bits(x.x), bits(x.y), 0x0040);
+          const uint32_t high = __byte_perm(bits(x.z), bits(x.w), 0x0040);
+          const uint32_t word = odd ? 0u : __byte_perm(low, high, 0x5410), below = negative_bytes(word);
+          code[c][k] = word & ~below;
+          code[kChunks / 2 + c][k] = word & below;
         }
-      largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
-      largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
-      const bool odd = largest >= 0x7f800000u;  // (its scale stays infinite or NaN, and so do its scores)
-      q_scale = odd ? __uint_as_float(largest) : fmaxf(__uint_as_float(largest), 1e-10f) * (1.f / 127.f);
-      const float inv = reciprocal(q_scale);
-      auto quantize = [&](auto&& divide) {
-#pragma unroll
-        for (int c = 0; c < kChunks / 2; ++c)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 x = load4(src + 64 * c + 4 * k);
-            // 1.5 * 2^23 more: the rounded number is in the last bits
-            auto bits = [&](float v) { return __float_as_uint(divide(v) + 12582912.f); };
-            const uint32_t low = __byte_perm(bits(x.x), bits(x.y), 0x0040);
-            const uint32_t high = __byte_perm(bits(x.z), bits(x.w), 0x0040);
-            const uint32_t word = odd ? 0u : __byte_perm(low, high, 0x5410), below = negative_bytes(word);
-            code[c][k] = word & ~below;
-            code[kChunks / 2 + c][k] = word & below;
-          }
-      };
-      if (__any_sync(0xffffffffu, all_ones(q_scale)))  // see quotient()
-        quantize([&](float x) { return __fdiv_rn(x, q_scale); });
-      else
-        quantize([&](float x) { return quotient(x, q_scale, inv); });
-    }
-    const float qs0 = __shfl_sync(0xffffffffu, q_scale, 8 * quarter);
-    const float qs1 = __shfl_sync(0xffffffffu, q_scale, 8 * quarter + 4);
-    uint32_t* keys = p.keys + (static_cast<int64_t>(row) * p.H_kv + h) * p.bt_stride;
+    };
+    if (__any_sync(0xffffffffu, all_ones(q_scale)))  // see quotient()
+      quantize([&](float x) { return __fdiv_rn(x, q_scale); });
+    else
+      quantize([&](float x) { return quotient(x, q_scale, inv); });
+  }
+  const float qs0 = __shfl_sync(0xffffffffu, q_scale, 8 * quarter);
+  const float qs1 = __shfl_sync(0xffffffffu, q_scale, 8 * quarter + 4);
 
-    for (; i < end; i += 16 * kTiles) {
+  for (; i < end; i += 16 * kTiles) {
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        const int first = i + 16 * t;
-        if (first >= end) break;
-        int32_t dot[4] = {0, 0, 0, 0};
+    for (int t = 0; t < kTiles; ++t) {
+      const int first = i + 16 * t;
+      if (first >= end) break;
+      int32_t dot[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          mma_s8(dot, w[t][0][c].x, w[t][1][c].x, w[t][0][c].y, w[t][1][c].y, code[c][0], code[c][1]);
-          mma_s8(dot, w[t][0][c].z, w[t][1][c].z, w[t][0][c].w, w[t][1][c].w, code[c][2], code[c][3]);
-        }
-        const float scale[2] = {s[t][0], s[t][1]};
-        const bool ok[2] = {good[t][0], good[t][1]};
-        if (first + 16 * kTiles < end) load(t);
-        float score[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {  // heads 2 quarter and 2 quarter + 1
-          float k0 = static_cast<float>(dot[2 * r]) * qs0 * scale[r];
-          const float k1 = static_cast<float>(dot[2 * r + 1]) * qs1 * scale[r];
-          if (G > 1) k0 = larger(k0, k1);
-          if (G < 8) k0 = 2 * quarter < G ? k0 : -INFINITY;
-          if (G > 2) k0 = larger(k0, __shfl_xor_sync(0xffffffffu, k0, 1));
-          if (G > 4) k0 = larger(k0, __shfl_xor_sync(0xffffffffu, k0, 2));
-          if (G <= 2) k0 = __shfl_sync(0xffffffffu, k0, lane & 28);
-          score[r] = k0;  // complete in the quad's first two lanes
-        }
-        const int slot = first + 8 * quarter + at;  // which store rows `at` and `at` + 8
-        if (quarter < 2 && slot < end) {
-          const bool fine = quarter ? ok[1] : ok[0];
-          keys[slot] = fine ? order_key(quarter ? score[1] : score[0]) : 0u;
-          if (!fine) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
-        }
+      for (int c = 0; c < kChunks; ++c) {
+        mma_s8(dot, w[t][0][c].x, w[t][1][c].x, w[t][0][c].y, w[t][1][c].y, code[c][0], code[c][1]);
+        mma_s8(dot, w[t][0][c].z, w[t][1][c].z, w[t][0][c].w, w[t][1][c].w, code[c][2], code[c][3]);
       }
-      look_up(i + 32 * kTiles);
+      const float scale[2] = {s[t][0], s[t][1]};
+      const bool ok[2] = {good[t][0], good[t][1]};
+      if (first + 16 * kTiles < end) load(t);
+      float score[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {  // heads 2 quarter and 2 quarter + 1
+        float k0 = static_cast<float>(dot[2 * r]) * qs0 * scale[r];
+        const float k1 = static_cast<float>(dot[2 * r + 1]) * qs1 * scale[r];
+        if (G > 1) k0 = larger(k0, k1);
+        if (G < 8) k0 = 2 * quarter < G ? k0 : -INFINITY;
+        if (G > 2) k0 = larger(k0, __shfl_xor_sync(0xffffffffu, k0, 1));
+        if (G > 4) k0 = larger(k0, __shfl_xor_sync(0xffffffffu, k0, 2));
+        if (G <= 2) k0 = __shfl_sync(0xffffffffu, k0, lane & 28);
+        score[r] = k0;  // complete in the quad's first two lanes
+      }
+      const int slot = first + 8 * quarter + at;  // which store rows `at` and `at` + 8
+      if (quarter < 2 && slot < end) {
+        const bool fine = quarter ? ok[1] : ok[0];
+        keys[slot] = fine ? order_key(quarter ? score[1] : score[0]) : 0u;
+        if (!fine) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
+      }
     }
+    look_up(i + 32 * kTiles);
+  }
+}
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kThreads, kResident) page_score_kernel(const T* q, const SelectParams p) {
+  pdl_launch_dependents();
+  __shared__ int64_t before[kThreads + 1];
+  const int64_t worker = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  make_plan<kThreads>(p, before);
+  const int64_t range = even_range(before[kThreads] * p.H_kv, p.warps);
+  Walk walk;
+  if (!walk.start<kThreads>(p, before, worker * range, (worker + 1) * range, threadIdx.x & 31)) {
+    pdl_wait_primary();
+    return;
+  }
+  bool waited = false;
+  do {
+    bool past;
+    const int have = pages_of(p, walk.row, &past);
+    uint32_t* keys = p.keys + (static_cast<int64_t>(walk.row) * p.H_kv + walk.h) * p.bt_stride;
+    score_pages<T, D, G>(q, p, walk.row, walk.h, 16 * walk.i0, min(have, 16 * walk.i1), keys, waited);
   } while (walk.next(p));
 }
 
@@ -272,22 +278,16 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t (&sums)[kWar
   return incl - v + __reduce_add_sync(0xffffffffu, mine);
 }
 
+// The list of item (row, kv head) from its `have` pages' keys; a whole CTA calls it.
 template <int kPickThreads>
-__global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectParams p) {
+__device__ __forceinline__ void pick_pages(const SelectParams& p, int64_t item, int have, const uint32_t* keys) {
   __shared__ uint32_t bins[kBins];
   __shared__ uint32_t ranked_key[kRanked], ranked_at[kRanked];
   __shared__ uint32_t words[kPickThreads];  // bits of the chosen, a stretch of pages at a time
   __shared__ uint32_t sums[kPickThreads / 32], low[kPickThreads / 32], high[kPickThreads / 32];
   __shared__ uint32_t sh_need, sh_bin, sh_count, sh_ranked;
   static_assert(kPickThreads / 32 <= 32 && kBins % kPickThreads == 0, "one warp adds up the warps' sums");
-  pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t item = blockIdx.x;  // (row, kv head)
-  const int row = static_cast<int>(item / p.H_kv);
-  bool past = false;
-  const int have = pages_of(p, row, &past);
-  pdl_wait_primary();  // so far the lengths alone were read
-  if (past && tid == 0) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
   int32_t* out = p.page_idx + item * p.pages;
   if (have <= p.pages) {
     for (int i = tid; i < p.pages; i += kPickThreads) out[i] = i < have ? i : -1;
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
   for (int i = tid; i < p.first; i += kPickThreads) out[i] = i;
   for (int i = tid; i < p.last; i += kPickThreads) out[p.pages - p.last + i] = have - p.last + i;
   if (need == 0u) return;
-  const uint32_t* keys = p.keys + item * p.bt_stride + p.first;
+  keys += p.first;
   uint32_t lo = 0xffffffffu, hi = 0u;
   const bool fits = n <= kKeys * kPickThreads;
   uint32_t kept[kKeys];
@@ -426,6 +426,38 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
   }
 }
 
+template <int kPickThreads>
+__global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectParams p) {
+  pdl_launch_dependents();
+  const int64_t item = blockIdx.x;
+  bool past = false;
+  const int have = pages_of(p, static_cast<int>(item / p.H_kv), &past);
+  pdl_wait_primary();  // so far the lengths alone were read
+  if (past && threadIdx.x == 0) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
+  pick_pages<kPickThreads>(p, item, have, p.keys + item * p.bt_stride);
+}
+
+// Scores and choice of an item by one CTA, keys in shared memory: one launch instead of two.
+template <typename T, int D, int G, int kWholeThreads>
+__global__ void __launch_bounds__(kWholeThreads, 512 / kWholeThreads)
+page_select_kernel(const T* q, const SelectParams p) {
+  __shared__ uint32_t keys[kWholePages];
+  pdl_launch_dependents();
+  constexpr int kOf = kWholeThreads / 32;
+  const int64_t item = blockIdx.x;
+  const int row = static_cast<int>(item / p.H_kv), h = static_cast<int>(item % p.H_kv), warp = threadIdx.x >> 5;
+  bool past = false, waited = false;
+  const int have = pages_of(p, row, &past);
+  if (have > p.pages && p.pages > p.first + p.last) {
+    const int tiles = (have + 15) / 16, t0 = tiles * warp / kOf, t1 = tiles * (warp + 1) / kOf;
+    if (t0 < t1) score_pages<T, D, G>(q, p, row, h, 16 * t0, min(have, 16 * t1), keys, waited);
+    __syncthreads();
+  }
+  if (!waited) pdl_wait_primary();
+  if (past && threadIdx.x == 0) set_device_error(p.err_word, TS_DEVERR_PAGE_RANGE);
+  pick_pages<kWholeThreads>(p, item, have, keys);
+}
+
 template <typename K, typename... A>
 cudaError_t launch_pdl(K kern, unsigned grid, int threads, cudaStream_t stream, A... args) {
   cudaLaunchAttribute attr[1];
@@ -438,6 +470,40 @@ cudaError_t launch_pdl(K kern, unsigned grid, int threads, cudaStream_t stream, 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// One launch, an item a CTA, where the CTAs are resident at once and have few steps: threads of a CTA, or 0. It saves the
+// second launch (the call for one sequence of up to 512 pages and 8 kv heads: 11.1 -> 8.6 us; the GPU's own time,
+// as in a captured step, is 5.8 us in two launches and 6.5 - 7.9 in one) and lets one item's choice run beside
+// another's scores. On the GPU, in two launches and in one:
+//   a CTA of 512 threads an SM: 80 items of 1000 pages 13.2, 10.6 us; of 2000 17.1, 15.6; of 4000 25.8, 28.7;
+//     152 of 2000 22.6, 17.7; but 8 of 1000 6.7, 10.4: longer tables need the items that fill half of the SMs;
+//   two of 256: 304 items of 500 pages 14.7, 11.5 us; of 1000 21.8, 17.9; 192 of 1000 17.0, 16.7; of 2000 26.3, 30.7.
+int whole_threads(int64_t items, int64_t slots) {
+  const int sms = device_sm_count();
+  if (items <= sms) return slots <= 512 || (slots <= kWholePages && 2 * items >= sms) ? 512 : 0;
+  return items <= 2 * sms && slots <= 1024 ? 256 : 0;
+}
+
+template <typename T, int D, int kWholeThreads>
+cudaError_t launch_whole(int g, unsigned grid, cudaStream_t stream, const void* q, const SelectParams& p) {
+  const T* src = static_cast<const T*>(q);
+  switch (g) {
+    case 1: return launch_pdl(page_select_kernel<T, D, 1, kWholeThreads>, grid, kWholeThreads, stream, src, p);
+    case 2: return launch_pdl(page_select_kernel<T, D, 2, kWholeThreads>, grid, kWholeThreads, stream, src, p);
+    case 4: return launch_pdl(page_select_kernel<T, D, 4, kWholeThreads>, grid, kWholeThreads, stream, src, p);
+    default: return launch_pdl(page_select_kernel<T, D, 8, kWholeThreads>, grid, kWholeThreads, stream, src, p);
+  }
+}
+
+template <int kWholeThreads>
+cudaError_t launch_whole(ts_dtype dtype, int D, int g, unsigned grid, cudaStream_t stream, const void* q,
+                         const SelectParams& p) {
+  if (dtype == TS_BF16)
+    return D == 64 ? launch_whole<__nv_bfloat16, 64, kWholeThreads>(g, grid, stream, q, p)
+                   : launch_whole<__nv_bfloat16, 128, kWholeThreads>(g, grid, stream, q, p);
+  return D == 64 ? launch_whole<float, 64, kWholeThreads>(g, grid, stream, q, p)
+                 : launch_whole<float, 128, kWholeThreads>(g, grid, stream, q, p);
 }
 
 template <typename T, int D>
@@ -506,6 +572,13 @@ extern "C" ts_status ts_select_pages(const void* q, const int8_t* bounds, const 
                        reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(workspace) + kWorkspaceAlign),
                        page_idx,  static_cast<uint32_t*>(workspace), bt_stride, static_cast<int32_t>(rows), q_len, H_kv,
                        page_size, num_pages, pages, first, last, static_cast<int32_t>(ctas) * kWarps};
+  if (const int threads = whole_threads(rows * H_kv, bt_stride)) {
+    LaunchTrace trace("page_select_kernel", s);
+    const unsigned items = static_cast<unsigned>(rows * H_kv);
+    const cudaError_t e = threads == 512 ? launch_whole<512>(dtype, D, g, items, s, q, p)
+                                         : launch_whole<256>(dtype, D, g, items, s, q, p);
+    return cuda_check(e, "ts_select_pages: launch");
+  }
   if (bt_stride > pages && pages > first + last) {  // else nothing is ranked
     LaunchTrace trace("page_score_kernel", s);
     const cudaError_t e = dtype == TS_BF16 ? (D == 64 ? launch_score<__nv_bfloat16, 64>(g, ctas, s, q, p)

@@ -111,6 +111,12 @@ def _select(c, pages, first=1, last=1, single=False, ws=None, **over):
     want = oracle.select_pages(c.q.float().numpy(), c.codes, c.scale, c.table, c.lens, c.ps, pages, first, last)
     got = out.cpu().numpy().reshape(want.shape)
     assert np.array_equal(got, want), f"{(got != want).sum()} of {got.size} entries"
+    slots = c.table.shape[1]
+    # not many short tables go through one kernel; wide ones never do
+    if slots <= 2048 and c.lens.max() <= slots * c.ps and not over:
+        a.update(block_table=i32(np.pad(c.table, ((0, 0), (0, 2049 - slots)), constant_values=-1)),
+                 workspace=ts.new_workspace(ts.ts_select_pages_workspace_size(B, q_len, c.H_kv, 2049)))
+        assert torch.equal(ts.ts_select_pages(**a), out)
     return out, ts.ts_read_device_error(ws)
 
 
@@ -127,6 +133,19 @@ def test_selection(dtype, D, g, H_kv):
 def test_selection_sizes(ps, pages, first, last):
     c = _select_case(32, [2500, 40, 1201, 2], 2, 2, 2, 64, ps)
     assert _select(c, pages, first, last)[1] == 0
+
+
+@pytest.mark.parametrize("slots,B,H_kv", [(511, 1, 1), (512, 9, 8), (513, 9, 8), (1024, 10, 4), (2047, 10, 8),
+                                          (2048, 38, 2), (2048, 39, 2), (2049, 10, 8), (1023, 20, 8), (1024, 38, 8),
+                                          (1025, 20, 8), (1024, 77, 4)])
+def test_selection_of_table_widths(slots, B, H_kv):
+    """On both sides of each rule that chooses between the kernels."""
+    rng = np.random.default_rng(slots * B)
+    lens = rng.integers(0, slots * 4 + 1, B)
+    lens[-1] = slots * 4
+    c = _select_case(42, lens, 1, 2, H_kv, 64, 4)
+    assert c.table.shape[1] == slots
+    assert _select(c, 19, 2, 3)[1] == 0
 
 
 def test_selection_of_several_tokens_across_page_ends():

@@ -472,8 +472,8 @@ cudaError_t launch_pdl(K kern, unsigned grid, int threads, cudaStream_t stream, 
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// One launch, an item a CTA, where the CTAs are resident at once and have few steps: threads of a CTA, or 0. It saves the
-// second launch (the call for one sequence of up to 512 pages and 8 kv heads: 11.1 -> 8.6 us; the GPU's own time,
+// One launch, an item a CTA, where the CTAs are resident at once and have few steps: threads of a CTA, or 0. It saves
+// the second launch (the call for one sequence of up to 512 pages and 8 kv heads: 11.1 -> 8.6 us; the GPU's own time,
 // as in a captured step, is 5.8 us in two launches and 6.5 - 7.9 in one) and lets one item's choice run beside
 // another's scores. On the GPU, in two launches and in one:
 //   a CTA of 512 threads an SM: 80 items of 1000 pages 13.2, 10.6 us; of 2000 17.1, 15.6; of 4000 25.8, 28.7;

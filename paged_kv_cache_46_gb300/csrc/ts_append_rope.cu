@@ -26,9 +26,10 @@
 // Angles: a float32 product of position and frequency is off by 2^-24 of the
 // angle, a hundredth of a turn at position 131,072. Turns are counted in 64-bit
 // fixed point instead: inv_freq / (2 pi) mod 1 as a 64-bit fraction (a float64
-// product and its remainder, once per CTA), times the position modulo 2^64, is the
-// angle in turns. Its nearest quarter turn is taken off exactly and the rest, at
-// most an eighth of a turn, is rounded to float32 once: 2^-24 of pi / 4 at most.
+// product and its remainder, once per CTA; off by two units at most), times the
+// position modulo 2^64, is the angle in turns. Its nearest quarter turn is taken off
+// exactly and the 64-bit rest, at most an eighth of a turn, is rounded to float32
+// once: by 2^-24 of itself, so that slow pairs keep their small sines.
 #include "ts_ragged.cuh"
 
 #include <cmath>
@@ -96,11 +97,12 @@ __device__ __forceinline__ unsigned long long turns_per_position(float inv_freq)
 
 // Cosine and sine of the angle at a position.
 __device__ __forceinline__ float2 turn(int pos, unsigned long long step) {
-  const uint32_t t = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * step) >> 32);
-  const uint32_t quarter = (t + 0x20000000u) >> 30;
-  const int32_t rest = static_cast<int32_t>(t - (quarter << 30));  // within an eighth of a turn
+  const unsigned long long t = static_cast<unsigned long long>(pos) * step;
+  const uint32_t quarter = static_cast<uint32_t>((t + (1ull << 61)) >> 62);
+  // within an eighth of a turn; all of its bits, since a slow pair's angle is small
+  const long long rest = static_cast<long long>(t - (static_cast<unsigned long long>(quarter) << 62));
   float s, c;
-  sincospif(static_cast<float>(rest) * 4.656612873077392578125e-10f, &s, &c);  // 2^-31: in half turns
+  sincospif(static_cast<float>(rest) * 0x1p-63f, &s, &c);  // in half turns
   const float u = quarter & 1u ? s : c, v = quarter & 1u ? c : s;
   return make_float2((quarter + 1u) & 2u ? -u : u, quarter & 2u ? -v : v);
 }

@@ -420,7 +420,7 @@ TS_API ts_status ts_paged_prefill_attn(const void* q, int64_t q_stride, const vo
  *   or (2 j, 2 j + 1) if interleaved, turns by a = position * inv_freq[j]:
  *   (y1 cos a - y2 sin a, y2 cos a + y1 sin a). Other columns stay.
  * Angles are off by position * 2^-63 turns and float32's rounding, at any position
- * and for inv_freq in 0 .. 2^40. Rows, positions and placement as
+ * and for |inv_freq| up to 2^40. Rows, positions and placement as
  * ts_kv_append_chunk; V is copied bit for bit, and so are K columns that neither
  * a weight nor a rotation touches. A decode step is n = 1 for every sequence.
  *

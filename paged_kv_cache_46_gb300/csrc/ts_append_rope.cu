@@ -87,12 +87,14 @@ struct Quad<float> {
   __device__ __forceinline__ void set(const float (&x)[4]) { w = make_float4(x[0], x[1], x[2], x[3]); }
 };
 
-// inv_freq / (2 pi) modulo 1, in units of 2^-64.
+// inv_freq / (2 pi) modulo 1, in units of 2^-64. Of its magnitude: f - floor(f) of a small negative f would lose
+// f's lower bits.
 __device__ __forceinline__ unsigned long long turns_per_position(float inv_freq) {
-  const double x = inv_freq, f = x * 0.15915494309189534;  // 1 / (2 pi), and what this product and constant leave
+  const double x = fabsf(inv_freq), f = x * 0.15915494309189534;  // 1 / (2 pi), and what this product and constant leave
   const double low = fma(x, 0.15915494309189534, -f) + x * -9.839338337591243e-18;
-  return static_cast<unsigned long long>((f - floor(f)) * 18446744073709551616.0) +
-         static_cast<unsigned long long>(static_cast<long long>(low * 18446744073709551616.0));
+  const unsigned long long turns = __double2ull_rn((f - floor(f)) * 0x1p64) +
+                                   static_cast<unsigned long long>(__double2ll_rn(low * 0x1p64));
+  return inv_freq < 0.f ? 0ull - turns : turns;
 }
 
 // Cosine and sine of the angle at a position.

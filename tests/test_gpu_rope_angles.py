@@ -69,3 +69,11 @@ def test_angles_of_slow_frequencies(D):
     none = np.zeros(D // 2)
     none[::3] = 1e-7
     _check(none, D, True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_angles_of_negative_and_of_fast_frequencies(D):
+    sign = np.where(np.arange(D // 2) % 3 == 0, 1.0, -1.0)
+    _check(-(2.0 ** -np.linspace(4, 36, D // 2)), D, False)
+    _check(sign * 500_000.0 ** (-np.arange(D // 2) / (D // 2)), D, True)
+    _check(sign * 2.0 ** np.linspace(-3, 40, D // 2), D, False)

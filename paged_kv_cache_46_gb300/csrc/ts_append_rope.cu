@@ -10,9 +10,13 @@
 //   rot / 2), or (2 j, 2 j + 1) where they are interleaved.
 // All in float32, rounded once to the stored type.
 //
-// Each value is read once and written once, and HBM bounds it: 18,900 rows of 32 +
-// 2 x 8 heads of 128 in bf16, a part of a fused projection's, 78.6 us, 464 MB at 5.9
-// TB/s, as fast as the plain append's copy. Issue slots are active 65 % of the time.
+// Each value is read once and written once, and HBM bounds rows of many heads: 18,900
+// rows of 32 + 2 x 8 heads of 128 in bf16, a part of a fused projection's, 78.8 us, 464
+// MB at 5.9 TB/s, as fast as the plain append's copy. Issue slots are active 62 % of the
+// time. Rows of few heads are bound by what each row costs its warp (the sequence's
+// search, the table's lookup, sines and two sets of factors) beside its five or six
+// steps of data: 18,900 rows of 8 + 2 x 1 heads 33.5 us (97 MB, 2.9 TB/s), 10,000
+// float32 rows of 4 + 2 x 2 heads of 64 12.9 us (41 MB, 3.2 TB/s).
 //
 // A warp takes a row, or one of `parts` shares of its heads where there are few
 // rows. D / 8 lanes hold a head, as two groups of four columns a lane, chosen so
@@ -90,7 +94,7 @@ struct Quad<float> {
 // inv_freq / (2 pi) modulo 1, in units of 2^-64. Of its magnitude: f - floor(f) of a small negative f would lose
 // f's lower bits.
 __device__ __forceinline__ unsigned long long turns_per_position(float inv_freq) {
-  const double x = fabsf(inv_freq), f = x * 0.15915494309189534;  // 1 / (2 pi), and what this product and constant leave
+  const double x = fabsf(inv_freq), f = x * 0.15915494309189534;  // 1 / (2 pi); low: what product and constant leave
   const double low = fma(x, 0.15915494309189534, -f) + x * -9.839338337591243e-18;
   const unsigned long long turns = __double2ull_rn((f - floor(f)) * 0x1p64) +
                                    static_cast<unsigned long long>(__double2ll_rn(low * 0x1p64));
@@ -324,7 +328,7 @@ ts_status launch(int D, const void* q, const void* k_new, const void* v_new, con
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // A row of few steps, or a share of one, is taken in batches that mix queries, keys and values: fewer waits one
-  // after another (float32, 4 + 2 x 2 heads of 64: 13.8 us for 10,000 rows, 26 in batches of their own). Whole rows
+  // after another (float32, 4 + 2 x 2 heads of 64: 12.9 us for 10,000 rows, 26 in batches of their own). Whole rows
   // of many steps are not: their batches' places are simpler to compute (18,900 rows of 32 / 8 heads of 128: 78.6
   // us, mixed 94).
   const bool mixed = p.parts > 1 || steps <= 3 * kBatch;

@@ -12,8 +12,9 @@
 // a call may be repeated, and a page given to another sequence needs no reset.
 //
 // HBM bounds a prompt step, latency a decode step: 15,000 rows of 8 x 128 in bf16 7.3
-// us (38 MB, 5.1 TB/s; from a cold L2 14 us under a profiler), one new row of each of
-// 64 sequences 2.6 us, of which three dependent lookups and the launch are most.
+// us (38 MB, 5.1 TB/s; from a cold L2 14 us under a profiler), in float32 9.4 us (74 MB,
+// 7.8 TB/s out of L2; cold 20 us), one new row of each of 64 sequences 2.6 us (float32
+// 2.9), of which three dependent lookups and the launch are most.
 // Extremes stay packed, two bf16 an instruction that keeps a NaN; with widened values
 // and a division each, 15,000 rows took 18 us.
 #include "ts_ragged.cuh"

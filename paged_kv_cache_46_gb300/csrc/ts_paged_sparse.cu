@@ -21,22 +21,23 @@
 // flight, brought by the TMA as boxes of one kv head's 8 or 16 rows and 64 columns,
 // with the 128-byte swizzle so that ldmatrix meets every bank once. (Copies of a row
 // each by its lane, cp.async.bulk, issue one after another: issue slots 32 % active,
-// with boxes 20 %.) The g query heads are the rows of an m16n8k16 product, padded to
+// with boxes 23 %.) The g query heads are the rows of an m16n8k16 product, padded to
 // 16: a 128-row tcgen05 tile would be 4 / 128 full, and these products keep the
-// tensor pipe active 13 % of the time. Both operands of P V are bf16: the weights
+// tensor pipe active 15 % of the time. Both operands of P V are bf16: the weights
 // enter as two terms, rounded weights in the rows of the heads and what the rounding
 // left in the eight rows of padding, so that they count with 16 bits. 64 rows of 128
-// pages of 16 (8 kv heads of 128, 4 queries each): 90 us with the join, 536 MB at 6.0
-// TB/s; the first kernel's warps end 76 to 85 us after the start. Two stages and two
-// CTAs an SM: 93.5 us when that was measured, three stages 97.3, six stages and one
-// CTA 103, two stages and three CTAs 96.9, one stage and four CTAs 101.
+// pages of 16 (8 kv heads of 128, 4 queries each): 90 to 92 us with the join, 536 MB at
+// 5.9 TB/s; nine tenths of the first kernel's warps end 76 to 85 us after the start. Two
+// stages and two CTAs an SM: 93.5 us when that was measured, three stages 97.3, six
+// stages and one CTA 103, two stages and three CTAs 96.9, one stage and four CTAs 101.
 // float32 (sparse_f32_kernel): on the CUDA cores, packed multiply-adds. Tiles of
 // eight tokens, two (D = 64: four) per warp in flight. For the scores a lane takes a
 // key and a quarter of its columns, so that a value of K is read once for the g
 // heads and the sums need two exchanges, not five per head; for P V it takes four
 // columns of all keys, with the weights from shared memory. 20 sequences of 57 pages
 // of 32, 4 kv heads of 128 (146 MB): one query a head 30 us, 4.9 TB/s (a row over all
-// lanes 48 us); eight queries a head 45 us, bound by multiply-adds and shared reads (85).
+// lanes 48 us); eight queries a head 45 us, 3.2 TB/s, bound by multiply-adds and by
+// reading each query's value from shared memory once per key of a lane (85).
 #include "ts_ranges.cuh"
 #include "ts_tcgen05.cuh"
 

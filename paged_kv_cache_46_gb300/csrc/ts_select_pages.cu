@@ -18,8 +18,10 @@
 // memory.
 // The tiles of all rows and heads are cut evenly over one wave of warps (ts_ranges):
 // 64 sequences of 4,096 .. 32,768 tokens (8 kv heads of 128, 4 queries each, pages of
-// 16) 30 us, 158 MB at 5.3 TB/s; the fastest SMs are done after 24. The tensor pipe is
-// active 42 % of the time (65 clocks a product). With dp4a, sixteen lanes a page, 49 us.
+// 16) 32 us, 158 MB at 4.9 TB/s; the fastest warps are done after 25. The tensor pipe is
+// active 41 % of the time (64 clocks a product). With dp4a, sixteen lanes a page, 49 us.
+// Every query row is scored by itself: the same with 2 and 4 tokens a sequence takes,
+// with the choice, 65 and 122 us (one token: 38).
 // page_pick_kernel: a CTA per query row and kv head. One histogram of 2048 equal
 // bins between the smallest and the largest key finds the bin of the threshold;
 // the few keys in it are ranked against each other (key, then page); a bit per
@@ -474,7 +476,7 @@ cudaError_t launch_pdl(K kern, unsigned grid, int threads, cudaStream_t stream, 
 
 // One launch, an item a CTA, where the CTAs are resident at once and have few steps: threads of a CTA, or 0. It saves
 // the second launch (the call for one sequence of up to 512 pages and 8 kv heads: 11.1 -> 8.6 us; the GPU's own time,
-// as in a captured step, is 5.8 us in two launches and 6.5 - 7.9 in one) and lets one item's choice run beside
+// as in a captured step, is 5.8 us in two launches and 6.5 - 7.8 in one) and lets one item's choice run beside
 // another's scores. On the GPU, in two launches and in one:
 //   a CTA of 512 threads an SM: 80 items of 1000 pages 13.2, 10.6 us; of 2000 17.1, 15.6; of 4000 25.8, 28.7;
 //     152 of 2000 22.6, 17.7; but 8 of 1000 6.7, 10.4: longer tables need the items that fill half of the SMs;
@@ -589,7 +591,8 @@ extern "C" ts_status ts_select_pages(const void* q, const int8_t* bounds, const 
     if (st != TS_OK) return st;
   }
   // Threads of a choosing CTA: as many as hold all of its keys in registers, 16 each; more keys are read again for
-  // every step. Small CTAs leave room for others (64 sequences of 2,048 pages: 256 threads, all 512 CTAs at once).
+  // every step. Small CTAs leave room for others (64 sequences of 2,048 pages: 256 threads, all 512 CTAs at once). The
+  // table's width decides, lengths are the device's: 64 sequences of 63 .. 250 pages 17.6 us, 28.0 in a table of 8,192.
   LaunchTrace trace("page_pick_kernel", s);
   const unsigned items = static_cast<unsigned>(rows * H_kv);
   return cuda_check(bt_stride <= 256 * kKeys ? launch_pdl(page_pick_kernel<256>, items, 256, s, p)
